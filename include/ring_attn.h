@@ -55,7 +55,9 @@ enum {
   RA_ERR_WORKSPACE = 4,   /* workspace null or smaller than required                   */
   RA_ERR_CUDA = 5,        /* a CUDA runtime or driver call failed                      */
   RA_ERR_TIMEOUT = 6,     /* a kernel gave up on a bounded internal wait               */
-  RA_ERR_DEVICE = 7       /* the current device is not compute capability 10.0         */
+  RA_ERR_DEVICE = 7,      /* the current device is not compute capability 10.0         */
+  RA_ERR_PAGES = 8        /* a cache call met a slot, length or page number out of range on the
+                             device, or too few free pages (device status word)        */
 };
 
 typedef enum { RA_BF16 = 0, RA_F32 = 1 } ra_dtype;
@@ -300,6 +302,142 @@ RA_API int ring_attn_merge(const float* o_parts, const float* lse_parts, int P, 
 /* ring_attn_merge_ex -- as ring_attn_merge with o of type out_dtype (RA_BF16 or RA_F32). */
 RA_API int ring_attn_merge_ex(const float* o_parts, const float* lse_parts, int P, void* o, float* lse, int B, int H,
                        int S, int Dh, ra_dtype out_dtype, ra_stream stream);
+
+/*
+ * ring_attn_rope -- rotary positions on Q and, in the same launch, K (no counterpart on the pages:
+ * the positions that the attention's inputs carry, applied before ring_attn_fwd or before keys are
+ * cached).  Every pair (x1, x2) of the first `rot` columns of each head is turned by the angle
+ * a = position * theta_i and scaled by `amplitude`:
+ *   y1 = amplitude (x1 cos a - x2 sin a),  y2 = amplitude (x1 sin a + x2 cos a);
+ * columns from `rot` on are copied.  inverse != 0 turns by -a: the gradient with respect to x
+ * of a call with inverse == 0, given the gradient of y.
+ *   q, q_out   [B][Hq][S][Dh] of type `dtype` (RA_BF16 or RA_F32), any strides with a contiguous last
+ *              dimension; q_strides = {in b, h, s, out b, h, s} in elements, host memory.  In place
+ *              (same address and strides) is allowed, any other overlap of q and q_out is refused.
+ *   k, k_out   the same with Hk heads, or NULL, NULL with Hk = 0.  q_out and k_out must not share
+ *              elements (interleaved rows of one buffer are fine).
+ *   steps      [rot / 2] device, theta_i / (2 pi) in units of 2^-64 turn (mod 2^64): position * step
+ *              mod 2^64 is the phase, exact at any position.
+ *   rot        rotated columns, even, 2 .. Dh; Dh even, at most 1024.
+ *   interleaved != 0: pairs (2i, 2i + 1); 0: pairs (i, i + rot / 2).
+ *   pos        device int64 positions at pos[b * pos_stride_b + s * pos_stride_s] (strides >= 0, 0 shares
+ *              a dimension), or NULL: position = offset + s.  Positions may be negative.
+ * One launch on `stream`.  Errors: RA_ERR_ARG, RA_ERR_SHAPE (rot, Dh, strides), RA_ERR_ALIGN (an
+ * address that is no multiple of its element), RA_ERR_CUDA.
+ */
+RA_API int ring_attn_rope(const void* q, void* q_out, int Hq, const long long* q_strides, const void* k, void* k_out,
+                          int Hk, const long long* k_strides, int B, int S, int Dh, const unsigned long long* steps,
+                          int rot, int interleaved, float amplitude, const long long* pos, long long pos_stride_b,
+                          long long pos_stride_s, long long offset, int inverse, ra_dtype dtype, ra_stream stream);
+
+/*
+ * ra_cache -- a paged key/value cache held in 8 bits (no counterpart on the pages; it keeps what
+ * ring_attn_fwd's keys and values were, for queries that come later).  All device memory, owned by
+ * the caller.
+ *   k, v              [layers][pages][heads][page][head_dim] e4m3 codes, 16-byte aligned.
+ *   k_scale, v_scale  [layers][pages][heads] float32, powers of two: value = code * scale.  One scale
+ *                     for each page and head (a block of `page` tokens).
+ *   table             [slots][max_pages] page numbers of each sequence, -1 behind its last page.
+ *   lens              [slots] tokens held.       refs  [pages] sequences that hold a page (0: free).
+ *   page              16, 32, 64 or 128 tokens;  head_dim  64 or 128.
+ * A new cache has table = -1, lens = 0, refs = 0, scales a power of two.  The calls below keep the
+ * three consistent.  They read slots, lengths and page numbers on the device: an entry with
+ * slot -1 is padding (skipped, its output rows left as they were); one that is out of range is
+ * skipped too and leaves RA_ERR_PAGES in the device status word (ring_attn_device_status).
+ * At most 1024 entries a call.  Calls that change a cache must not overlap on the GPU with other
+ * calls on the same cache.
+ */
+typedef struct ra_cache {
+  void *k, *v;
+  float *k_scale, *v_scale;
+  int *table, *lens, *refs;
+  int layers, pages, heads, page, head_dim, slots, max_pages;
+} ra_cache;
+
+/*
+ * ring_attn_cache_pages_workspace_size -- bytes of device workspace (256-byte aligned) that reserve
+ * and fork need for B entries, and compact with B = 0.  0 for invalid sizes.
+ */
+RA_API size_t ring_attn_cache_pages_workspace_size(int B, int pages);
+
+/*
+ * ring_attn_cache_reserve -- makes room for n_new[b] more tokens of every slots[b], once for all
+ * layers, before they are appended: pages for positions lens .. lens + n_new - 1 (the lowest free
+ * ones, in batch order), and lens += n_new.  A partly filled last page that other sequences hold too
+ * is copied first (all layers), as long as one holder is left; the copy takes its place in the
+ * batch order before the entry's new pages.  All or nothing: with too few free pages the call
+ * changes nothing and records RA_ERR_PAGES; so does, for itself alone, an entry that repeats a
+ * slot or would pass max_pages.  Two launches.
+ */
+RA_API int ring_attn_cache_reserve(const ra_cache* cache, const int* slots, const int* n_new, int B, void* workspace,
+                                   size_t workspace_bytes, ra_stream stream);
+
+/*
+ * ring_attn_cache_append -- writes the last n_new[b] tokens of every slots[b] (those that
+ * ring_attn_cache_reserve made room for) into one layer's pages.
+ *   k, v      [B][heads][T][head_dim] bf16, strides {b, h, t} in elements (multiples of 8), 16-byte
+ *             aligned; tokens t < n_new[b] <= T are read.  n_new NULL: T for every entry.
+ * Per page and head: e = least exponent with amax <= 448 * 2^e over the finite new elements, within
+ * [-117, 120], and not below the page's own if it holds older tokens (whose codes are then
+ * restated at the larger scale, rounded to nearest even); codes = e4m3(x * 2^-e), nearest even.  What
+ * is not finite is stored as NaN.  A page that another sequence holds too is not written and records
+ * RA_ERR_PAGES.  One launch.
+ */
+RA_API int ring_attn_cache_append(const ra_cache* cache, int layer, const int* slots, const int* n_new, int B, int T,
+                                  const void* k, const long long* k_strides, const void* v,
+                                  const long long* v_strides, ra_stream stream);
+
+/*
+ * ring_attn_cache_read -- one layer's keys and values as bf16 (exact): positions start[b] ..
+ * start[b] + length - 1 of slots[b] (start NULL: 0) into k, v [B][heads][length][head_dim], zero
+ * at positions that the sequence does not hold.  One launch.
+ */
+RA_API int ring_attn_cache_read(const ra_cache* cache, int layer, const int* slots, const int* start, int B,
+                                int length, void* k, void* v, ra_stream stream);
+
+/*
+ * ring_attn_cache_attend -- attention of each sequence's last n_new[b] tokens over one layer.
+ *   q         [B][Hq][T][head_dim] bf16, strides {b, h, t} in elements (multiples of 8), 16-byte
+ *             aligned; Hq a multiple of the cache's heads (query head h reads head h / (Hq / heads)).
+ *             Token t < n_new[b] is at position lens - n_new + t.  n_new NULL: T.
+ *   causal    != 0: a query sees positions up to its own; 0: all lens of them.
+ *   scale     > 0 overrides 1 / sqrt(head_dim).
+ *   o         [B][Hq][T][head_dim] bf16 or (o_dtype RA_F32) float32, and lse [B][Hq][T] float32, as
+ *             ring_attn_fwd's (float32 o and lse are one part of ring_attn_merge).  Rows t >= n_new[b]
+ *             are left as they were; a query that sees nothing has o = 0, lse = -inf.
+ *   workspace ring_attn_cache_attend_workspace_size bytes, 256-byte aligned, of this call alone while
+ *             it runs; contents on entry do not matter.
+ * exp(s - lse) is rounded to fp16 (11 bits) before it multiplies v; sums are float32.  A clear of
+ * the workspace's counters and one launch.
+ */
+RA_API size_t ring_attn_cache_attend_workspace_size(int T, int Hq, int Hkv, int Dh);
+RA_API int ring_attn_cache_attend(const ra_cache* cache, int layer, const int* slots, const int* n_new, int B, int T,
+                                  int Hq, const void* q, const long long* q_strides, float scale, int causal, void* o,
+                                  ra_dtype o_dtype, float* lse, void* workspace, size_t workspace_bytes,
+                                  ra_stream stream);
+
+/*
+ * ring_attn_cache_fork -- slots dst[b] (empty) become copies of src[b]: the same pages, one more
+ * reference each, no data moved.  Sources are read as they were before the call; of entries that name
+ * the same destination the first has it, and a destination that is not empty is left alone (both
+ * record RA_ERR_PAGES).  src = dst = -1: padding.  Two launches.
+ */
+RA_API int ring_attn_cache_fork(const ra_cache* cache, const int* src, const int* dst, int B, void* workspace,
+                                size_t workspace_bytes, ra_stream stream);
+
+/*
+ * ring_attn_cache_trim -- keeps the first keep[b] tokens of slots[b] (keep NULL: 0, the sequence is
+ * freed): pages behind them lose one reference.  keep >= lens changes nothing.  A slot that is named
+ * twice is trimmed by its first entry.  One launch.
+ */
+RA_API int ring_attn_cache_trim(const ra_cache* cache, const int* slots, const int* keep, int B, ra_stream stream);
+
+/*
+ * ring_attn_cache_compact -- moves the pages in use to the lowest numbers (the i-th one at or above
+ * their count goes to the i-th free one below it, all layers) and renumbers table and refs.  Two
+ * launches.
+ */
+RA_API int ring_attn_cache_compact(const ra_cache* cache, void* workspace, size_t workspace_bytes, ra_stream stream);
 
 /*
  * ring_attn_ring_order -- host only, no GPU needed.  Writes to blocks[0..n) the key/value

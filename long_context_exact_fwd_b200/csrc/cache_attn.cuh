@@ -1,0 +1,588 @@
+// Attention of a few new queries per sequence over the 8-bit paged cache.
+//
+//   s_j = scale * q . k_j over the keys the query sees,  lse = log sum_j exp s_j,
+//   o = sum_j exp(s_j - lse) v_j;   a query that sees no key: o = 0, lse = -inf.
+//
+// The rows of one kv head are its g query heads times the T new tokens (row = t * g + head), taken
+// 8 * NT at a time.  Products are computed transposed, S^T = K Q^T and O^T = V^T P^T, with
+// mma.sync.m16n8k16: the 16 rows are tokens (then head columns) and the 8 columns are queries, so
+// 8 query rows cost one MMA column block and each code is turned into an fp16 fragment once, in
+// registers, for all rows.  A token's 128 codes are spread so that a thread's fragments come from
+// whole 16-byte words: any order of the contracted index is right if both operands share it.
+//
+// Numbers.  Codes are exact in fp16.  A query row is scaled by a power of two to just below fp16's
+// top and keeps its bf16 values exactly down to 2^-29 of the row's largest; scores and sums are
+// fp32.  exp uses a reference that is raised when a score passes it by 2^8; P is rounded to fp16
+// (half a step: 2^-12 relative) at 2^7 times its value, so terms down to 2^-21 of the largest keep
+// full precision and smaller ones an absolute 2^-32.  P carries the value scale of its page
+// relative to the largest met so far (a power of two); the sum for lse uses unrounded terms.
+//
+// Bound: memory, 2 Dh bytes per token and head.  Work is a line of 32-token tiles over (sequence,
+// head, row block); every block takes an equal stretch of it, whatever the lengths (they are only
+// known on the device), so stretches end inside sequences: such parts go to the workspace, and the
+// block that finishes a sequence's last part joins them in order.  Each warp streams its own tiles
+// with cp.async through a private ring in shared memory, no block barrier inside a stretch.
+#pragma once
+#include "cache.cuh"
+
+namespace ra {
+namespace cache {
+
+constexpr int AT_WARPS = 8;
+constexpr int AT_THREADS = AT_WARPS * 32;
+constexpr int AT_TILE = 32;          // tokens of a warp's tile
+constexpr int AT_STAGES = 3;
+constexpr int AT_MAX_CTAS = 160;     // blocks that the workspace has room for (one per SM)
+constexpr float AT_RAISE = 8.f;      // log2: P <= 2^8, times 2^7 still an fp16 number
+constexpr float AT_P_UNIT = 128.f;
+
+struct AttendParams {
+  Pool c;                      // one layer
+  const __nv_bfloat16* q;      // [B][Hq][T][Dh], strides in elements
+  long long qb, qh, qt;
+  const int *slots, *n_new;    // n_new null: T
+  void* o;                     // [B][Hq][T][Dh] bf16 (or fp32)
+  float* lse;                  // [B][Hq][T]
+  float* part;                 // [2 * CTAs][8 NT rows][Dh + 2]
+  unsigned* tickets;           // [CTAs], 0 at launch
+  int B, T, g, n_blocks;       // row blocks per (sequence, head)
+  int page_shift, causal, o_f32;
+  float scale_log2;
+};
+
+template <int HD>
+struct AttLayout {
+  static constexpr int KV = AT_TILE * HD;              // bytes of a tile's keys
+  static constexpr int STAGE = 2 * KV;
+  static constexpr int RING = AT_STAGES * STAGE;       // per warp
+  static constexpr int SCALES = AT_WARPS * RING;       // [warp][stage][4] floats
+  static constexpr int ML = SCALES + AT_WARPS * AT_STAGES * 16;   // [warp][rows][2] floats, rows <= 32
+  static constexpr int NANS = ML + AT_WARPS * 32 * 8;  // [HD] ints
+  static constexpr int PREFIX = NANS + HD * 4;         // [B + 1] ints
+  static int bytes(int B) { return PREFIX + (B + 1) * 4; }
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool fill) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(fill ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool fill) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(fill ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ bool has_nan_code(uint32_t w) {
+  return (((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0;
+}
+
+// Byte offset of 16-byte chunk `chunk` of token `t` in a warp's tile.  Lines of 128 bytes; the
+// exclusive-or spreads the eight threads of a shared-memory phase over all banks: keys are read at
+// tokens t, t + 1 (four chunks each), values at tokens t, t + 2, t + 4, t + 6 (two chunks each).
+template <int HD>
+__device__ __forceinline__ uint32_t key_offset(int t, int chunk) {
+  return HD == 128 ? t * 128 + ((chunk ^ (t & 1)) << 4) : t * 64 + (chunk << 4);
+}
+template <int HD>
+__device__ __forceinline__ uint32_t value_offset(int t, int chunk) {
+  const int line = HD == 128 ? t : t >> 1;
+  const int at = HD == 128 ? chunk : ((t & 1) << 2) + chunk;
+  return line * 128 + ((at ^ (((t >> 1) & 3) << 1)) << 4);
+}
+
+template <int HD, int NT>
+__global__ void __launch_bounds__(AT_THREADS, 1) attend_kernel(const AttendParams p) {
+  using L = AttLayout<HD>;
+  constexpr int ROWS = 8 * NT;
+  constexpr int KS = HD / 16;          // k steps of a score, and 16-column blocks of a head
+  extern __shared__ __align__(128) uint8_t smem[];
+  const Pool& c = p.c;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gr = lane >> 2, gc = lane & 3;
+  const uint32_t ring = smem_u32(smem) + warp * L::RING;
+  uint8_t* ring_ptr = smem + warp * L::RING;
+  float* scales = reinterpret_cast<float*>(smem + L::SCALES) + warp * AT_STAGES * 4;
+  const uint32_t scales_u = smem_u32(scales);
+  float* s_ml = reinterpret_cast<float*>(smem + L::ML);
+  int* s_nan = reinterpret_cast<int*>(smem + L::NANS);
+  int* s_prefix = reinterpret_cast<int*>(smem + L::PREFIX);
+  __shared__ int s_warp[33], s_last;
+
+  // ---- the line of tiles: per_row[b] tiles for each (head, row block) of sequence b
+  int total = 0;
+  for (int b0 = 0; b0 < p.B; b0 += AT_THREADS) {
+    const int b = b0 + threadIdx.x;
+    int w = 0;
+    if (b < p.B) {
+      const int slot = p.slots[b];
+      if (slot >= 0 && slot < c.slots) {
+        const int len = c.lens[slot], n = p.n_new ? p.n_new[b] : p.T;
+        const bool ok = n >= 0 && n <= p.T && len >= 0 && len <= c.max_pages * static_cast<long long>(c.page);
+        if (!ok && blockIdx.x == 0) record_status(RA_ERR_PAGES);
+        if (ok && n > 0) w = max(1, (len + AT_TILE - 1) / AT_TILE) * c.heads * p.n_blocks;
+      } else if (slot != -1 && blockIdx.x == 0) {
+        record_status(RA_ERR_PAGES);
+      }
+    }
+    // block prefix sum
+    int s = w;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, s, d);
+      if (lane >= d) s += y;
+    }
+    if (lane == 31) s_warp[warp] = s;
+    __syncthreads();
+    int before = total, all = total;
+#pragma unroll
+    for (int i = 0; i < AT_WARPS; ++i) {
+      if (i < warp) before += s_warp[i];
+      all += s_warp[i];
+    }
+    if (b < p.B) s_prefix[b] = before + s - w;
+    total = all;
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) s_prefix[p.B] = total;
+  for (int i = threadIdx.x; i < HD; i += AT_THREADS) s_nan[i] = INT_MAX;
+  __syncthreads();
+  const int per = max((total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x), AT_WARPS);
+  const int line0 = min(static_cast<long long>(total), static_cast<long long>(blockIdx.x) * per);
+  const int line1 = min(total, line0 + per);
+
+  for (int x = line0; x < line1;) {
+    // ---- which sequence, head and row block
+    int b = 0;
+    {
+      int hi = p.B;
+      while (hi - b > 1) {
+        const int mid = (b + hi) >> 1;
+        if (s_prefix[mid] <= x) b = mid; else hi = mid;
+      }
+    }
+    const int w_b = s_prefix[b + 1] - s_prefix[b];
+    const int nt = w_b / (c.heads * p.n_blocks);
+    const int seg = (x - s_prefix[b]) / nt;
+    const int seg0 = s_prefix[b] + seg * nt;
+    const int h = seg / p.n_blocks, rb = seg - h * p.n_blocks;
+    const int t0 = x - seg0, t1 = min(nt, line1 - seg0);
+    x = seg0 + t1;
+    const int slot = p.slots[b], len = c.lens[slot], n = p.n_new ? p.n_new[b] : p.T;
+    const int row0 = rb * ROWS, rows = min(ROWS, n * p.g - row0);
+    // keys that a row sees: its token's position + 1 (causal), or all
+    auto limit_of = [&](int r) { return p.causal ? max(0, min(len, len - n + (row0 + r) / p.g + 1)) : len; };
+    const int lim_min = rows > 0 ? limit_of(0) : 0;
+    const int lim_max = rows > 0 ? limit_of(rows - 1) : 0;
+    const int* table = c.table + static_cast<long long>(slot) * c.max_pages;
+
+    // ---- this warp's tiles: t0 + warp, + AT_WARPS, ...; those behind every row's limit are empty
+    const int t_end = min(t1, (lim_max + AT_TILE - 1) / AT_TILE);
+    const int first = t0 + warp;
+    const int count = first < t_end ? (t_end - first + AT_WARPS - 1) / AT_WARPS : 0;
+    auto page_of = [&](int tile, int sub) {   // page of the tile's 16-token half `sub`, -1: none
+      const int tok = tile * AT_TILE + sub * 16;
+      if (tok >= len) return -1;
+      const int pid = table[tok >> p.page_shift];
+      if (pid < 0 || pid >= c.pages) {
+        record_status(RA_ERR_PAGES);
+        return -1;
+      }
+      return pid;
+    };
+    int next_pid0 = -1, next_pid1 = -1;
+    auto look_up = [&](int i) {
+      next_pid0 = next_pid1 = -1;
+      if (i < count) {
+        const int tile = first + i * AT_WARPS;
+        next_pid0 = page_of(tile, 0);
+        next_pid1 = p.page_shift == 4 ? page_of(tile, 1) : next_pid0;
+      }
+    };
+    auto fetch = [&](int i) {                 // tile i into its stage; the next one's pages on the way
+      if (i < count) {
+        const int tile = first + i * AT_WARPS, stage = i % AT_STAGES;
+        const int pid0 = next_pid0, pid1 = next_pid1;
+        const int in_page = (tile * AT_TILE) & (c.page - 1);
+        const long long at0 = ((static_cast<long long>(max(pid0, 0)) * c.heads + h) * c.page + in_page) * HD;
+        const long long at1 = p.page_shift == 4
+                                  ? (static_cast<long long>(max(pid1, 0)) * c.heads + h) * c.page * HD
+                                  : at0 + 16 * HD;
+        const uint32_t dst = ring + stage * L::STAGE;
+        constexpr int CHUNKS = HD / 16;       // per token
+        constexpr int PER_HALF = 16 * CHUNKS / 32;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const long long at = half ? at1 : at0;
+          const int pid = half ? pid1 : pid0;
+#pragma unroll
+          for (int j = 0; j < PER_HALF; ++j) {
+            const int ch = j * 32 + lane, t = ch / CHUNKS, k = ch % CHUNKS;
+            const int tok = half * 16 + t;
+            const bool fill = pid >= 0 && tile * AT_TILE + tok < len;
+            cp_async16(dst + key_offset<HD>(tok, k), c.k + at + ch * 16, fill);
+            cp_async16(dst + L::KV + value_offset<HD>(tok, k), c.v + at + ch * 16, fill);
+          }
+        }
+        if (lane < 4) {                       // key scales of both halves, then value scales
+          const int pid = lane & 1 ? pid1 : pid0;
+          const bool fill = pid >= 0 && (!(lane & 1) || tile * AT_TILE + 16 < len);
+          cp_async4(scales_u + (stage * 4 + lane) * 4,
+                    (lane & 2 ? c.v_scale : c.k_scale) + static_cast<long long>(max(pid, 0)) * c.heads + h, fill);
+        }
+        look_up(i + 1);
+      }
+      cp_async_commit();
+    };
+    look_up(0);
+#pragma unroll
+    for (int i = 0; i < AT_STAGES - 1; ++i) fetch(i);
+
+    // ---- queries as B fragments: column gr of block j is row j * 8 + gr, head columns gc * HD / 4 ..
+    uint32_t qf[NT][KS][2];
+    float row_scale[NT][2];                   // of the accumulator's columns 2 gc, 2 gc + 1
+    int limit[NT][2];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const int r = j * 8 + gr;
+      uint32_t w[KS * 2];
+#pragma unroll
+      for (int i = 0; i < KS * 2; ++i) w[i] = 0;
+      if (r < rows) {
+        const int tt = (row0 + r) / p.g, hq = h * p.g + (row0 + r) % p.g;
+        const uint4* src = reinterpret_cast<const uint4*>(p.q + b * p.qb + hq * p.qh + tt * p.qt + gc * (HD / 4));
+#pragma unroll
+        for (int i = 0; i < KS / 2; ++i) {
+          const uint4 v = src[i];
+          w[4 * i] = v.x;
+          w[4 * i + 1] = v.y;
+          w[4 * i + 2] = v.z;
+          w[4 * i + 3] = v.w;
+        }
+      }
+      float amax = 0.f;
+#pragma unroll
+      for (int i = 0; i < KS * 2; ++i) {
+        const float lo = fabsf(__uint_as_float(w[i] << 16)), hi = fabsf(__uint_as_float(w[i] & 0xffff0000u));
+        amax = fmaxf(amax, fmaxf(lo <= 3.4028234663852886e38f ? lo : 0.f, hi <= 3.4028234663852886e38f ? hi : 0.f));
+      }
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+      const int up = amax > 0.f ? min(max(14 - exponent_of(amax), -113), 126) : 0;   // amax -> [2^14, 2^15)
+      const float f = two_to(up);
+#pragma unroll
+      for (int s = 0; s < KS; ++s)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t v = w[2 * s + i];
+          qf[j][s][i] = pack_half2(__uint_as_float(v << 16) * f, __uint_as_float(v & 0xffff0000u) * f);
+        }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int rr = j * 8 + 2 * gc + e;
+        row_scale[j][e] = p.scale_log2 * two_to(-__shfl_sync(0xffffffffu, up, (2 * gc + e) * 4));
+        limit[j][e] = rr < rows ? limit_of(rr) : len;
+      }
+    }
+
+    float o[KS][NT][4];
+    float m_ref[NT][2], l[NT][2];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      m_ref[j][0] = m_ref[j][1] = -INFINITY;
+      l[j][0] = l[j][1] = 0.f;
+#pragma unroll
+      for (int m = 0; m < KS; ++m)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[m][j][i] = 0.f;
+    }
+    float v_ref = 0.f;                        // largest value scale so far; O is in units of it
+
+    for (int i = 0; i < count; ++i) {
+      cp_async_wait<AT_STAGES - 2>();
+      __syncwarp();
+      fetch(i + AT_STAGES - 1);
+      const int tile = first + i * AT_WARPS, stage = i % AT_STAGES, tok0 = tile * AT_TILE;
+      const uint32_t kst = ring + stage * L::STAGE, vst = kst + L::KV;
+      const float4 sc = *reinterpret_cast<const float4*>(scales + stage * 4);
+
+      // scores: S^T, rows tokens gr and gr + 8 of each half, columns queries 2 gc, 2 gc + 1
+      float s[2][NT][4];
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[half][j][e] = 0.f;
+        uint32_t ka[KS], kb[KS];              // codes of tokens gr, gr + 8: head columns gc * HD / 4 ..
+#pragma unroll
+        for (int w = 0; w < KS / 4; ++w) {
+          const uint4 a = lds128(kst + key_offset<HD>(half * 16 + gr, gc * (KS / 4) + w));
+          const uint4 z = lds128(kst + key_offset<HD>(half * 16 + gr + 8, gc * (KS / 4) + w));
+          ka[4 * w] = a.x; ka[4 * w + 1] = a.y; ka[4 * w + 2] = a.z; ka[4 * w + 3] = a.w;
+          kb[4 * w] = z.x; kb[4 * w + 1] = z.y; kb[4 * w + 2] = z.z; kb[4 * w + 3] = z.w;
+        }
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          const uint32_t a[4] = {codes_to_half2(static_cast<uint16_t>(ka[ks])), codes_to_half2(static_cast<uint16_t>(kb[ks])),
+                                 codes_to_half2(static_cast<uint16_t>(ka[ks] >> 16)),
+                                 codes_to_half2(static_cast<uint16_t>(kb[ks] >> 16))};
+#pragma unroll
+          for (int j = 0; j < NT; ++j) mma_f16(s[half][j], a, qf[j][ks][0], qf[j][ks][1]);
+        }
+      }
+
+      // log2 units, mask, and the largest of each column
+      const bool masked = tok0 + AT_TILE > lim_min;
+      bool raise = false;
+      float mx[NT][2];
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float f0 = row_scale[j][e] * sc.x, f1 = row_scale[j][e] * sc.y;
+          s[0][j][e] *= f0;
+          s[0][j][e + 2] *= f0;
+          s[1][j][e] *= f1;
+          s[1][j][e + 2] *= f1;
+          if (masked) {
+            const int left = limit[j][e] - tok0 - gr;   // tokens of the tile, from this thread's first, that are seen
+            if (left <= 0) s[0][j][e] = -INFINITY;
+            if (left <= 8) s[0][j][e + 2] = -INFINITY;
+            if (left <= 16) s[1][j][e] = -INFINITY;
+            if (left <= 24) s[1][j][e + 2] = -INFINITY;
+          }
+          mx[j][e] = fmaxf(fmaxf(s[0][j][e], s[0][j][e + 2]), fmaxf(s[1][j][e], s[1][j][e + 2]));
+          raise |= mx[j][e] > m_ref[j][e] + AT_RAISE;
+        }
+      }
+      const float v_max = fmaxf(sc.z, sc.w);
+      const bool raise_v = v_max > v_ref;               // the same in the whole warp
+      if (__any_sync(0xffffffffu, raise) || raise_v) {
+        const float fv = raise_v ? v_ref / v_max : 1.f; // powers of two: exact
+        if (raise_v) v_ref = v_max;
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float m = fmaxf(m_ref[j][e], mx[j][e]);
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+            const float a = m_ref[j][e] == m ? 1.f : ex2_approx(m_ref[j][e] - m);   // from -inf: 0
+            m_ref[j][e] = m;
+            l[j][e] *= a;
+#pragma unroll
+            for (int k = 0; k < KS; ++k) {
+              o[k][j][e] *= a * fv;
+              o[k][j][e + 2] *= a * fv;
+            }
+          }
+      }
+      const float inv_v = v_ref > 0.f ? 1.f / v_ref : 0.f;
+      const float w0 = sc.z * inv_v * AT_P_UNIT, w1 = sc.w * inv_v * AT_P_UNIT;
+
+      // P^T as B fragments
+      uint32_t pf[2][NT][2];
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        const float r0 = m_ref[j][0] == -INFINITY ? 0.f : m_ref[j][0], r1 = m_ref[j][1] == -INFINITY ? 0.f : m_ref[j][1];
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const float w = half ? w1 : w0;
+          const float a0 = ex2_approx(s[half][j][0] - r0), a1 = ex2_approx(s[half][j][1] - r1);
+          const float b0 = ex2_approx(s[half][j][2] - r0), b1 = ex2_approx(s[half][j][3] - r1);
+          l[j][0] += a0 + b0;
+          l[j][1] += a1 + b1;
+          pf[half][j][0] = transpose8(pack_half2(a0 * w, a1 * w));
+          pf[half][j][1] = transpose8(pack_half2(b0 * w, b1 * w));
+        }
+      }
+
+      // O^T += V^T P^T: thread's tokens 2 gc, 2 gc + 1, 2 gc + 8, 2 gc + 9, head columns gr * HD / 8 ..
+      const bool diagonal = masked && lim_max > lim_min;   // rows of the block see different keys here
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t v[4][HD / 32];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int t = half * 16 + 2 * gc + (k & 1) + (k & 2) * 4;
+          if (HD == 128) {
+            const uint4 a = lds128(vst + value_offset<HD>(t, gr));
+            v[k][0] = a.x; v[k][1] = a.y; v[k][2 % (HD / 32)] = a.z; v[k][3 % (HD / 32)] = a.w;
+          } else {
+            const uint2 a = lds64(vst + value_offset<HD>(t, gr >> 1) + (gr & 1) * 8);
+            v[k][0] = a.x; v[k][1] = a.y;
+          }
+          // A NaN that some rows of the block do not see must not reach them through 0 * NaN: it is
+          // taken out here and put back into the rows that see it at the end.
+          if (diagonal) {
+#pragma unroll
+            for (int w = 0; w < HD / 32; ++w)
+              if (has_nan_code(v[k][w])) {
+#pragma unroll
+                for (int y = 0; y < 4; ++y)
+                  if (((v[k][w] >> (8 * y)) & 0x7fu) == 0x7fu) {
+                    atomicMin(s_nan + gr * (HD / 8) + 4 * w + y, tok0 + t);
+                    v[k][w] &= ~(0xffu << (8 * y));
+                  }
+              }
+          }
+        }
+#pragma unroll
+        for (int w = 0; w < HD / 32; ++w) {
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const uint32_t lo = __byte_perm(v[0][w], v[1][w], y ? 0x7362 : 0x5140);
+            const uint32_t hi = __byte_perm(v[2][w], v[3][w], y ? 0x7362 : 0x5140);
+            const uint32_t a[4] = {codes_to_half2(static_cast<uint16_t>(lo)), codes_to_half2(static_cast<uint16_t>(lo >> 16)),
+                                   codes_to_half2(static_cast<uint16_t>(hi)), codes_to_half2(static_cast<uint16_t>(hi >> 16))};
+#pragma unroll
+            for (int j = 0; j < NT; ++j) mma_f16(o[2 * w + y][j], a, pf[half][j][0], pf[half][j][1]);
+          }
+        }
+      }
+    }
+
+    // ---- join the warps: each leaves m, l and O (true units) where its ring was
+    cp_async_wait<0>();
+    __syncwarp();
+    float* mine = reinterpret_cast<float*>(ring_ptr);   // [ROWS][HD]
+    const float unit = v_ref * (1.f / AT_P_UNIT);
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float z = l[j][e];
+        z += __shfl_xor_sync(0xffffffffu, z, 4);
+        z += __shfl_xor_sync(0xffffffffu, z, 8);
+        z += __shfl_xor_sync(0xffffffffu, z, 16);
+        const int r = j * 8 + 2 * gc + e;
+        if (gr == 0) {
+          s_ml[(warp * 32 + r) * 2] = m_ref[j][e];
+          s_ml[(warp * 32 + r) * 2 + 1] = z;
+        }
+#pragma unroll
+        for (int k = 0; k < KS / 2; ++k)
+          *reinterpret_cast<float4*>(mine + r * HD + gr * (HD / 8) + 4 * k) =
+              make_float4(o[2 * k][j][e] * unit, o[2 * k][j][e + 2] * unit, o[2 * k + 1][j][e] * unit,
+                          o[2 * k + 1][j][e + 2] * unit);
+      }
+    __syncthreads();
+    const bool whole = t0 == 0 && t1 == nt;
+    const int c0 = seg0 / per, c1 = (seg0 + nt - 1) / per;
+    constexpr int GROUPS = HD / 4;            // float4 groups of a row
+    float* part = p.part + static_cast<long long>(2 * blockIdx.x + (static_cast<int>(blockIdx.x) == c0 ? 1 : 0)) * ROWS * (HD + 2);
+    auto finish = [&](int r, int d, float m, float z, float4 a) {   // one row's group of 4 columns
+      const int tt = (row0 + r) / p.g, hq = h * p.g + (row0 + r) % p.g;
+      const long long row = (static_cast<long long>(b) * c.heads * p.g + hq) * p.T + tt;
+      const float inv = z > 0.f ? 1.f / z : (z == 0.f ? 0.f : z);   // NaN stays
+      a = make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
+      if (p.o_f32)
+        *reinterpret_cast<float4*>(static_cast<float*>(p.o) + row * HD + d) = a;
+      else
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + row * HD + d) =
+            make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
+      if (d == 0) p.lse[row] = z == 0.f ? -INFINITY : (m + log2f(z)) * 0.69314718055994531f;
+    };
+    for (int i = threadIdx.x; i < ROWS * GROUPS; i += AT_THREADS) {
+      const int r = i / GROUPS, d = (i % GROUPS) * 4;
+      if (r >= rows) continue;
+      float m = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < AT_WARPS; ++w) m = fmaxf(m, s_ml[(w * 32 + r) * 2]);
+      float z = 0.f;
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < AT_WARPS; ++w) {
+        const float mw = s_ml[(w * 32 + r) * 2], zw = s_ml[(w * 32 + r) * 2 + 1];
+        if (zw == 0.f) continue;              // saw nothing
+        const float f = mw == m ? 1.f : ex2_approx(mw - m);
+        const float4 y = *reinterpret_cast<const float4*>(smem + w * L::RING + (r * HD + d) * 4);
+        z += zw * f;
+        a = make_float4(fmaf(y.x, f, a.x), fmaf(y.y, f, a.y), fmaf(y.z, f, a.z), fmaf(y.w, f, a.w));
+      }
+      if (lim_max > lim_min) {
+        const int lim = limit_of(r);
+        const float nan = __uint_as_float(0x7fffffffu);
+        if (s_nan[d] < lim) a.x = nan;
+        if (s_nan[d + 1] < lim) a.y = nan;
+        if (s_nan[d + 2] < lim) a.z = nan;
+        if (s_nan[d + 3] < lim) a.w = nan;
+      }
+      if (whole) {
+        finish(r, d, m, z, a);
+      } else {
+        float* row = part + r * (HD + 2);
+        *reinterpret_cast<float2*>(row + d) = make_float2(a.x, a.y);
+        *reinterpret_cast<float2*>(row + d + 2) = make_float2(a.z, a.w);
+        if (d == 0) *reinterpret_cast<float2*>(row + HD) = make_float2(m, z);
+      }
+    }
+    if (!whole) {
+      // the block that brings a segment's last part joins all of them, in order
+      __threadfence();
+      __syncthreads();
+      if (threadIdx.x == 0) s_last = atomicAdd(p.tickets + c0, 1u) == static_cast<unsigned>(c1 - c0);
+      __syncthreads();
+      if (s_last) {
+        __threadfence();
+        for (int i = threadIdx.x; i < ROWS * GROUPS; i += AT_THREADS) {
+          const int r = i / GROUPS, d = (i % GROUPS) * 4;
+          if (r >= rows) continue;
+          const long long step = 2ll * ROWS * (HD + 2);
+          const float* row = p.part + (2ll * c0 * ROWS + r) * (HD + 2);   // part of block c: + (c - c0) * step
+          const float* row_c0 = row + ROWS * (HD + 2);                    // block c0 left its end part
+          float m = -INFINITY;
+          for (int k = c0; k <= c1; ++k) m = fmaxf(m, __ldcg((k == c0 ? row_c0 : row + (k - c0) * step) + HD));
+          float z = 0.f;
+          float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+          for (int k = c0; k <= c1; ++k) {
+            const float* y = k == c0 ? row_c0 : row + (k - c0) * step;
+            const float2 ml = __ldcg(reinterpret_cast<const float2*>(y + HD));
+            const float2 u = __ldcg(reinterpret_cast<const float2*>(y + d));
+            const float2 v = __ldcg(reinterpret_cast<const float2*>(y + d + 2));
+            const float f = ml.y == 0.f ? 0.f : (ml.x == m ? 1.f : ex2_approx(ml.x - m));
+            if (ml.y == 0.f) continue;        // saw nothing
+            z += ml.y * f;
+            a = make_float4(fmaf(u.x, f, a.x), fmaf(u.y, f, a.y), fmaf(v.x, f, a.z), fmaf(v.y, f, a.w));
+          }
+          finish(r, d, m, z, a);
+        }
+      }
+    }
+    __syncthreads();                          // rings and s_nan are free again
+    if (lim_max > lim_min) {
+      for (int i = threadIdx.x; i < HD; i += AT_THREADS) s_nan[i] = INT_MAX;
+      __syncthreads();
+    }
+  }
+}
+
+}  // namespace cache
+}  // namespace ra

@@ -1,0 +1,287 @@
+// Host side of the 8-bit key/value cache: argument checks, workspaces and launches.  Included once,
+// at the end of ring_attn.cu (it uses that file's device info, status and alignment helpers).
+#pragma once
+#include "cache.cuh"
+#include "cache_attn.cuh"
+#include "cache_io.cuh"
+#include "cache_pages.cuh"
+
+namespace {
+
+namespace rc = ra::cache;
+
+// Checks the description of a cache and fills `p` with all layers' view; layer >= 0 picks one.
+int cache_pool(const ra_cache* c, int layer, rc::Pool* p) {
+  if (!c || !c->k || !c->v || !c->k_scale || !c->v_scale || !c->table || !c->lens || !c->refs) return RA_ERR_ARG;
+  if (c->layers <= 0 || c->pages <= 0 || c->heads <= 0 || c->slots <= 0 || c->max_pages <= 0) return RA_ERR_ARG;
+  if (layer >= c->layers) return RA_ERR_ARG;
+  if (c->page != 16 && c->page != 32 && c->page != 64 && c->page != 128) return RA_ERR_SHAPE;
+  if (c->head_dim != 64 && c->head_dim != 128) return RA_ERR_SHAPE;
+  // positions fit in int (with a tile to spare), page numbers and per-layer head indexes too
+  if (static_cast<long long>(c->max_pages) * c->page > INT_MAX - 1024) return RA_ERR_SHAPE;
+  if (c->pages > (1 << 28) || c->heads > 32767 || c->layers > (1 << 20)) return RA_ERR_SHAPE;
+  if (static_cast<double>(c->layers) * c->pages * c->heads * c->page * c->head_dim > 9.0e18 / 4) return RA_ERR_SHAPE;
+  if (!aligned16(c->k) || !aligned16(c->v)) return RA_ERR_ALIGN;
+  for (const void* q : {static_cast<const void*>(c->k_scale), static_cast<const void*>(c->v_scale),
+                        static_cast<const void*>(c->table), static_cast<const void*>(c->lens),
+                        static_cast<const void*>(c->refs)})
+    if (reinterpret_cast<uintptr_t>(q) % 4) return RA_ERR_ALIGN;
+  const long long rows = layer > 0 ? static_cast<long long>(layer) * c->pages * c->heads : 0;
+  const long long codes = rows * c->page * c->head_dim;
+  *p = {static_cast<uint8_t*>(c->k) + codes, static_cast<uint8_t*>(c->v) + codes, c->k_scale + rows, c->v_scale + rows,
+        c->table, c->lens, c->refs, c->layers, c->pages, c->heads, c->page, c->head_dim, c->slots, c->max_pages};
+  return RA_OK;
+}
+
+int cache_batch(const int* slots, int B) {
+  if (!slots || B <= 0) return RA_ERR_ARG;
+  if (B > rc::MAX_BATCH) return RA_ERR_SHAPE;
+  return reinterpret_cast<uintptr_t>(slots) % 4 ? RA_ERR_ALIGN : RA_OK;
+}
+
+// Rows of a [B][heads][T][Dh] bf16 tensor that kernels read 16 bytes at a time.
+int cache_rows(const void* x, const long long* st, int B, int H, int T) {
+  if (!x || !st) return RA_ERR_ARG;
+  const int n[3] = {B, H, T};
+  for (int i = 0; i < 3; ++i) {
+    if (n[i] == 1) continue;
+    if (st[i] < 0 || st[i] > (1ll << 59) / n[i]) return RA_ERR_SHAPE;
+    if (st[i] % 8) return RA_ERR_ALIGN;
+  }
+  return aligned16(x) ? RA_OK : RA_ERR_ALIGN;
+}
+
+size_t pages_workspace(long long words) { return align256(sizeof(rc::Plan)) + align256(static_cast<size_t>(words) * 4); }
+
+int pages_check_ws(const void* workspace, size_t have, size_t need) {
+  return !workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) || have < need ? RA_ERR_WORKSPACE : RA_OK;
+}
+
+int copy_grid(const rc::Pool& c, long long pairs, int sm_count) {
+  const long long chunks = (static_cast<long long>(c.heads) * c.page * c.Dh + rc::COPY_BYTES - 1) / rc::COPY_BYTES;
+  const long long units = pairs * c.layers * 2 * chunks;
+  const long long most = 8ll * sm_count;   // resident at 256 threads
+  return static_cast<int>(units < 1 ? 1 : (units < most ? units : most));
+}
+
+// Rows per block of the attention kernel: as few blocks as 8 * NT rows allow, the narrowest that do.
+constexpr int AT_MAX_NT = 3;
+int attend_nt(long long rows) {
+  const long long blocks = (rows + 8 * AT_MAX_NT - 1) / (8 * AT_MAX_NT);
+  return static_cast<int>((rows + 8 * blocks - 1) / (8 * blocks));
+}
+
+template <int HD, int NT>
+int attend_launch(const rc::AttendParams& p, DevInfo* di, int grid, cudaStream_t stream) {
+  const int smem = rc::AttLayout<HD>::bytes(p.B);
+  std::atomic<bool>& set = di->attend_attr[HD == 128 ? 0 : 1][NT - 1];
+  if (!set) {
+    const cudaError_t e = cudaFuncSetAttribute(rc::attend_kernel<HD, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               rc::AttLayout<HD>::bytes(rc::MAX_BATCH));
+    if (e != cudaSuccess) return cuda_fail(static_cast<int>(e), "cudaFuncSetAttribute(cache attention smem)");
+    set = true;
+  }
+  rc::attend_kernel<HD, NT><<<grid, rc::AT_THREADS, smem, stream>>>(p);
+  return launch_status();
+}
+
+template <int HD>
+int attend_nt_launch(int nt, const rc::AttendParams& p, DevInfo* di, int grid, cudaStream_t stream) {
+  if (nt == 1) return attend_launch<HD, 1>(p, di, grid, stream);
+  if (nt == 2) return attend_launch<HD, 2>(p, di, grid, stream);
+  return attend_launch<HD, 3>(p, di, grid, stream);
+}
+
+size_t attend_part_bytes(int nt, int Dh) {
+  return align256(static_cast<size_t>(2 * rc::AT_MAX_CTAS) * 8 * nt * (Dh + 2) * sizeof(float));
+}
+
+}  // namespace
+
+extern "C" {
+
+int ring_attn_cache_append(const ra_cache* cache, int layer, const int* slots, const int* n_new, int B, int T,
+                           const void* k, const long long* k_strides, const void* v, const long long* v_strides,
+                           ra_stream stream) {
+  rc::AppendParams p{};
+  if (layer < 0 || T <= 0) return RA_ERR_ARG;
+  int st = cache_pool(cache, layer, &p.c);
+  if (st != RA_OK) return st;
+  if ((st = cache_batch(slots, B)) != RA_OK) return st;
+  if ((st = cache_rows(k, k_strides, B, p.c.heads, T)) != RA_OK) return st;
+  if ((st = cache_rows(v, v_strides, B, p.c.heads, T)) != RA_OK) return st;
+  if (reinterpret_cast<uintptr_t>(n_new) % 4) return RA_ERR_ALIGN;
+  if (T > INT_MAX - 1024) return RA_ERR_SHAPE;
+  DevInfo* di = dev_info(&st);
+  if (!di) return st;
+  p.k = static_cast<const __nv_bfloat16*>(k);
+  p.v = static_cast<const __nv_bfloat16*>(v);
+  p.kb = k_strides[0], p.kh = k_strides[1], p.kt = k_strides[2];
+  p.vb = v_strides[0], p.vh = v_strides[1], p.vt = v_strides[2];
+  p.slots = slots;
+  p.n_new = n_new;
+  p.T = T;
+  const long long touched = (T + static_cast<long long>(p.c.page) - 2) / p.c.page + 1;   // pages T tokens can lie in
+  const long long most = touched < p.c.max_pages ? touched : p.c.max_pages;
+  const dim3 grid(static_cast<unsigned>(most), p.c.heads, 2 * B);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int units = p.c.page * p.c.Dh / rc::UNIT;
+  if (units <= rc::IO_THREADS)
+    rc::append_kernel<1><<<grid, rc::IO_THREADS, 0, s>>>(p);
+  else if (units <= 2 * rc::IO_THREADS)
+    rc::append_kernel<2><<<grid, rc::IO_THREADS, 0, s>>>(p);
+  else
+    rc::append_kernel<4><<<grid, rc::IO_THREADS, 0, s>>>(p);
+  return launch_status();
+}
+
+int ring_attn_cache_read(const ra_cache* cache, int layer, const int* slots, const int* start, int B, int length,
+                         void* k, void* v, ra_stream stream) {
+  rc::ReadParams p{};
+  if (layer < 0 || length <= 0 || !k || !v || k == v) return RA_ERR_ARG;
+  int st = cache_pool(cache, layer, &p.c);
+  if (st != RA_OK) return st;
+  if ((st = cache_batch(slots, B)) != RA_OK) return st;
+  if (!aligned16(k) || !aligned16(v) || reinterpret_cast<uintptr_t>(start) % 4) return RA_ERR_ALIGN;
+  DevInfo* di = dev_info(&st);
+  if (!di) return st;
+  p.slots = slots;
+  p.start = start;
+  p.k = static_cast<__nv_bfloat16*>(k);
+  p.v = static_cast<__nv_bfloat16*>(v);
+  p.length = length;
+  const long long blocks = (static_cast<long long>(length) * (p.c.Dh / rc::UNIT) + rc::IO_THREADS - 1) / rc::IO_THREADS;
+  const dim3 grid(static_cast<unsigned>(blocks), p.c.heads, 2 * B);
+  rc::read_kernel<<<grid, rc::IO_THREADS, 0, static_cast<cudaStream_t>(stream)>>>(p);
+  return launch_status();
+}
+
+size_t ring_attn_cache_attend_workspace_size(int T, int Hq, int Hkv, int Dh) {
+  if (T <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || (Dh != 64 && Dh != 128)) return 0;
+  const int nt = attend_nt(static_cast<long long>(T) * (Hq / Hkv));
+  return attend_part_bytes(nt, Dh) + align256(rc::AT_MAX_CTAS * sizeof(unsigned));
+}
+
+int ring_attn_cache_attend(const ra_cache* cache, int layer, const int* slots, const int* n_new, int B, int T, int Hq,
+                           const void* q, const long long* q_strides, float scale, int causal, void* o,
+                           ra_dtype o_dtype, float* lse, void* workspace, size_t workspace_bytes, ra_stream stream) {
+  rc::AttendParams p{};
+  if (layer < 0 || T <= 0 || Hq <= 0 || !o || !lse) return RA_ERR_ARG;
+  if (o_dtype != RA_BF16 && o_dtype != RA_F32) return RA_ERR_ARG;
+  int st = cache_pool(cache, layer, &p.c);
+  if (st != RA_OK) return st;
+  if ((st = cache_batch(slots, B)) != RA_OK) return st;
+  if (Hq % p.c.heads) return RA_ERR_SHAPE;
+  if ((st = cache_rows(q, q_strides, B, Hq, T)) != RA_OK) return st;
+  if (!aligned16(o) || reinterpret_cast<uintptr_t>(lse) % 4 || reinterpret_cast<uintptr_t>(n_new) % 4) return RA_ERR_ALIGN;
+  p.g = Hq / p.c.heads;
+  const long long rows = static_cast<long long>(T) * p.g;
+  if (rows > INT_MAX / 2) return RA_ERR_SHAPE;
+  const int nt = attend_nt(rows);
+  p.n_blocks = static_cast<int>((rows + 8 * nt - 1) / (8 * nt));
+  // the line of tiles is numbered in int
+  const double tiles = std::ceil(static_cast<double>(p.c.max_pages) * p.c.page / rc::AT_TILE);
+  if (tiles * p.c.heads * p.n_blocks * B > INT_MAX / 2) return RA_ERR_SHAPE;
+  if ((st = pages_check_ws(workspace, workspace_bytes, ring_attn_cache_attend_workspace_size(T, Hq, p.c.heads, p.c.Dh))) != RA_OK)
+    return st;
+  DevInfo* di = dev_info(&st);
+  if (!di) return st;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.qb = q_strides[0], p.qh = q_strides[1], p.qt = q_strides[2];
+  p.slots = slots;
+  p.n_new = n_new;
+  p.o = o;
+  p.lse = lse;
+  p.part = static_cast<float*>(workspace);
+  p.tickets = reinterpret_cast<unsigned*>(static_cast<char*>(workspace) + attend_part_bytes(nt, p.c.Dh));
+  p.B = B;
+  p.T = T;
+  p.page_shift = p.c.page == 16 ? 4 : p.c.page == 32 ? 5 : p.c.page == 64 ? 6 : 7;
+  p.causal = causal != 0;
+  p.o_f32 = o_dtype == RA_F32;
+  const float sc = (scale > 0.f && std::isfinite(scale)) ? scale : 1.0f / std::sqrt(static_cast<float>(p.c.Dh));
+  p.scale_log2 = sc * 1.4426950408889634f;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int grid = di->sm_count < rc::AT_MAX_CTAS ? di->sm_count : rc::AT_MAX_CTAS;
+  const cudaError_t e = cudaMemsetAsync(p.tickets, 0, grid * sizeof(unsigned), s);
+  if (e != cudaSuccess) return cuda_fail(static_cast<int>(e), "cudaMemsetAsync(cache attention tickets)");
+  return p.c.Dh == 128 ? attend_nt_launch<128>(nt, p, di, grid, s) : attend_nt_launch<64>(nt, p, di, grid, s);
+}
+
+size_t ring_attn_cache_pages_workspace_size(int B, int pages) {
+  if (B < 0 || pages <= 0) return 0;
+  return pages_workspace(3ll * pages + 2ll * B + 1);
+}
+
+int ring_attn_cache_reserve(const ra_cache* cache, const int* slots, const int* n_new, int B, void* workspace,
+                            size_t workspace_bytes, ra_stream stream) {
+  rc::Pool c;
+  int st = cache_pool(cache, -1, &c);
+  if (st != RA_OK) return st;
+  if ((st = cache_batch(slots, B)) != RA_OK) return st;
+  if (!n_new) return RA_ERR_ARG;
+  if (reinterpret_cast<uintptr_t>(n_new) % 4) return RA_ERR_ALIGN;
+  if ((st = pages_check_ws(workspace, workspace_bytes, ring_attn_cache_pages_workspace_size(B, c.pages))) != RA_OK) return st;
+  DevInfo* di = dev_info(&st);
+  if (!di) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  rc::Plan* plan = static_cast<rc::Plan*>(workspace);
+  int* pairs = reinterpret_cast<int*>(static_cast<char*>(workspace) + align256(sizeof(rc::Plan)));
+  int* free_list = pairs + 2 * B;
+  rc::reserve_plan_kernel<<<1, rc::PLAN_THREADS, 0, s>>>(c, slots, n_new, B, plan, pairs, free_list);
+  if ((st = launch_status()) != RA_OK) return st;
+  rc::copy_pages_kernel<<<copy_grid(c, B, di->sm_count), rc::COPY_THREADS, 0, s>>>(c, plan, pairs, pairs + 1, 2, nullptr);
+  return launch_status();
+}
+
+int ring_attn_cache_fork(const ra_cache* cache, const int* src, const int* dst, int B, void* workspace,
+                         size_t workspace_bytes, ra_stream stream) {
+  rc::Pool c;
+  int st = cache_pool(cache, -1, &c);
+  if (st != RA_OK) return st;
+  if ((st = cache_batch(src, B)) != RA_OK || (st = cache_batch(dst, B)) != RA_OK) return st;
+  if ((st = pages_check_ws(workspace, workspace_bytes, ring_attn_cache_pages_workspace_size(B, c.pages))) != RA_OK) return st;
+  DevInfo* di = dev_info(&st);
+  if (!di) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  rc::Plan* plan = static_cast<rc::Plan*>(workspace);
+  int* first = reinterpret_cast<int*>(static_cast<char*>(workspace) + align256(sizeof(rc::Plan)));
+  rc::fork_plan_kernel<<<1, rc::PLAN_THREADS, 0, s>>>(c, src, dst, B, plan, first);
+  if ((st = launch_status()) != RA_OK) return st;
+  const long long items = static_cast<long long>(B) * c.max_pages;
+  const long long blocks = (items + rc::COPY_THREADS - 1) / rc::COPY_THREADS;
+  const int grid = static_cast<int>(blocks < 2ll * di->sm_count ? blocks : 2ll * di->sm_count);
+  rc::fork_apply_kernel<<<grid, rc::COPY_THREADS, 0, s>>>(c, src, dst, plan, first);
+  return launch_status();
+}
+
+int ring_attn_cache_trim(const ra_cache* cache, const int* slots, const int* keep, int B, ra_stream stream) {
+  rc::Pool c;
+  int st = cache_pool(cache, -1, &c);
+  if (st != RA_OK) return st;
+  if ((st = cache_batch(slots, B)) != RA_OK) return st;
+  if (reinterpret_cast<uintptr_t>(keep) % 4) return RA_ERR_ALIGN;
+  if (!dev_info(&st)) return st;
+  rc::trim_kernel<<<B, rc::COPY_THREADS, 0, static_cast<cudaStream_t>(stream)>>>(c, slots, keep, B);
+  return launch_status();
+}
+
+int ring_attn_cache_compact(const ra_cache* cache, void* workspace, size_t workspace_bytes, ra_stream stream) {
+  rc::Pool c;
+  int st = cache_pool(cache, -1, &c);
+  if (st != RA_OK) return st;
+  if ((st = pages_check_ws(workspace, workspace_bytes, ring_attn_cache_pages_workspace_size(0, c.pages))) != RA_OK) return st;
+  DevInfo* di = dev_info(&st);
+  if (!di) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  rc::Plan* plan = static_cast<rc::Plan*>(workspace);
+  int* holes = reinterpret_cast<int*>(static_cast<char*>(workspace) + align256(sizeof(rc::Plan)));
+  int *movers = holes + c.pages, *moved_to = movers + c.pages;
+  rc::compact_plan_kernel<<<1, rc::PLAN_THREADS, 0, s>>>(c, plan, holes, movers, moved_to);
+  if ((st = launch_status()) != RA_OK) return st;
+  const int grid = copy_grid(c, c.pages / 2 + 1, di->sm_count);
+  rc::copy_pages_kernel<<<grid, rc::COPY_THREADS, 0, s>>>(c, plan, movers, holes, 1, moved_to);
+  return launch_status();
+}
+
+}  // extern "C"

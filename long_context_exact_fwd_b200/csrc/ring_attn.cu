@@ -62,6 +62,7 @@ struct DevInfo {
   std::atomic<bool> fwd_attr[4] = {false, false, false, false};
   std::atomic<bool> bwd_attr[2] = {false, false};   // [HD 128, HD 64]
   std::atomic<bool> ffn_attr{false};
+  std::atomic<bool> attend_attr[2][3] = {};         // [Dh 128, Dh 64][8-row column blocks - 1]
 };
 
 std::mutex g_dev_mu;
@@ -383,6 +384,7 @@ const char* ring_attn_strerror(int code) {
     case RA_ERR_CUDA: return "CUDA runtime/driver call failed";
     case RA_ERR_TIMEOUT: return "a kernel gave up on a bounded internal wait";
     case RA_ERR_DEVICE: return "current device is not an sm_100 (B200-class) GPU";
+    case RA_ERR_PAGES: return "a slot, length or page number on the device is out of range, or no page is free";
     default: return "unknown status code";
   }
 }
@@ -664,3 +666,7 @@ int ring_attn_bwd_noalloc(const void* q, const void* k, const void* v, const voi
 
 // The blockwise feedforward's host side (workspace, checks, launch, entry points).
 #include "ffn_host.cuh"
+
+// Rotary positions, and the 8-bit key/value cache.
+#include "rope_host.cuh"
+#include "cache_host.cuh"

@@ -1,0 +1,159 @@
+// Rotary positions: every pair (x1, x2) of the first `rot` columns of a head is turned by the
+// angle a = position * theta_i and scaled by the plan's amplitude A:
+//   y1 = A (x1 cos a - x2 sin a),   y2 = A (x1 sin a + x2 cos a);
+// columns from `rot` on pass through.  The gradient is the inverse turn (sin -> -sin) with the
+// same A.  Pairs are (2i, 2i + 1), or (i, i + rot / 2).
+//
+// Angles.  The plan holds theta_i / 2 pi as a 64-bit fixed-point fraction of a turn, so
+// position * step mod 2^64 is the phase with whole turns dropped, exact in integer arithmetic:
+// the error left is position * 2^-65 turns, at any position.  The phase is brought to the nearest
+// quarter turn before it becomes a float (|r| <= 1/8 turn keeps 24 good bits), sincospif does the
+// rest.  No table is kept or read.
+//
+// Bound: memory (each element read and written once).  A thread owns one group of pairs of one
+// token and walks over heads, so one sine and cosine serve `heads_per_thread` heads of Q and K.
+#pragma once
+#include <cstdint>
+#include <cuda_bf16.h>
+
+namespace ra {
+namespace rope {
+
+constexpr int THREADS = 256;
+
+struct Tensor {               // one of Q, K: strides in elements, last dimension contiguous
+  const void* x;
+  void* y;
+  long long xb, xh, xs, yb, yh, ys;
+  int heads;
+};
+
+struct Params {
+  Tensor t[2];                // heads of t[0], then of t[1] (heads 0: absent)
+  const unsigned long long* steps;   // [rot / 2], theta / 2 pi in units of 2^-64 turn
+  const long long* pos;       // or null: position = offset + s
+  long long pos_b, pos_s, offset;
+  long long tokens;           // B * S
+  int S, Dh, rot;
+  int units;                  // groups of columns per token
+  int rot_units;              // of them, groups that are rotated
+  int heads_per_thread;
+  float amplitude;
+  int inverse;
+};
+
+__device__ __forceinline__ float to_f(float v) { return v; }
+__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ void from_f(float v, float& o) { o = v; }
+__device__ __forceinline__ void from_f(float v, __nv_bfloat16& o) { o = __float2bfloat16_rn(v); }
+
+template <typename T, int N>
+struct alignas(sizeof(T) * N) Pack {
+  T v[N];
+};
+
+// VECTOR: N elements move as one aligned access; otherwise one by one.
+template <typename T, int N, bool VECTOR>
+__device__ __forceinline__ void load(const T* p, T (&v)[N]) {
+  if (VECTOR) {
+    const Pack<T, N> a = *reinterpret_cast<const Pack<T, N>*>(p);
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = a.v[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = p[i];
+  }
+}
+template <typename T, int N, bool VECTOR>
+__device__ __forceinline__ void store(T* p, const T (&v)[N]) {
+  if (VECTOR) {
+    Pack<T, N> a;
+#pragma unroll
+    for (int i = 0; i < N; ++i) a.v[i] = v[i];
+    *reinterpret_cast<Pack<T, N>*>(p) = a;
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) p[i] = v[i];
+  }
+}
+
+// cos and sin of 2 pi * phase * 2^-64.
+__device__ __forceinline__ void turn(unsigned long long phase, float& c, float& s) {
+  const unsigned quarter = static_cast<unsigned>((phase + (1ull << 61)) >> 62) & 3u;
+  const long long r = static_cast<long long>(phase - (static_cast<unsigned long long>(quarter) << 62));
+  // r * 2^-64 turns = 2 r * 2^-64 half turns; the top 32 bits of r hold more than a float does
+  const float x = static_cast<float>(static_cast<int>(r >> 32)) * 4.6566128730773926e-10f;   // 2^-31
+  float sr, cr;
+  sincospif(x, &sr, &cr);
+  const float a = (quarter & 1u) ? sr : cr, b = (quarter & 1u) ? cr : sr;
+  c = (quarter == 1u || quarter == 2u) ? -a : a;
+  s = (quarter >= 2u) ? -b : b;
+}
+
+// A unit is N columns (interleaved: N / 2 pairs) or N columns and their N partners (half).
+template <typename T, int N, bool INTERLEAVED, bool VECTOR>
+__global__ void __launch_bounds__(THREADS) rope_kernel(const Params p) {
+  const long long id = static_cast<long long>(blockIdx.x) * THREADS + threadIdx.x;
+  const long long token = id / p.units;
+  if (token >= p.tokens) return;
+  const int unit = static_cast<int>(id - token * p.units);
+  const long long b = token / p.S, s = token - b * p.S;
+  const int h0 = blockIdx.y * p.heads_per_thread;
+  const int all = p.t[0].heads + p.t[1].heads;
+  const int h1 = min(h0 + p.heads_per_thread, all);
+  const bool rotated = unit < p.rot_units;
+  constexpr int PAIRS = INTERLEAVED ? N / 2 : N;
+  float c[PAIRS], sn[PAIRS];
+  int col, col2 = 0;
+  if (rotated) {
+    const long long pos = p.pos ? p.pos[b * p.pos_b + s * p.pos_s] : p.offset + s;
+    const int i0 = unit * PAIRS;
+#pragma unroll
+    for (int i = 0; i < PAIRS; ++i) {
+      turn(static_cast<unsigned long long>(pos) * p.steps[i0 + i], c[i], sn[i]);
+      c[i] *= p.amplitude;
+      sn[i] *= p.inverse ? -p.amplitude : p.amplitude;
+    }
+    col = INTERLEAVED ? unit * N : i0;
+    col2 = i0 + p.rot / 2;
+  } else {
+    col = p.rot + (unit - p.rot_units) * N;
+  }
+#pragma unroll 2
+  for (int h = h0; h < h1; ++h) {
+    const bool second = h >= p.t[0].heads;
+    const Tensor& t = p.t[second ? 1 : 0];
+    const int hh = second ? h - p.t[0].heads : h;
+    const T* x = static_cast<const T*>(t.x) + b * t.xb + hh * t.xh + s * t.xs;
+    T* y = static_cast<T*>(t.y) + b * t.yb + hh * t.yh + s * t.ys;
+    T a[N];
+    load<T, N, VECTOR>(x + col, a);
+    if (!rotated) {
+      if (y != x) store<T, N, VECTOR>(y + col, a);
+      continue;
+    }
+    if (INTERLEAVED) {
+#pragma unroll
+      for (int i = 0; i < PAIRS; ++i) {
+        const float x1 = to_f(a[2 * i]), x2 = to_f(a[2 * i + 1]);
+        from_f(fmaf(x1, c[i], -x2 * sn[i]), a[2 * i]);
+        from_f(fmaf(x1, sn[i], x2 * c[i]), a[2 * i + 1]);
+      }
+      store<T, N, VECTOR>(y + col, a);
+    } else {
+      T a2[N];
+      load<T, N, VECTOR>(x + col2, a2);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const float x1 = to_f(a[i]), x2 = to_f(a2[i]);
+        from_f(fmaf(x1, c[i], -x2 * sn[i]), a[i]);
+        from_f(fmaf(x1, sn[i], x2 * c[i]), a2[i]);
+      }
+      store<T, N, VECTOR>(y + col, a);
+      store<T, N, VECTOR>(y + col2, a2);
+    }
+  }
+}
+
+}  // namespace rope
+}  // namespace ra

@@ -1,0 +1,138 @@
+// Host side of the rotary positions: argument checks, the choice of the access width and the
+// launch.  Included once, at the end of ring_attn.cu (it uses that file's helpers).
+#pragma once
+#include "rope.cuh"
+
+namespace {
+
+// Bytes from the first to behind the last element of a [B][H][S][Dh] view.
+long long rope_extent(long long sb, long long sh, long long ss, int B, int H, int S, int Dh) {
+  return (B - 1) * sb + (H - 1) * sh + (S - 1) * ss + Dh;
+}
+
+int rope_tensor(ra::rope::Tensor* t, const void* x, void* y, int H, const long long* st, int B, int S, int Dh,
+                int size) {
+  if (!x || !y || !st || H <= 0) return RA_ERR_ARG;
+  const int n[3] = {B, H, S};
+  long long d[6];   // strides, those of dimensions of one element dropped
+  for (int i = 0; i < 6; ++i) {
+    d[i] = n[i % 3] == 1 ? 0 : st[i];
+    if (d[i] < 0 || d[i] > (1ll << 59) / n[i % 3]) return RA_ERR_SHAPE;
+  }
+  // Every output element is written by one thread: going up the strides, each dimension has to
+  // step over all of the smaller ones.
+  bool seen[3] = {n[0] == 1, n[1] == 1, n[2] == 1};
+  for (long long reach = Dh;;) {
+    int m = -1;
+    for (int i = 0; i < 3; ++i)
+      if (!seen[i] && (m < 0 || d[3 + i] < d[3 + m])) m = i;
+    if (m < 0) break;
+    if (d[3 + m] < reach) return RA_ERR_SHAPE;
+    reach += d[3 + m] * (n[m] - 1);
+    seen[m] = true;
+  }
+  *t = {x, y, d[0], d[1], d[2], d[3], d[4], d[5], H};
+  const uintptr_t xa = reinterpret_cast<uintptr_t>(x), ya = reinterpret_cast<uintptr_t>(y);
+  if (xa % size || ya % size) return RA_ERR_ALIGN;
+  bool same = xa == ya;
+  for (int i = 0; i < 3; ++i) same = same && d[i] == d[i + 3];
+  const uintptr_t xe = xa + rope_extent(d[0], d[1], d[2], B, H, S, Dh) * size;
+  const uintptr_t ye = ya + rope_extent(d[3], d[4], d[5], B, H, S, Dh) * size;
+  if (!same && xa < ye && ya < xe) return RA_ERR_ARG;   // in place, or apart
+  return RA_OK;
+}
+
+template <typename T, int N, bool VECTOR>
+int rope_launch(ra::rope::Params& p, int sm_count, bool interleaved, cudaStream_t stream) {
+  using namespace ra::rope;
+  p.rot_units = interleaved ? p.rot / N : p.rot / 2 / N;
+  p.units = p.rot_units + (p.Dh - p.rot) / N;
+  const long long threads = p.tokens * p.units;
+  const long long blocks = (threads + THREADS - 1) / THREADS;
+  const int heads = p.t[0].heads + p.t[1].heads;
+  // As many heads per thread (one sine and cosine for all of them) as leaves about two waves of
+  // full SMs.
+  int hpt = 1;
+  while (hpt < heads && hpt < 16 && blocks * ((heads + 2 * hpt - 1) / (2 * hpt)) >= 16ll * sm_count) hpt *= 2;
+  p.heads_per_thread = hpt;
+  const int gy = (heads + hpt - 1) / hpt;
+  if (blocks > INT_MAX || gy > 65535) return RA_ERR_SHAPE;
+  const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(gy));
+  if (interleaved) {
+    if constexpr (N >= 2) rope_kernel<T, N, true, VECTOR><<<grid, THREADS, 0, stream>>>(p);
+  } else {
+    rope_kernel<T, N, false, VECTOR><<<grid, THREADS, 0, stream>>>(p);
+  }
+  return launch_status();
+}
+
+template <typename T>
+int rope_dispatch(ra::rope::Params& p, int sm_count, bool interleaved, cudaStream_t stream) {
+  constexpr int WIDE = 16 / static_cast<int>(sizeof(T));
+  // The widest access that every row start, the pairs' distance and the untouched rest allow.
+  int n = WIDE;
+  auto fits = [&](int m) {
+    if ((interleaved ? p.rot : p.rot / 2) % m || (p.Dh - p.rot) % m) return false;
+    for (const ra::rope::Tensor& t : p.t) {
+      if (!t.heads) continue;
+      if (reinterpret_cast<uintptr_t>(t.x) % (m * sizeof(T)) || reinterpret_cast<uintptr_t>(t.y) % (m * sizeof(T)))
+        return false;
+      for (long long st : {t.xb, t.xh, t.xs, t.yb, t.yh, t.ys})
+        if (st % m) return false;
+    }
+    return true;
+  };
+  while (n > 1 && !fits(n)) n /= 2;
+  if constexpr (WIDE == 8) {
+    if (n == 8) return rope_launch<T, 8, true>(p, sm_count, interleaved, stream);
+  }
+  if (n == 4) return rope_launch<T, 4, true>(p, sm_count, interleaved, stream);
+  if (n == 2) return rope_launch<T, 2, true>(p, sm_count, interleaved, stream);
+  // Nothing lines up: single elements (an interleaved pair is still one thread's; its partner
+  // columns and an even rest are two at a time).
+  if (interleaved && (p.Dh - p.rot) % 2 == 0) return rope_launch<T, 2, false>(p, sm_count, true, stream);
+  if (interleaved) return RA_ERR_SHAPE;   // unreachable: Dh is even
+  return rope_launch<T, 1, false>(p, sm_count, false, stream);
+}
+
+}  // namespace
+
+extern "C" {
+
+int ring_attn_rope(const void* q, void* q_out, int Hq, const long long* q_strides, const void* k, void* k_out, int Hk,
+                   const long long* k_strides, int B, int S, int Dh, const unsigned long long* steps, int rot,
+                   int interleaved, float amplitude, const long long* pos, long long pos_stride_b,
+                   long long pos_stride_s, long long offset, int inverse, ra_dtype dtype, ra_stream stream) {
+  if (!steps || B <= 0 || S <= 0 || Dh <= 0 || !std::isfinite(amplitude)) return RA_ERR_ARG;
+  if (dtype != RA_BF16 && dtype != RA_F32) return RA_ERR_ARG;
+  if (Dh % 2 || Dh > 1024 || rot <= 0 || rot > Dh || rot % 2) return RA_ERR_SHAPE;
+  if (pos && (pos_stride_b < 0 || pos_stride_s < 0)) return RA_ERR_SHAPE;
+  if (reinterpret_cast<uintptr_t>(steps) % 8 || reinterpret_cast<uintptr_t>(pos) % 8) return RA_ERR_ALIGN;
+  const int size = dtype == RA_BF16 ? 2 : 4;
+  ra::rope::Params p{};
+  int st = rope_tensor(&p.t[0], q, q_out, Hq, q_strides, B, S, Dh, size);
+  if (st != RA_OK) return st;
+  if (k || k_out || Hk) {
+    if ((st = rope_tensor(&p.t[1], k, k_out, Hk, k_strides, B, S, Dh, size)) != RA_OK) return st;
+    if (q_out == k_out) return RA_ERR_ARG;
+  }
+  if (static_cast<long long>(Hq) + Hk > 65535) return RA_ERR_SHAPE;
+  DevInfo* di = dev_info(&st);
+  if (!di) return st;
+  p.steps = steps;
+  p.pos = pos;
+  p.pos_b = pos_stride_b;
+  p.pos_s = pos_stride_s;
+  p.offset = offset;
+  p.tokens = static_cast<long long>(B) * S;
+  p.S = S;
+  p.Dh = Dh;
+  p.rot = rot;
+  p.amplitude = amplitude;
+  p.inverse = inverse != 0;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return dtype == RA_BF16 ? rope_dispatch<__nv_bfloat16>(p, di->sm_count, interleaved != 0, s)
+                          : rope_dispatch<float>(p, di->sm_count, interleaved != 0, s);
+}
+
+}  // extern "C"

@@ -7,9 +7,11 @@ importing this module fails loudly when the library has not been built.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import math
 import os
-from typing import List, Optional, Tuple
+from typing import List, NamedTuple, Optional, Tuple
 
 import torch
 
@@ -20,7 +22,8 @@ if not os.path.exists(_LIB_PATH):
         "(there is no CPU fallback)")
 _lib = ctypes.CDLL(_LIB_PATH)
 
-RA_OK, RA_ERR_ARG, RA_ERR_SHAPE, RA_ERR_ALIGN, RA_ERR_WORKSPACE, RA_ERR_CUDA, RA_ERR_TIMEOUT, RA_ERR_DEVICE = range(8)
+(RA_OK, RA_ERR_ARG, RA_ERR_SHAPE, RA_ERR_ALIGN, RA_ERR_WORKSPACE, RA_ERR_CUDA, RA_ERR_TIMEOUT, RA_ERR_DEVICE,
+ RA_ERR_PAGES) = range(9)
 RA_BF16, RA_F32 = 0, 1
 
 _vp, _i, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
@@ -59,6 +62,27 @@ _noalloc_max = _sig("ring_attn_bwd_noalloc_max_bytes", _sz)
 _ffn_ws = _sig("ring_attn_ffn_workspace_size", _sz, _i, _i, _i, _i)
 _ffn_fwd = _sig("ring_attn_ffn_fwd", _i, _vp, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _i, _vp, _vp, _sz, _vp)
 _ffn_block = _sig("ring_attn_ffn_block", _i, _vp, _i, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _i, _vp, _vp, _sz, _vp)
+_ll = ctypes.c_longlong
+
+
+class _CacheStruct(ctypes.Structure):   # ra_cache
+    _fields_ = ([(n, _vp) for n in ("k", "v", "k_scale", "v_scale", "table", "lens", "refs")]
+                + [(n, _i) for n in ("layers", "pages", "heads", "page", "head_dim", "slots", "max_pages")])
+
+
+_llp, _cp = ctypes.POINTER(_ll), ctypes.POINTER(_CacheStruct)
+_rope = _sig("ring_attn_rope", _i, _vp, _vp, _i, _llp, _vp, _vp, _i, _llp, _i, _i, _i, _vp, _i, _i, _f, _vp, _ll, _ll,
+             _ll, _i, _i, _vp)
+_cache_pages_ws = _sig("ring_attn_cache_pages_workspace_size", _sz, _i, _i)
+_cache_reserve = _sig("ring_attn_cache_reserve", _i, _cp, _vp, _vp, _i, _vp, _sz, _vp)
+_cache_append = _sig("ring_attn_cache_append", _i, _cp, _i, _vp, _vp, _i, _i, _vp, _llp, _vp, _llp, _vp)
+_cache_read = _sig("ring_attn_cache_read", _i, _cp, _i, _vp, _vp, _i, _i, _vp, _vp, _vp)
+_cache_attend_ws = _sig("ring_attn_cache_attend_workspace_size", _sz, _i, _i, _i, _i)
+_cache_attend = _sig("ring_attn_cache_attend", _i, _cp, _i, _vp, _vp, _i, _i, _i, _vp, _llp, _f, _i, _vp, _i, _vp, _vp,
+                     _sz, _vp)
+_cache_fork = _sig("ring_attn_cache_fork", _i, _cp, _vp, _vp, _i, _vp, _sz, _vp)
+_cache_trim = _sig("ring_attn_cache_trim", _i, _cp, _vp, _vp, _i, _vp)
+_cache_compact = _sig("ring_attn_cache_compact", _i, _cp, _vp, _sz, _vp)
 _exp2_check = _sig("ring_attn_exp2_check", _i, _vp, _vp, _vp, ctypes.c_longlong, _vp)
 _wait_selftest = _sig("ring_attn_wait_selftest", _i, ctypes.c_longlong, _vp)
 
@@ -313,6 +337,337 @@ def ffn(o: torch.Tensor, w1: torch.Tensor, b1: torch.Tensor, w2: torch.Tensor, b
                           b2.data_ptr(), f, out.data_ptr(), workspace.data_ptr(), wsb, _stream(stream))
         _check(code, "ring_attn_ffn_block")
     return out
+
+
+# ---------------------------------------------------------------------------- rotary positions
+class RopePlan(NamedTuple):
+    """What rope() goes by: per pair the turn per position (theta / 2 pi in units of 2^-64 turn, as
+    int64 bits, on the device), the pairing and the amplitude.  Made once by rope_plan()."""
+    steps: torch.Tensor
+    rot: int
+    interleaved: bool
+    amplitude: float
+
+
+def rope_inv_freq(rot: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                  original_length: int = 0, fast: float = 32.0, slow: float = 1.0) -> Tuple[torch.Tensor, float]:
+    """Inverse frequencies theta_i = base^(-2i / rot), i < rot / 2 (float64, CPU), and the amplitude,
+    for contexts `factor` times as long as trained on:
+      "none"    as they are;
+      "linear"  theta / factor (positions interpolated);
+      "base"    base grown to base * factor^(rot / (rot - 2)): the slowest pair is stretched by `factor`, the
+                fastest not at all;
+      "ramp"    by how often a pair turns over `original_length` positions: from `fast` turns on theta, up to
+                `slow` turns theta / factor, linear between; amplitude 0.1 ln(factor) + 1 (the YaRN rule,
+                arXiv 2309.00071)."""
+    if rot <= 0 or rot % 2:
+        raise ValueError(f"rot must be positive and even, got {rot}")
+    if not (base > 0 and math.isfinite(base)) or not (factor > 0 and math.isfinite(factor)):
+        raise ValueError("base and factor must be positive and finite")
+    if scaling == "base":
+        if rot < 4:
+            raise ValueError('scaling "base" needs rot >= 4')
+        base = base * factor ** (rot / (rot - 2))
+    theta = torch.tensor([base ** (-2.0 * i / rot) for i in range(rot // 2)], dtype=torch.float64)
+    if scaling in ("none", "base"):
+        return theta, 1.0
+    if scaling == "linear":
+        return theta / factor, 1.0
+    if scaling == "ramp":
+        if original_length <= 0 or not fast > slow:
+            raise ValueError('scaling "ramp" needs original_length > 0 and fast > slow')
+        turns = original_length * theta / (2 * math.pi)
+        keep = ((turns - slow) / (fast - slow)).clamp(0.0, 1.0)
+        return theta / factor * (1 - keep) + theta * keep, 0.1 * math.log(factor) + 1.0
+    raise ValueError(f"unknown scaling {scaling!r}")
+
+
+def rope_plan(inv_freq: torch.Tensor, layout: str = "half", amplitude: float = 1.0, device=None) -> RopePlan:
+    """The plan for rope(): inv_freq [rot / 2] (radians per position, finite), layout "half" (pairs
+    i, i + rot / 2) or "interleaved" (pairs 2i, 2i + 1)."""
+    if layout not in ("half", "interleaved"):
+        raise ValueError(f'layout must be "half" or "interleaved", got {layout!r}')
+    if inv_freq.dim() != 1 or inv_freq.numel() == 0:
+        raise ValueError("inv_freq must be [rot / 2]")
+    if not math.isfinite(amplitude):
+        raise ValueError("amplitude must be finite")
+    steps = []
+    for w in inv_freq.detach().double().cpu().tolist():
+        if not math.isfinite(w):
+            raise ValueError("inv_freq must be finite")
+        u = round(math.ldexp(math.fmod(w / (2 * math.pi), 1.0), 64)) % (1 << 64)
+        steps.append(u - (1 << 64) if u >= 1 << 63 else u)
+    device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    return RopePlan(torch.tensor(steps, dtype=torch.int64).to(device), 2 * len(steps), layout == "interleaved",
+                    float(amplitude))
+
+
+def _need_rows(t: torch.Tensor, name: str, dtype=None, shape=None) -> None:
+    """As _need, for tensors that may be views: only the last dimension has to be contiguous."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device} but the current device is cuda:{torch.cuda.current_device()}; "
+                         "make the tensors' device current (torch.cuda.device) before the call")
+    if t.dim() != 4 or (t.shape[3] > 1 and t.stride(3) != 1):
+        raise ValueError(f"{name} must have 4 dimensions, the last one contiguous")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _on(stream):
+    """Context in which tensors are allocated for work on `stream` (None: the current one), so that
+    their memory is handed out again only behind that work."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        if not int(stream):
+            return torch.cuda.stream(torch.cuda.default_stream())
+        stream = torch.cuda.ExternalStream(int(stream))
+    return torch.cuda.stream(stream)
+
+
+def rope(q: torch.Tensor, plan: RopePlan, k: Optional[torch.Tensor] = None, pos: Optional[torch.Tensor] = None,
+         offset: int = 0, inverse: bool = False, out: Optional[torch.Tensor] = None,
+         k_out: Optional[torch.Tensor] = None, stream=None):
+    """Rotary positions (ring_attn_rope) on q [B, Hq, S, Dh] and, in the same launch, k [B, Hk, S, Dh];
+    bf16 or float32, views with a contiguous last dimension (a fused projection's columns) included.
+    Position of token s: pos[b, s] (int64, [B, S] or [S]), or offset + s.  `out` / `k_out` may be the
+    inputs themselves.  inverse=True turns back: the gradient of the inputs from that of the outputs.
+    Returns the rotated q, or (q, k)."""
+    if q.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("inputs must be bfloat16 or float32")
+    _need_rows(q, "q", q.dtype)
+    B, Hq, S, Dh = q.shape
+    if plan.rot > Dh:
+        raise ValueError(f"the plan rotates {plan.rot} columns, heads have {Dh}")
+    _need(plan.steps, "plan.steps", torch.int64, (plan.rot // 2,))
+    pos_ptr = pos_b = pos_s = 0
+    if pos is not None:
+        if not pos.is_cuda or pos.device.index != q.device.index:
+            raise ValueError(f"pos must be on {q.device}")
+        if pos.dtype != torch.int64:
+            raise ValueError(f"pos must be torch.int64, got {pos.dtype}")
+        if tuple(pos.shape) not in ((S,), (B, S)):
+            raise ValueError(f"pos must have shape {(S,)} or {(B, S)}, got {tuple(pos.shape)}")
+        pos_ptr, pos_s = pos.data_ptr(), pos.stride(-1)
+        pos_b = pos.stride(0) if pos.dim() == 2 else 0
+    k_ptr = k_out_ptr = Hk = 0
+    k_strides = None
+    if k is not None:
+        _need_rows(k, "k", q.dtype, (B, k.shape[1], S, Dh))
+        Hk = k.shape[1]
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    with _on(stream):
+        if out is None:
+            out = torch.empty((B, Hq, S, Dh), dtype=q.dtype, device=q.device)
+        if k is not None and k_out is None:
+            k_out = torch.empty((B, Hk, S, Dh), dtype=q.dtype, device=q.device)
+    _need_rows(out, "out", q.dtype, q.shape)
+    strides = (_ll * 6)(*q.stride()[:3], *out.stride()[:3])
+    if k is not None:
+        _need_rows(k_out, "k_out", q.dtype, k.shape)
+        k_strides = (_ll * 6)(*k.stride()[:3], *k_out.stride()[:3])
+        k_ptr, k_out_ptr = k.data_ptr(), k_out.data_ptr()
+    code = _rope(q.data_ptr(), out.data_ptr(), Hq, strides, k_ptr or None, k_out_ptr or None, Hk, k_strides, B, S, Dh,
+                 plan.steps.data_ptr(), plan.rot, 1 if plan.interleaved else 0, plan.amplitude, pos_ptr or None, pos_b,
+                 pos_s, int(offset), 1 if inverse else 0, RA_BF16 if q.dtype == torch.bfloat16 else RA_F32,
+                 _stream(stream))
+    _check(code, "ring_attn_rope")
+    return out if k is None else (out, k_out)
+
+
+# ---------------------------------------------------------------------------- 8-bit key/value cache
+class KVCache:
+    """A paged key/value cache in 8 bits (ra_cache): checks its tensors once and keeps them.
+      k, v              uint8 [layers, pages, heads, page, Dh] (bits of torch.float8_e4m3fn)
+      k_scale, v_scale  float32 [layers, pages, heads], powers of two: value = code * scale
+      table             int32 [slots, max_pages], page numbers, -1: none
+      lens, refs        int32 [slots] tokens held, [pages] holders of a page
+    kv_cache() makes an empty one."""
+    __slots__ = ("k", "v", "k_scale", "v_scale", "table", "lens", "refs", "_c", "_ref")
+
+    def __init__(self, k, v, k_scale, v_scale, table, lens, refs):
+        if k.dim() != 5 or table.dim() != 2:
+            raise ValueError("k must be [layers, pages, heads, page, Dh] and table [slots, max_pages]")
+        L, P, H, page, Dh = k.shape
+        N, M = table.shape
+        for name, t, dt, shape in (("k", k, torch.uint8, k.shape), ("v", v, torch.uint8, k.shape),
+                                   ("k_scale", k_scale, torch.float32, (L, P, H)),
+                                   ("v_scale", v_scale, torch.float32, (L, P, H)),
+                                   ("table", table, torch.int32, (N, M)), ("lens", lens, torch.int32, (N,)),
+                                   ("refs", refs, torch.int32, (P,))):
+            _need(t, name, dt, shape)
+        if page not in (16, 32, 64, 128) or Dh not in (64, 128):
+            raise ValueError(f"pages of 16, 32, 64 or 128 tokens and heads of 64 or 128, got {page} and {Dh}")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.table, self.lens, self.refs = table, lens, refs
+        self._c = _CacheStruct(*(t.data_ptr() for t in (k, v, k_scale, v_scale, table, lens, refs)), L, P, H, page, Dh,
+                               N, M)
+        self._ref = ctypes.byref(self._c)
+
+    def _at(self) -> "_CacheStruct":
+        """The C description, for a call on the current device."""
+        if self.k.device.index != torch.cuda.current_device():
+            raise ValueError(f"the cache is on {self.k.device} but the current device is "
+                             f"cuda:{torch.cuda.current_device()}")
+        return self._ref
+
+
+def kv_cache(layers: int, pages: int, heads: int, page: int, Dh: int, slots: int, max_pages: int,
+             device=None) -> KVCache:
+    """An empty cache: `pages` pages of `page` tokens shared by `slots` sequences of up to max_pages pages."""
+    device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    z = lambda *shape: torch.zeros(shape, dtype=torch.int32, device=device)  # noqa: E731
+    codes = [torch.zeros((layers, pages, heads, page, Dh), dtype=torch.uint8, device=device) for _ in range(2)]
+    scales = [torch.full((layers, pages, heads), 2.0 ** -117, dtype=torch.float32, device=device) for _ in range(2)]
+    return KVCache(*codes, *scales, z(slots, max_pages) - 1, z(slots), z(pages))
+
+
+def _batch(t: torch.Tensor, name: str, cache: KVCache, shape=None) -> int:
+    if t.dim() != 1 or t.dtype != torch.int32 or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor of one dimension")
+    if t.device != cache.k.device:
+        raise ValueError(f"{name} is on {t.device}, the cache on {cache.k.device}")
+    if shape is not None and t.shape[0] != shape:
+        raise ValueError(f"{name} must have {shape} entries, got {t.shape[0]}")
+    return t.data_ptr()
+
+
+def _pages_workspace(cache: KVCache, B: int, workspace, stream):
+    need = int(_cache_pages_ws(B, cache._c.pages))
+    if workspace is None:
+        with _on(stream):
+            workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=cache.k.device)
+    _need(workspace, "workspace")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def cache_pages_workspace_bytes(B: int, pages: int) -> int:
+    return int(_cache_pages_ws(B, pages))
+
+
+def cache_reserve(cache: KVCache, slots: torch.Tensor, n_new: torch.Tensor, workspace: Optional[torch.Tensor] = None,
+                  stream=None) -> None:
+    """Room for n_new[b] more tokens of slots[b] (int32, on the device), once for all layers; lens grow
+    (ring_attn_cache_reserve).  Too few pages, or a slot out of range: device_status()."""
+    ref = cache._at()
+    B = slots.shape[0]
+    s, n = _batch(slots, "slots", cache), _batch(n_new, "n_new", cache, B)
+    ws, size = _pages_workspace(cache, B, workspace, stream)
+    _check(_cache_reserve(ref, s, n, B, ws.data_ptr(), size, _stream(stream)), "ring_attn_cache_reserve")
+
+
+def cache_append(cache: KVCache, layer: int, slots: torch.Tensor, n_new: Optional[torch.Tensor], k: torch.Tensor,
+                 v: torch.Tensor, stream=None) -> None:
+    """Writes the last n_new[b] tokens (None: T) of slots[b] into one layer: k, v [B, heads, T, Dh] bf16,
+    views with a contiguous last dimension included (ring_attn_cache_append)."""
+    ref = cache._at()
+    B, H, T, Dh = k.shape
+    if H != cache._c.heads or Dh != cache._c.head_dim:
+        raise ValueError(f"k must be [B, {cache._c.heads}, T, {cache._c.head_dim}], got {tuple(k.shape)}")
+    _need_rows(k, "k", torch.bfloat16)
+    _need_rows(v, "v", torch.bfloat16, k.shape)
+    s = _batch(slots, "slots", cache, B)
+    n = None if n_new is None else _batch(n_new, "n_new", cache, B)
+    code = _cache_append(ref, layer, s, n, B, T, k.data_ptr(), (_ll * 3)(*k.stride()[:3]), v.data_ptr(),
+                         (_ll * 3)(*v.stride()[:3]), _stream(stream))
+    _check(code, "ring_attn_cache_append")
+
+
+def cache_read(cache: KVCache, layer: int, slots: torch.Tensor, length: int, start: Optional[torch.Tensor] = None,
+               k: Optional[torch.Tensor] = None, v: Optional[torch.Tensor] = None,
+               stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """One layer's keys and values, exact in bf16, [B, heads, length, Dh]: positions start[b] (None: 0) ..
+    of slots[b], zero where the sequence holds none (ring_attn_cache_read)."""
+    ref = cache._at()
+    B = slots.shape[0]
+    s = _batch(slots, "slots", cache)
+    at = None if start is None else _batch(start, "start", cache, B)
+    shape = (B, cache._c.heads, length, cache._c.head_dim)
+    with _on(stream):
+        k = torch.empty(shape, dtype=torch.bfloat16, device=cache.k.device) if k is None else k
+        v = torch.empty(shape, dtype=torch.bfloat16, device=cache.k.device) if v is None else v
+    _need(k, "k", torch.bfloat16, shape)
+    _need(v, "v", torch.bfloat16, shape)
+    _check(_cache_read(ref, layer, s, at, B, length, k.data_ptr(), v.data_ptr(), _stream(stream)),
+           "ring_attn_cache_read")
+    return k, v
+
+
+def cache_attend_workspace_bytes(T: int, Hq: int, Hkv: int, Dh: int) -> int:
+    return int(_cache_attend_ws(T, Hq, Hkv, Dh))
+
+
+def cache_attend(cache: KVCache, layer: int, slots: torch.Tensor, n_new: Optional[torch.Tensor], q: torch.Tensor,
+                 scale: Optional[float] = None, causal: bool = True, out_dtype=torch.bfloat16,
+                 workspace: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                 lse: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Attention of each sequence's last n_new[b] tokens (None: T) over one layer of the cache
+    (ring_attn_cache_attend): q [B, Hq, T, Dh] bf16, views with a contiguous last dimension included, Hq a
+    multiple of the cache's heads.  Returns (o [B, Hq, T, Dh] bf16 or float32, lse [B, Hq, T] float32) as
+    fwd() does; a float32 o is one part for merge()."""
+    ref = cache._at()
+    _need_rows(q, "q", torch.bfloat16)
+    B, Hq, T, Dh = q.shape
+    if Dh != cache._c.head_dim or Hq % cache._c.heads:
+        raise ValueError(f"q must be [B, a multiple of {cache._c.heads}, T, {cache._c.head_dim}], got {tuple(q.shape)}")
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("out_dtype must be bfloat16 or float32")
+    s = _batch(slots, "slots", cache, B)
+    n = None if n_new is None else _batch(n_new, "n_new", cache, B)
+    with _on(stream):
+        if workspace is None:
+            workspace = torch.empty(max(cache_attend_workspace_bytes(T, Hq, cache._c.heads, Dh), 1), dtype=torch.uint8,
+                                    device=q.device)
+        out = torch.empty((B, Hq, T, Dh), dtype=out_dtype, device=q.device) if out is None else out
+        lse = torch.empty((B, Hq, T), dtype=torch.float32, device=q.device) if lse is None else lse
+    _need(workspace, "workspace")
+    _need(out, "out", out_dtype, (B, Hq, T, Dh))
+    _need(lse, "lse", torch.float32, (B, Hq, T))
+    code = _cache_attend(ref, layer, s, n, B, T, Hq, q.data_ptr(), (_ll * 3)(*q.stride()[:3]),
+                         float(scale) if scale else 0.0, 1 if causal else 0, out.data_ptr(),
+                         RA_BF16 if out_dtype == torch.bfloat16 else RA_F32, lse.data_ptr(), workspace.data_ptr(),
+                         workspace.numel() * workspace.element_size(), _stream(stream))
+    _check(code, "ring_attn_cache_attend")
+    return out, lse
+
+
+def cache_fork(cache: KVCache, src: torch.Tensor, dst: torch.Tensor, workspace: Optional[torch.Tensor] = None,
+               stream=None) -> None:
+    """The empty slots dst[b] share the pages of src[b] from here on (ring_attn_cache_fork); a page that
+    both hold is copied when cache_reserve() makes room in it."""
+    ref = cache._at()
+    B = src.shape[0]
+    a, d = _batch(src, "src", cache), _batch(dst, "dst", cache, B)
+    ws, size = _pages_workspace(cache, B, workspace, stream)
+    _check(_cache_fork(ref, a, d, B, ws.data_ptr(), size, _stream(stream)), "ring_attn_cache_fork")
+
+
+def cache_trim(cache: KVCache, slots: torch.Tensor, keep: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Keeps the first keep[b] tokens of slots[b] (None: 0, the sequence is freed) and gives up the pages
+    behind them (ring_attn_cache_trim)."""
+    ref = cache._at()
+    B = slots.shape[0]
+    s = _batch(slots, "slots", cache)
+    n = None if keep is None else _batch(keep, "keep", cache, B)
+    _check(_cache_trim(ref, s, n, B, _stream(stream)), "ring_attn_cache_trim")
+
+
+def cache_free(cache: KVCache, slots: torch.Tensor, stream=None) -> None:
+    """Frees the sequences slots[b]: cache_trim() to nothing."""
+    cache_trim(cache, slots, None, stream)
+
+
+def cache_compact(cache: KVCache, workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Moves the pages in use to the lowest page numbers, all layers (ring_attn_cache_compact)."""
+    ref = cache._at()
+    ws, size = _pages_workspace(cache, 0, workspace, stream)
+    _check(_cache_compact(ref, ws.data_ptr(), size, _stream(stream)), "ring_attn_cache_compact")
+
 
 
 def bwd_noalloc_max_bytes() -> int:
