@@ -407,8 +407,8 @@ RA_API int ring_attn_cache_read(const ra_cache* cache, int layer, const int* slo
  *             are left as they were; a query that sees nothing has o = 0, lse = -inf.
  *   workspace ring_attn_cache_attend_workspace_size bytes, 256-byte aligned, of this call alone while
  *             it runs; contents on entry do not matter.
- * exp(s - lse) is rounded to fp16 (11 bits) before it multiplies v; sums are float32.  A clear of
- * the workspace's counters and one launch.
+ * exp(s - lse) is rounded to fp16 (11 bits) before it multiplies v; sums are float32.  Two
+ * launches.
  */
 RA_API size_t ring_attn_cache_attend_workspace_size(int T, int Hq, int Hkv, int Dh);
 RA_API int ring_attn_cache_attend(const ra_cache* cache, int layer, const int* slots, const int* n_new, int B, int T,

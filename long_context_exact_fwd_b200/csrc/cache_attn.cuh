@@ -19,8 +19,8 @@
 //
 // Bound: memory, 2 Dh bytes per token and head.  Work is a line of 32-token tiles over (sequence,
 // head, row block); every block takes an equal stretch of it, whatever the lengths (they are only
-// known on the device), so stretches end inside sequences: such parts go to the workspace, and the
-// block that finishes a sequence's last part joins them in order.  Each warp streams its own tiles
+// known on the device), so stretches end inside sequences: such parts go to the workspace and a
+// second, small launch joins them.  Each warp streams its own tiles
 // with cp.async through a private ring in shared memory, no block barrier inside a stretch.
 #pragma once
 #include "cache.cuh"
@@ -28,11 +28,16 @@
 namespace ra {
 namespace cache {
 
-constexpr int AT_WARPS = 8;
+constexpr int AT_WARPS = 4;
+constexpr int AT_PER_SM = 2;         // blocks per SM: one joins its warps while the other streams
 constexpr int AT_THREADS = AT_WARPS * 32;
 constexpr int AT_TILE = 32;          // tokens of a warp's tile
 constexpr int AT_STAGES = 3;
-constexpr int AT_MAX_CTAS = 160;     // blocks that the workspace has room for (one per SM)
+constexpr int AT_MAX_CTAS = 320;     // blocks that the workspace has room for (AT_PER_SM per SM)
+// What starting and joining a stretch costs, in tiles: it counts in a block's share.  Measured for 32
+// contexts of 16 to 16384 tokens, 8 heads: 0 115.8 us, 8 102.2, 16 98.7, 24 100.4.
+constexpr int AT_START = 16;
+constexpr int AT_LEAST = 8;          // tiles of a stretch, at least
 constexpr float AT_RAISE = 8.f;      // log2: P <= 2^8, times 2^7 still an fp16 number
 constexpr float AT_P_UNIT = 128.f;
 
@@ -43,8 +48,8 @@ struct AttendParams {
   const int *slots, *n_new;    // n_new null: T
   void* o;                     // [B][Hq][T][Dh] bf16 (or fp32)
   float* lse;                  // [B][Hq][T]
-  float* part;                 // [2 * CTAs][8 NT rows][Dh + 2]
-  unsigned* tickets;           // [CTAs], 0 at launch
+  float* part;                 // [2 * CTAs][8 NT rows][Dh + 4]: O, then m and l
+  int4* split;                 // [CTAs] the segment that starts in a block and ends in another
   int B, T, g, n_blocks;       // row blocks per (sequence, head)
   int page_shift, causal, o_f32;
   float scale_log2;
@@ -58,8 +63,8 @@ struct AttLayout {
   static constexpr int SCALES = AT_WARPS * RING;       // [warp][stage][4] floats
   static constexpr int ML = SCALES + AT_WARPS * AT_STAGES * 16;   // [warp][rows][2] floats, rows <= 32
   static constexpr int NANS = ML + AT_WARPS * 32 * 8;  // [HD] ints
-  static constexpr int PREFIX = NANS + HD * 4;         // [B + 1] ints
-  static int bytes(int B) { return PREFIX + (B + 1) * 4; }
+  static constexpr int PREFIX = NANS + HD * 4;         // [B + 1] ints, then slots [B], lengths [B]
+  static int bytes(int B) { return PREFIX + (3 * B + 1) * 4; }
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool fill) {
@@ -116,8 +121,23 @@ __device__ __forceinline__ uint32_t value_offset(int t, int chunk) {
   return line * 128 + ((at ^ (((t >> 1) & 3) << 1)) << 4);
 }
 
+// Four columns of one finished row (row = t * g + head) from its reference m, sum z and product a.
+template <int HD>
+__device__ __forceinline__ void store_row(const AttendParams& p, int b, int h, int row, int d, float m, float z, float4 a) {
+  const int tt = row / p.g, hq = h * p.g + row % p.g;
+  const long long at = (static_cast<long long>(b) * p.c.heads * p.g + hq) * p.T + tt;
+  const float inv = z > 0.f ? 1.f / z : z;   // nothing seen: 0; NaN stays
+  a = make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
+  if (p.o_f32)
+    *reinterpret_cast<float4*>(static_cast<float*>(p.o) + at * HD + d) = a;
+  else
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + at * HD + d) =
+        make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
+  if (d == 0) p.lse[at] = z == 0.f ? -INFINITY : (m + log2f(z)) * 0.69314718055994531f;
+}
+
 template <int HD, int NT>
-__global__ void __launch_bounds__(AT_THREADS, 1) attend_kernel(const AttendParams p) {
+__global__ void __launch_bounds__(AT_THREADS, AT_PER_SM) attend_kernel(const AttendParams p) {
   using L = AttLayout<HD>;
   constexpr int ROWS = 8 * NT;
   constexpr int KS = HD / 16;          // k steps of a score, and 16-column blocks of a head
@@ -131,9 +151,10 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attend_kernel(const AttendParam
   float* s_ml = reinterpret_cast<float*>(smem + L::ML);
   int* s_nan = reinterpret_cast<int*>(smem + L::NANS);
   int* s_prefix = reinterpret_cast<int*>(smem + L::PREFIX);
-  __shared__ int s_warp[33], s_last;
+  int *s_slot = s_prefix + p.B + 1, *s_len = s_slot + p.B;
+  __shared__ int s_warp[AT_WARPS];
 
-  // ---- the line of tiles: per_row[b] tiles for each (head, row block) of sequence b
+  // ---- the line: for each (head, row block) of a sequence AT_START places, then its tiles
   int total = 0;
   for (int b0 = 0; b0 < p.B; b0 += AT_THREADS) {
     const int b = b0 + threadIdx.x;
@@ -144,7 +165,9 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attend_kernel(const AttendParam
         const int len = c.lens[slot], n = p.n_new ? p.n_new[b] : p.T;
         const bool ok = n >= 0 && n <= p.T && len >= 0 && len <= c.max_pages * static_cast<long long>(c.page);
         if (!ok && blockIdx.x == 0) record_status(RA_ERR_PAGES);
-        if (ok && n > 0) w = max(1, (len + AT_TILE - 1) / AT_TILE) * c.heads * p.n_blocks;
+        if (ok && n > 0) w = (max(1, (len + AT_TILE - 1) / AT_TILE) + AT_START) * c.heads * p.n_blocks;
+        s_slot[b] = slot;
+        s_len[b] = len;
       } else if (slot != -1 && blockIdx.x == 0) {
         record_status(RA_ERR_PAGES);
       }
@@ -171,10 +194,11 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attend_kernel(const AttendParam
   if (threadIdx.x == 0) s_prefix[p.B] = total;
   for (int i = threadIdx.x; i < HD; i += AT_THREADS) s_nan[i] = INT_MAX;
   __syncthreads();
-  const int per = max((total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x), AT_WARPS);
+  const int per = max((total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x), AT_LEAST);
   const int line0 = min(static_cast<long long>(total), static_cast<long long>(blockIdx.x) * per);
   const int line1 = min(total, line0 + per);
 
+  int4 mine_split = make_int4(-1, 0, 0, 0);
   for (int x = line0; x < line1;) {
     // ---- which sequence, head and row block
     int b = 0;
@@ -186,13 +210,14 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attend_kernel(const AttendParam
       }
     }
     const int w_b = s_prefix[b + 1] - s_prefix[b];
-    const int nt = w_b / (c.heads * p.n_blocks);
-    const int seg = (x - s_prefix[b]) / nt;
-    const int seg0 = s_prefix[b] + seg * nt;
+    const int places = w_b / (c.heads * p.n_blocks), nt = places - AT_START;
+    const int seg = (x - s_prefix[b]) / places;
+    const int seg0 = s_prefix[b] + seg * places + AT_START;   // of its tiles
     const int h = seg / p.n_blocks, rb = seg - h * p.n_blocks;
-    const int t0 = x - seg0, t1 = min(nt, line1 - seg0);
-    x = seg0 + t1;
-    const int slot = p.slots[b], len = c.lens[slot], n = p.n_new ? p.n_new[b] : p.T;
+    const int t0 = max(0, x - seg0), t1 = min(nt, line1 - seg0);
+    x = seg0 + nt;
+    if (t0 >= t1) continue;                   // its tiles are the next block's
+    const int slot = s_slot[b], len = s_len[b], n = p.n_new ? p.n_new[b] : p.T;
     const int row0 = rb * ROWS, rows = min(ROWS, n * p.g - row0);
     // keys that a row sees: its token's position + 1 (causal), or all
     auto limit_of = [&](int r) { return p.causal ? max(0, min(len, len - n + (row0 + r) / p.g + 1)) : len; };
@@ -496,19 +521,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attend_kernel(const AttendParam
     const bool whole = t0 == 0 && t1 == nt;
     const int c0 = seg0 / per, c1 = (seg0 + nt - 1) / per;
     constexpr int GROUPS = HD / 4;            // float4 groups of a row
-    float* part = p.part + static_cast<long long>(2 * blockIdx.x + (static_cast<int>(blockIdx.x) == c0 ? 1 : 0)) * ROWS * (HD + 2);
-    auto finish = [&](int r, int d, float m, float z, float4 a) {   // one row's group of 4 columns
-      const int tt = (row0 + r) / p.g, hq = h * p.g + (row0 + r) % p.g;
-      const long long row = (static_cast<long long>(b) * c.heads * p.g + hq) * p.T + tt;
-      const float inv = z > 0.f ? 1.f / z : (z == 0.f ? 0.f : z);   // NaN stays
-      a = make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
-      if (p.o_f32)
-        *reinterpret_cast<float4*>(static_cast<float*>(p.o) + row * HD + d) = a;
-      else
-        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + row * HD + d) =
-            make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
-      if (d == 0) p.lse[row] = z == 0.f ? -INFINITY : (m + log2f(z)) * 0.69314718055994531f;
-    };
+    float* part = p.part + static_cast<long long>(2 * blockIdx.x + (static_cast<int>(blockIdx.x) == c0 ? 1 : 0)) * ROWS * (HD + 4);
     for (int i = threadIdx.x; i < ROWS * GROUPS; i += AT_THREADS) {
       const int r = i / GROUPS, d = (i % GROUPS) * 4;
       if (r >= rows) continue;
@@ -535,53 +548,97 @@ __global__ void __launch_bounds__(AT_THREADS, 1) attend_kernel(const AttendParam
         if (s_nan[d + 3] < lim) a.w = nan;
       }
       if (whole) {
-        finish(r, d, m, z, a);
+        store_row<HD>(p, b, h, row0 + r, d, m, z, a);
       } else {
-        float* row = part + r * (HD + 2);
-        *reinterpret_cast<float2*>(row + d) = make_float2(a.x, a.y);
-        *reinterpret_cast<float2*>(row + d + 2) = make_float2(a.z, a.w);
+        float* row = part + r * (HD + 4);
+        *reinterpret_cast<float4*>(row + d) = a;
         if (d == 0) *reinterpret_cast<float2*>(row + HD) = make_float2(m, z);
       }
     }
-    if (!whole) {
-      // the block that brings a segment's last part joins all of them, in order
-      __threadfence();
-      __syncthreads();
-      if (threadIdx.x == 0) s_last = atomicAdd(p.tickets + c0, 1u) == static_cast<unsigned>(c1 - c0);
-      __syncthreads();
-      if (s_last) {
-        __threadfence();
-        for (int i = threadIdx.x; i < ROWS * GROUPS; i += AT_THREADS) {
-          const int r = i / GROUPS, d = (i % GROUPS) * 4;
-          if (r >= rows) continue;
-          const long long step = 2ll * ROWS * (HD + 2);
-          const float* row = p.part + (2ll * c0 * ROWS + r) * (HD + 2);   // part of block c: + (c - c0) * step
-          const float* row_c0 = row + ROWS * (HD + 2);                    // block c0 left its end part
-          float m = -INFINITY;
-          for (int k = c0; k <= c1; ++k) m = fmaxf(m, __ldcg((k == c0 ? row_c0 : row + (k - c0) * step) + HD));
-          float z = 0.f;
-          float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-          for (int k = c0; k <= c1; ++k) {
-            const float* y = k == c0 ? row_c0 : row + (k - c0) * step;
-            const float2 ml = __ldcg(reinterpret_cast<const float2*>(y + HD));
-            const float2 u = __ldcg(reinterpret_cast<const float2*>(y + d));
-            const float2 v = __ldcg(reinterpret_cast<const float2*>(y + d + 2));
-            const float f = ml.y == 0.f ? 0.f : (ml.x == m ? 1.f : ex2_approx(ml.x - m));
-            if (ml.y == 0.f) continue;        // saw nothing
-            z += ml.y * f;
-            a = make_float4(fmaf(u.x, f, a.x), fmaf(u.y, f, a.y), fmaf(v.x, f, a.z), fmaf(v.y, f, a.w));
-          }
-          finish(r, d, m, z, a);
-        }
-      }
-    }
+    if (!whole && static_cast<int>(blockIdx.x) == c0) mine_split = make_int4(c1, b, h, rb);
     __syncthreads();                          // rings and s_nan are free again
     if (lim_max > lim_min) {
       for (int i = threadIdx.x; i < HD; i += AT_THREADS) s_nan[i] = INT_MAX;
       __syncthreads();
     }
   }
+  if (threadIdx.x == 0) p.split[blockIdx.x] = mine_split;
+}
+
+// Joins the parts of the segments that attend_kernel left split: block (c, j) rows 8 j .. 8 j + 7 of the
+// segment that starts in its block c, JOIN_WARPS warps a row, each lane 4 columns of every
+// JOIN_WARPS-th part.  Parts are added in an order that only the lengths fix.  Bound: latency of
+// three dependent reads; one block alone doing this at the end of its stretch cost 0.6 us per part.
+constexpr int JOIN_WARPS = 4;
+constexpr int JOIN_THREADS = 8 * JOIN_WARPS * 32;
+
+template <int HD, int NT>
+__global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const AttendParams p) {
+  constexpr int ROWS = 8 * NT, GROUPS = HD / 4;
+  __shared__ float4 s_o[8][JOIN_WARPS][GROUPS];
+  __shared__ float2 s_ml[8][JOIN_WARPS];
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // the parts are complete
+  const int c0 = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int4 d = p.split[c0];
+  if (d.x < 0) return;
+  const int c1 = d.x, b = d.y, h = d.z;
+  const int row0 = d.w * ROWS, rows = min(ROWS, (p.n_new ? p.n_new[b] : p.T) * p.g - row0);
+  const int rr = warp / JOIN_WARPS, w = warp % JOIN_WARPS;
+  const int r = blockIdx.y * 8 + rr;
+  const long long step = 2ll * ROWS * (HD + 4);
+  // part of block c0: its second place; of a block behind it: the first
+  const float* second = p.part + (2ll * c0 + 1) * ROWS * (HD + 4) + r * (HD + 4);
+  const float* firsts = p.part + 2ll * c0 * ROWS * (HD + 4) + r * (HD + 4);
+  auto part = [&](int k) { return k == 0 ? second : firsts + k * step; };
+  const int n = c1 - c0 + 1;
+  float m = -INFINITY, z = 0.f;
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k0 = w; k0 < n; k0 += 32 * JOIN_WARPS) {   // 32 parts of this warp at a time, one per lane
+    const int k = k0 + lane * JOIN_WARPS;
+    const float2 ml = k < n ? *reinterpret_cast<const float2*>(part(k) + HD) : make_float2(-INFINITY, 0.f);
+    float mk = ml.x;
+#pragma unroll
+    for (int i = 16; i; i >>= 1) mk = fmaxf(mk, __shfl_xor_sync(0xffffffffu, mk, i));
+    mk = fmaxf(mk, m);
+    const float old = m == mk ? 1.f : ex2_approx(m - mk);   // nothing yet: 0, or both -inf
+    m = mk;
+    z *= old;
+    a = make_float4(a.x * old, a.y * old, a.z * old, a.w * old);
+    const float f = ml.y == 0.f ? 0.f : (ml.x == m ? 1.f : ex2_approx(ml.x - m));
+    const unsigned seen = __ballot_sync(0xffffffffu, ml.y != 0.f);
+    float zs = ml.y == 0.f ? 0.f : ml.y * f;
+#pragma unroll
+    for (int i = 16; i; i >>= 1) zs += __shfl_xor_sync(0xffffffffu, zs, i);
+    z += zs;
+    const int here = min(32, (n - k0 + JOIN_WARPS - 1) / JOIN_WARPS);
+#pragma unroll 8
+    for (int j = 0; j < here; ++j) {
+      const float fj = __shfl_sync(0xffffffffu, f, j);
+      if (lane < GROUPS && (seen >> j & 1u)) {
+        const float4 y = *reinterpret_cast<const float4*>(part(k0 + j * JOIN_WARPS) + 4 * lane);
+        a = make_float4(fmaf(y.x, fj, a.x), fmaf(y.y, fj, a.y), fmaf(y.z, fj, a.z), fmaf(y.w, fj, a.w));
+      }
+    }
+  }
+  if (lane < GROUPS) s_o[rr][w][lane] = a;
+  if (lane == 0) s_ml[rr][w] = make_float2(m, z);
+  __syncthreads();
+  if (w || lane >= GROUPS || r >= rows) return;
+  m = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < JOIN_WARPS; ++i) m = fmaxf(m, s_ml[rr][i].x);
+  z = 0.f;
+  a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int i = 0; i < JOIN_WARPS; ++i) {
+    const float2 ml = s_ml[rr][i];
+    if (ml.y == 0.f) continue;
+    const float f = ml.x == m ? 1.f : ex2_approx(ml.x - m);
+    const float4 y = s_o[rr][i][lane];
+    z += ml.y * f;
+    a = make_float4(fmaf(y.x, f, a.x), fmaf(y.y, f, a.y), fmaf(y.z, f, a.z), fmaf(y.w, f, a.w));
+  }
+  store_row<HD>(p, b, h, row0 + r, 4 * lane, m, z, a);
 }
 
 }  // namespace cache

@@ -82,6 +82,20 @@ int attend_launch(const rc::AttendParams& p, DevInfo* di, int grid, cudaStream_t
     set = true;
   }
   rc::attend_kernel<HD, NT><<<grid, rc::AT_THREADS, smem, stream>>>(p);
+  const int st = launch_status();
+  if (st != RA_OK) return st;
+  // The join is set up while attend_kernel runs and waits in the kernel for its end.
+  cudaLaunchAttribute early;
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid, NT);
+  cfg.blockDim = dim3(rc::JOIN_THREADS);
+  cfg.stream = stream;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, rc::join_kernel<HD, NT>, p);
+  if (e != cudaSuccess) return cuda_fail(static_cast<int>(e), "cudaLaunchKernelEx(cache attention join)");
   return launch_status();
 }
 
@@ -93,7 +107,7 @@ int attend_nt_launch(int nt, const rc::AttendParams& p, DevInfo* di, int grid, c
 }
 
 size_t attend_part_bytes(int nt, int Dh) {
-  return align256(static_cast<size_t>(2 * rc::AT_MAX_CTAS) * 8 * nt * (Dh + 2) * sizeof(float));
+  return align256(static_cast<size_t>(2 * rc::AT_MAX_CTAS) * 8 * nt * (Dh + 4) * sizeof(float));
 }
 
 }  // namespace
@@ -150,16 +164,20 @@ int ring_attn_cache_read(const ra_cache* cache, int layer, const int* slots, con
   p.k = static_cast<__nv_bfloat16*>(k);
   p.v = static_cast<__nv_bfloat16*>(v);
   p.length = length;
-  const long long blocks = (static_cast<long long>(length) * (p.c.Dh / rc::UNIT) + rc::IO_THREADS - 1) / rc::IO_THREADS;
-  const dim3 grid(static_cast<unsigned>(blocks), p.c.heads, 2 * B);
-  rc::read_kernel<<<grid, rc::IO_THREADS, 0, static_cast<cudaStream_t>(stream)>>>(p);
+  const int per_block = rc::READ_UNITS * rc::IO_THREADS * rc::UNIT / p.c.Dh;   // tokens
+  const dim3 grid((length + static_cast<long long>(per_block) - 1) / per_block, p.c.heads, 2 * B);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (p.c.Dh == 128)
+    rc::read_kernel<128><<<grid, rc::IO_THREADS, 0, s>>>(p);
+  else
+    rc::read_kernel<64><<<grid, rc::IO_THREADS, 0, s>>>(p);
   return launch_status();
 }
 
 size_t ring_attn_cache_attend_workspace_size(int T, int Hq, int Hkv, int Dh) {
   if (T <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || (Dh != 64 && Dh != 128)) return 0;
   const int nt = attend_nt(static_cast<long long>(T) * (Hq / Hkv));
-  return attend_part_bytes(nt, Dh) + align256(rc::AT_MAX_CTAS * sizeof(unsigned));
+  return attend_part_bytes(nt, Dh) + align256(rc::AT_MAX_CTAS * sizeof(int4));
 }
 
 int ring_attn_cache_attend(const ra_cache* cache, int layer, const int* slots, const int* n_new, int B, int T, int Hq,
@@ -180,7 +198,7 @@ int ring_attn_cache_attend(const ra_cache* cache, int layer, const int* slots, c
   const int nt = attend_nt(rows);
   p.n_blocks = static_cast<int>((rows + 8 * nt - 1) / (8 * nt));
   // the line of tiles is numbered in int
-  const double tiles = std::ceil(static_cast<double>(p.c.max_pages) * p.c.page / rc::AT_TILE);
+  const double tiles = std::ceil(static_cast<double>(p.c.max_pages) * p.c.page / rc::AT_TILE) + rc::AT_START;
   if (tiles * p.c.heads * p.n_blocks * B > INT_MAX / 2) return RA_ERR_SHAPE;
   if ((st = pages_check_ws(workspace, workspace_bytes, ring_attn_cache_attend_workspace_size(T, Hq, p.c.heads, p.c.Dh))) != RA_OK)
     return st;
@@ -193,7 +211,7 @@ int ring_attn_cache_attend(const ra_cache* cache, int layer, const int* slots, c
   p.o = o;
   p.lse = lse;
   p.part = static_cast<float*>(workspace);
-  p.tickets = reinterpret_cast<unsigned*>(static_cast<char*>(workspace) + attend_part_bytes(nt, p.c.Dh));
+  p.split = reinterpret_cast<int4*>(static_cast<char*>(workspace) + attend_part_bytes(nt, p.c.Dh));
   p.B = B;
   p.T = T;
   p.page_shift = p.c.page == 16 ? 4 : p.c.page == 32 ? 5 : p.c.page == 64 ? 6 : 7;
@@ -202,9 +220,8 @@ int ring_attn_cache_attend(const ra_cache* cache, int layer, const int* slots, c
   const float sc = (scale > 0.f && std::isfinite(scale)) ? scale : 1.0f / std::sqrt(static_cast<float>(p.c.Dh));
   p.scale_log2 = sc * 1.4426950408889634f;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int grid = di->sm_count < rc::AT_MAX_CTAS ? di->sm_count : rc::AT_MAX_CTAS;
-  const cudaError_t e = cudaMemsetAsync(p.tickets, 0, grid * sizeof(unsigned), s);
-  if (e != cudaSuccess) return cuda_fail(static_cast<int>(e), "cudaMemsetAsync(cache attention tickets)");
+  const int want = rc::AT_PER_SM * di->sm_count;
+  const int grid = want < rc::AT_MAX_CTAS ? want : rc::AT_MAX_CTAS;
   return p.c.Dh == 128 ? attend_nt_launch<128>(nt, p, di, grid, s) : attend_nt_launch<64>(nt, p, di, grid, s);
 }
 

@@ -32,21 +32,35 @@ __device__ __forceinline__ void unpack2(uint32_t w, float& lo, float& hi) {
   lo = __uint_as_float(w << 16);
   hi = __uint_as_float(w & 0xffff0000u);
 }
-__device__ __forceinline__ float finite_abs(float x) {
-  x = fabsf(x);
-  return x <= 3.4028234663852886e38f ? x : 0.f;   // not finite: 0
+constexpr uint32_t BF16_INF = 0x7f80u;
+// Magnitudes of two bf16, as the numbers that their bits are (they order alike); what is not finite
+// counts as 0.
+__device__ __forceinline__ uint32_t finite_bits(uint32_t w) {
+  w &= 0x7fff7fffu;
+  return __vcmpltu2(w, BF16_INF * 0x10001u) & w;
 }
+// EXACT_RANGE: elements that are not finite, or past 240 * 2^120 (all that a code and scale hold).
+template <bool EXACT_RANGE>
 __device__ __forceinline__ uint32_t quantise4(uint32_t w0, uint32_t w1, float inv) {
-  constexpr float TOP = 240.f * 1.329227995784916e36f;   // 240 * 2^120: all a code and scale can hold
   float x[4];
   unpack2(w0, x[0], x[1]);
   unpack2(w1, x[2], x[3]);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float y = fminf(fmaxf(x[i], -TOP), TOP) * inv;
-    x[i] = fabsf(x[i]) <= 3.4028234663852886e38f ? y : __uint_as_float(0x7fffffffu);
+    if (EXACT_RANGE) {
+      constexpr float TOP = 240.f * 1.329227995784916e36f;
+      const float y = fminf(fmaxf(x[i], -TOP), TOP) * inv;
+      x[i] = fabsf(x[i]) <= 3.4028234663852886e38f ? y : __uint_as_float(0x7fffffffu);
+    } else {
+      x[i] *= inv;
+    }
   }
   return floats_to_codes(x[0], x[1]) | (floats_to_codes(x[2], x[3]) << 16);
+}
+template <bool EXACT_RANGE>
+__device__ __forceinline__ uint4 quantise16(const Elems& x, float inv) {
+  return make_uint4(quantise4<EXACT_RANGE>(x.a.x, x.a.y, inv), quantise4<EXACT_RANGE>(x.a.z, x.a.w, inv),
+                    quantise4<EXACT_RANGE>(x.b.x, x.b.y, inv), quantise4<EXACT_RANGE>(x.b.z, x.b.w, inv));
 }
 __device__ __forceinline__ uint32_t restate4(uint32_t codes, float f) {
   const float2 a = half2_to_float2(codes_to_half2(static_cast<uint16_t>(codes)));
@@ -90,16 +104,16 @@ __global__ void __launch_bounds__(IO_THREADS) append_kernel(const AppendParams p
   float* scale = (kv ? c.v_scale : c.k_scale) + static_cast<long long>(pid) * c.heads + h;
   const int skip = max(0, static_cast<int>(p0 - at0));                       // older tokens in the page
   const int end = static_cast<int>(min(static_cast<long long>(c.page), len - at0));
-  const int per_row = c.Dh / UNIT;
+  const int row_shift = c.Dh == 128 ? 3 : 2;      // units of a row: 8 or 4
+  src += (at0 - p0) * st;
 
   Elems x[NU];
-  float amax = 0.f;
 #pragma unroll
   for (int i = 0; i < NU; ++i) {
     const int u = threadIdx.x + i * IO_THREADS;
-    const int t = u / per_row;
+    const int t = u >> row_shift;
     if (t >= skip && t < end) {
-      const uint4* q = reinterpret_cast<const uint4*>(src + (at0 + t - p0) * st + (u - t * per_row) * UNIT);
+      const uint4* q = reinterpret_cast<const uint4*>(src + t * st + (u & ((1 << row_shift) - 1)) * UNIT);
       x[i].a = q[0];
       x[i].b = q[1];
     } else {
@@ -107,28 +121,37 @@ __global__ void __launch_bounds__(IO_THREADS) append_kernel(const AppendParams p
     }
   }
   const float old_scale = skip ? *scale : 0.f;
+  // Two running magnitudes per word; whether anything is not finite shows in the plain maximum, and
+  // only then are the finite ones looked for.
+  uint32_t top = 0;
 #pragma unroll
-  for (int i = 0; i < NU; ++i) {
-    const uint32_t w[8] = {x[i].a.x, x[i].a.y, x[i].a.z, x[i].a.w, x[i].b.x, x[i].b.y, x[i].b.z, x[i].b.w};
+  for (int i = 0; i < NU; ++i)
+    for (uint32_t w : {x[i].a.x, x[i].a.y, x[i].a.z, x[i].a.w, x[i].b.x, x[i].b.y, x[i].b.z, x[i].b.w})
+      top = __vmaxu2(top, w & 0x7fff7fffu);
+  uint32_t amax = max(top >> 16, top & 0xffffu);
+  if (amax >= BF16_INF) {
+    top = 0;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      float lo, hi;
-      unpack2(w[k], lo, hi);
-      amax = fmaxf(amax, fmaxf(finite_abs(lo), finite_abs(hi)));
-    }
+    for (int i = 0; i < NU; ++i)
+      for (uint32_t w : {x[i].a.x, x[i].a.y, x[i].a.z, x[i].a.w, x[i].b.x, x[i].b.y, x[i].b.z, x[i].b.w})
+        top = __vmaxu2(top, finite_bits(w));
+    amax = max(top >> 16, top & 0xffffu) | 0x10000u;
   }
-  // magnitudes order like their bits
+  const uint32_t flag = __any_sync(0xffffffffu, amax >> 16) ? 0x10000u : 0u;
   __shared__ unsigned s_max[IO_THREADS / 32];
-  const unsigned wmax = __reduce_max_sync(0xffffffffu, __float_as_uint(amax));
+  const unsigned wmax = __reduce_max_sync(0xffffffffu, amax & 0xffffu) | flag;
   if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = wmax;
   if (named_before(p.slots, b, slot)) {           // barrier: s_max and every read of the old scale
     if (reports) record_status(RA_ERR_PAGES);
     return;
   }
-  unsigned m = 0;
+  unsigned m = 0, odd = 0;
 #pragma unroll
-  for (int i = 0; i < IO_THREADS / 32; ++i) m = max(m, s_max[i]);
-  int e = scale_exponent(__uint_as_float(m));
+  for (int i = 0; i < IO_THREADS / 32; ++i) {
+    m = max(m, s_max[i] & 0xffffu);
+    odd |= s_max[i] >> 16;
+  }
+  int e = scale_exponent(__uint_as_float(m << 16));
   int e_old = e;
   if (skip) {
     e_old = min(max(exponent_of(old_scale), E_MIN), E_MAX);
@@ -136,14 +159,14 @@ __global__ void __launch_bounds__(IO_THREADS) append_kernel(const AppendParams p
   }
   const float inv = two_to(-e);
   const float shrink = two_to(max(e_old - e, -126));
+  const bool exact_range = odd || e == E_MAX;     // the same in the whole block
 #pragma unroll
   for (int i = 0; i < NU; ++i) {
     const int u = threadIdx.x + i * IO_THREADS;
-    const int t = u / per_row;
+    const int t = u >> row_shift;
     uint4* dst = reinterpret_cast<uint4*>(codes) + u;
     if (t >= skip && t < end) {
-      *dst = make_uint4(quantise4(x[i].a.x, x[i].a.y, inv), quantise4(x[i].a.z, x[i].a.w, inv),
-                        quantise4(x[i].b.x, x[i].b.y, inv), quantise4(x[i].b.z, x[i].b.w, inv));
+      *dst = exact_range ? quantise16<true>(x[i], inv) : quantise16<false>(x[i], inv);
     } else if (t < skip && e > e_old) {
       const uint4 o = *dst;
       *dst = make_uint4(restate4(o.x, shrink), restate4(o.y, shrink), restate4(o.z, shrink), restate4(o.w, shrink));
@@ -159,8 +182,12 @@ struct ReadParams {
   int length;
 };
 
-// Positions start .. start + length - 1 of each sequence; zero behind its end (and before 0).
+// Positions start .. start + length - 1 of each sequence; zero behind its end (and before 0).  Bound:
+// memory, 1 byte in and 2 out per element; a thread moves READ_UNITS units, loads first.
+constexpr int READ_UNITS = 4;
+template <int HD>
 __global__ void __launch_bounds__(IO_THREADS) read_kernel(const ReadParams p) {
+  constexpr int PER_ROW = HD / UNIT;
   const Pool& c = p.c;
   const int b = blockIdx.z >> 1, kv = blockIdx.z & 1, h = blockIdx.y;
   const int slot = p.slots[b];
@@ -169,35 +196,50 @@ __global__ void __launch_bounds__(IO_THREADS) read_kernel(const ReadParams p) {
     if (blockIdx.x == 0 && threadIdx.x == 0) record_status(RA_ERR_PAGES);
     return;
   }
-  const int per_row = c.Dh / UNIT;
-  const long long u = static_cast<long long>(blockIdx.x) * IO_THREADS + threadIdx.x;
-  const long long t = u / per_row;
-  if (t >= p.length) return;
-  const long long pos = (p.start ? p.start[b] : 0) + t;
-  const int col = static_cast<int>(u - t * per_row) * UNIT;
-  uint32_t out[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-  if (pos >= 0 && pos < c.lens[slot] && pos < c.max_pages * static_cast<long long>(c.page)) {
-    const int pid = c.table[static_cast<long long>(slot) * c.max_pages + pos / c.page];
-    if (pid < 0 || pid >= c.pages) {
-      record_status(RA_ERR_PAGES);
-    } else {
-      const long long ph = static_cast<long long>(pid) * c.heads + h;
-      const uint4 w = *reinterpret_cast<const uint4*>((kv ? c.v : c.k) + (ph * c.page + pos % c.page) * c.Dh + col);
-      const float s = (kv ? c.v_scale : c.k_scale)[ph];
-      const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+  const int start = p.start ? p.start[b] : 0;
+  const int len = static_cast<int>(min(static_cast<long long>(c.lens[slot]), c.max_pages * static_cast<long long>(c.page)));
+  const int* row = c.table + static_cast<long long>(slot) * c.max_pages;
+  const int page_shift = 31 - __clz(c.page);
+  const uint8_t* codes = kv ? c.v : c.k;
+  const float* scales = kv ? c.v_scale : c.k_scale;
+  const int col = (threadIdx.x % PER_ROW) * UNIT;
+  const long long t0 = static_cast<long long>(blockIdx.x) * (READ_UNITS * IO_THREADS / PER_ROW) + threadIdx.x / PER_ROW;
+  uint4 w[READ_UNITS];
+  float s[READ_UNITS];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 lo = half2_to_float2(codes_to_half2(static_cast<uint16_t>(in[i])));
-        const float2 hi = half2_to_float2(codes_to_half2(static_cast<uint16_t>(in[i] >> 16)));
-        out[2 * i] = pack_bf16x2(lo.x * s, lo.y * s);
-        out[2 * i + 1] = pack_bf16x2(hi.x * s, hi.y * s);
+  for (int i = 0; i < READ_UNITS; ++i) {
+    const long long t = t0 + i * (IO_THREADS / PER_ROW), pos = start + t;
+    w[i] = make_uint4(0, 0, 0, 0);
+    s[i] = 0.f;
+    if (t < p.length && pos >= 0 && pos < len) {
+      const int pid = row[pos >> page_shift];
+      if (pid < 0 || pid >= c.pages) {
+        record_status(RA_ERR_PAGES);
+      } else {
+        const long long ph = static_cast<long long>(pid) * c.heads + h;
+        w[i] = *reinterpret_cast<const uint4*>(codes + (((ph << page_shift) + (pos & (c.page - 1))) * HD + col));
+        s[i] = scales[ph];
       }
     }
   }
-  uint4* dst = reinterpret_cast<uint4*>((kv ? p.v : p.k) +
-                                        ((static_cast<long long>(b) * c.heads + h) * p.length + t) * c.Dh + col);
-  dst[0] = make_uint4(out[0], out[1], out[2], out[3]);
-  dst[1] = make_uint4(out[4], out[5], out[6], out[7]);
+  __nv_bfloat16* out = (kv ? p.v : p.k) + (static_cast<long long>(b) * c.heads + h) * p.length * HD + col;
+#pragma unroll
+  for (int i = 0; i < READ_UNITS; ++i) {
+    const long long t = t0 + i * (IO_THREADS / PER_ROW);
+    if (t >= p.length) break;
+    uint32_t y[8];
+    const uint32_t in[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 lo = half2_to_float2(codes_to_half2(static_cast<uint16_t>(in[k])));
+      const float2 hi = half2_to_float2(codes_to_half2(static_cast<uint16_t>(in[k] >> 16)));
+      y[2 * k] = pack_bf16x2(lo.x * s[i], lo.y * s[i]);
+      y[2 * k + 1] = pack_bf16x2(hi.x * s[i], hi.y * s[i]);
+    }
+    uint4* dst = reinterpret_cast<uint4*>(out + t * HD);
+    dst[0] = make_uint4(y[0], y[1], y[2], y[3]);
+    dst[1] = make_uint4(y[4], y[5], y[6], y[7]);
+  }
 }
 
 }  // namespace cache

@@ -50,10 +50,10 @@ int rope_launch(ra::rope::Params& p, int sm_count, bool interleaved, cudaStream_
   const long long threads = p.tokens * p.units;
   const long long blocks = (threads + THREADS - 1) / THREADS;
   const int heads = p.t[0].heads + p.t[1].heads;
-  // As many heads per thread (one sine and cosine for all of them) as leaves about two waves of
-  // full SMs.
+  // As many heads per thread (one sine and cosine for all of them) as leave 8 blocks per SM.  Measured
+  // (16K prompt / float32 gradient): 4 blocks 53.6 / 15.2 us, 8 49.5 / 15.0, 16 50.9 / 16.3, 32 58.9 / 19.2.
   int hpt = 1;
-  while (hpt < heads && hpt < 16 && blocks * ((heads + 2 * hpt - 1) / (2 * hpt)) >= 16ll * sm_count) hpt *= 2;
+  while (hpt < heads && hpt < 16 && blocks * ((heads + 2 * hpt - 1) / (2 * hpt)) >= 8ll * sm_count) hpt *= 2;
   p.heads_per_thread = hpt;
   const int gy = (heads + hpt - 1) / hpt;
   if (blocks > INT_MAX || gy > 65535) return RA_ERR_SHAPE;

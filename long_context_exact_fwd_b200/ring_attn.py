@@ -7,8 +7,8 @@ importing this module fails loudly when the library has not been built.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 import math
 import os
 from typing import List, NamedTuple, Optional, Tuple
@@ -402,31 +402,58 @@ def rope_plan(inv_freq: torch.Tensor, layout: str = "half", amplitude: float = 1
                     float(amplitude))
 
 
-def _need_rows(t: torch.Tensor, name: str, dtype=None, shape=None) -> None:
-    """As _need, for tensors that may be views: only the last dimension has to be contiguous."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device} but the current device is cuda:{torch.cuda.current_device()}; "
+def _need_on(t: torch.Tensor, name: str, dev: int) -> None:
+    if t.get_device() != dev:
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        raise ValueError(f"{name} is on {t.device} but the current device is cuda:{dev}; "
                          "make the tensors' device current (torch.cuda.device) before the call")
-    if t.dim() != 4 or (t.shape[3] > 1 and t.stride(3) != 1):
-        raise ValueError(f"{name} must have 4 dimensions, the last one contiguous")
-    if dtype is not None and t.dtype != dtype:
+
+
+def _need_rows(t: torch.Tensor, name: str, dev: int, dtype, shape=None) -> Tuple[int, ...]:
+    """As _need, for [B, heads, T, Dh] tensors that may be views: only the last dimension has to be
+    contiguous.  Returns the other three strides."""
+    _need_on(t, name, dev)
+    if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dim() != 4 or (shape is not None and t.shape != shape):
+        raise ValueError(f"{name} must have shape {'[B, heads, T, Dh]' if shape is None else tuple(shape)}, "
+                         f"got {tuple(t.shape)}")
+    st = t.stride()
+    if st[3] != 1 and t.shape[3] > 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+    return st[:3]
+
+
+def _need_dense(t: torch.Tensor, name: str, dev: int, dtype, shape) -> None:
+    _need_on(t, name, dev)
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
+
+
+@functools.lru_cache(maxsize=1024)
+def _strides(*strides):
+    """Strides as the C calls take them (read only, so one array serves every call with the same)."""
+    return (_ll * len(strides))(*strides)
+
+
+def _raw_stream(stream, dev: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
 def _on(stream):
-    """Context in which tensors are allocated for work on `stream` (None: the current one), so that
-    their memory is handed out again only behind that work."""
-    if stream is None:
-        return contextlib.nullcontext()
+    """Context in which tensors are allocated for work on `stream`, so that their memory is handed out
+    again only behind that work."""
     if not isinstance(stream, torch.cuda.Stream):
-        if not int(stream):
-            return torch.cuda.stream(torch.cuda.default_stream())
-        stream = torch.cuda.ExternalStream(int(stream))
+        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
     return torch.cuda.stream(stream)
+
+
+def _new(like: torch.Tensor, shape, dtype, stream) -> torch.Tensor:
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    with _on(stream):
+        return like.new_empty(shape, dtype=dtype)
 
 
 def rope(q: torch.Tensor, plan: RopePlan, k: Optional[torch.Tensor] = None, pos: Optional[torch.Tensor] = None,
@@ -437,45 +464,42 @@ def rope(q: torch.Tensor, plan: RopePlan, k: Optional[torch.Tensor] = None, pos:
     Position of token s: pos[b, s] (int64, [B, S] or [S]), or offset + s.  `out` / `k_out` may be the
     inputs themselves.  inverse=True turns back: the gradient of the inputs from that of the outputs.
     Returns the rotated q, or (q, k)."""
-    if q.dtype not in (torch.bfloat16, torch.float32):
+    dt, dev = q.dtype, torch.cuda.current_device()
+    if dt != torch.bfloat16 and dt != torch.float32:
         raise ValueError("inputs must be bfloat16 or float32")
-    _need_rows(q, "q", q.dtype)
+    q_st = _need_rows(q, "q", dev, dt)
     B, Hq, S, Dh = q.shape
     if plan.rot > Dh:
         raise ValueError(f"the plan rotates {plan.rot} columns, heads have {Dh}")
-    _need(plan.steps, "plan.steps", torch.int64, (plan.rot // 2,))
-    pos_ptr = pos_b = pos_s = 0
+    _need_dense(plan.steps, "plan.steps", dev, torch.int64, (plan.rot // 2,))
+    pos_ptr, pos_b, pos_s = None, 0, 0
     if pos is not None:
-        if not pos.is_cuda or pos.device.index != q.device.index:
-            raise ValueError(f"pos must be on {q.device}")
+        _need_on(pos, "pos", dev)
         if pos.dtype != torch.int64:
             raise ValueError(f"pos must be torch.int64, got {pos.dtype}")
-        if tuple(pos.shape) not in ((S,), (B, S)):
+        if pos.shape == (B, S):
+            pos_b, pos_s = pos.stride()
+        elif pos.shape == (S,):
+            pos_s = pos.stride(0)
+        else:
             raise ValueError(f"pos must have shape {(S,)} or {(B, S)}, got {tuple(pos.shape)}")
-        pos_ptr, pos_s = pos.data_ptr(), pos.stride(-1)
-        pos_b = pos.stride(0) if pos.dim() == 2 else 0
-    k_ptr = k_out_ptr = Hk = 0
-    k_strides = None
+        pos_ptr = pos.data_ptr()
+    if out is None:
+        out = _new(q, (B, Hq, S, Dh), dt, stream)
+    o_st = _need_rows(out, "out", dev, dt, q.shape)
+    k_ptr, k_out_ptr, Hk, k_strides = None, None, 0, None
     if k is not None:
-        _need_rows(k, "k", q.dtype, (B, k.shape[1], S, Dh))
-        Hk = k.shape[1]
+        Hk = k.shape[1] if k.dim() == 4 else 0
+        k_st = _need_rows(k, "k", dev, dt, (B, Hk, S, Dh))
+        if k_out is None:
+            k_out = _new(q, (B, Hk, S, Dh), dt, stream)
+        k_strides = _strides(*k_st, *_need_rows(k_out, "k_out", dev, dt, k.shape))
+        k_ptr, k_out_ptr = k.data_ptr(), k_out.data_ptr()
     elif k_out is not None:
         raise ValueError("k_out without k")
-    with _on(stream):
-        if out is None:
-            out = torch.empty((B, Hq, S, Dh), dtype=q.dtype, device=q.device)
-        if k is not None and k_out is None:
-            k_out = torch.empty((B, Hk, S, Dh), dtype=q.dtype, device=q.device)
-    _need_rows(out, "out", q.dtype, q.shape)
-    strides = (_ll * 6)(*q.stride()[:3], *out.stride()[:3])
-    if k is not None:
-        _need_rows(k_out, "k_out", q.dtype, k.shape)
-        k_strides = (_ll * 6)(*k.stride()[:3], *k_out.stride()[:3])
-        k_ptr, k_out_ptr = k.data_ptr(), k_out.data_ptr()
-    code = _rope(q.data_ptr(), out.data_ptr(), Hq, strides, k_ptr or None, k_out_ptr or None, Hk, k_strides, B, S, Dh,
-                 plan.steps.data_ptr(), plan.rot, 1 if plan.interleaved else 0, plan.amplitude, pos_ptr or None, pos_b,
-                 pos_s, int(offset), 1 if inverse else 0, RA_BF16 if q.dtype == torch.bfloat16 else RA_F32,
-                 _stream(stream))
+    code = _rope(q.data_ptr(), out.data_ptr(), Hq, _strides(*q_st, *o_st), k_ptr, k_out_ptr, Hk, k_strides, B, S, Dh,
+                 plan.steps.data_ptr(), plan.rot, plan.interleaved, plan.amplitude, pos_ptr, pos_b, pos_s, int(offset),
+                 bool(inverse), RA_BF16 if dt == torch.bfloat16 else RA_F32, _raw_stream(stream, dev))
     _check(code, "ring_attn_rope")
     return out if k is None else (out, k_out)
 
@@ -509,12 +533,11 @@ class KVCache:
                                N, M)
         self._ref = ctypes.byref(self._c)
 
-    def _at(self) -> "_CacheStruct":
-        """The C description, for a call on the current device."""
-        if self.k.device.index != torch.cuda.current_device():
-            raise ValueError(f"the cache is on {self.k.device} but the current device is "
-                             f"cuda:{torch.cuda.current_device()}")
-        return self._ref
+    def _at(self) -> int:
+        """The current device, which has to be the cache's."""
+        dev = torch.cuda.current_device()
+        _need_on(self.k, "the cache", dev)
+        return dev
 
 
 def kv_cache(layers: int, pages: int, heads: int, page: int, Dh: int, slots: int, max_pages: int,
@@ -527,54 +550,56 @@ def kv_cache(layers: int, pages: int, heads: int, page: int, Dh: int, slots: int
     return KVCache(*codes, *scales, z(slots, max_pages) - 1, z(slots), z(pages))
 
 
-def _batch(t: torch.Tensor, name: str, cache: KVCache, shape=None) -> int:
-    if t.dim() != 1 or t.dtype != torch.int32 or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int32 tensor of one dimension")
-    if t.device != cache.k.device:
-        raise ValueError(f"{name} is on {t.device}, the cache on {cache.k.device}")
-    if shape is not None and t.shape[0] != shape:
-        raise ValueError(f"{name} must have {shape} entries, got {t.shape[0]}")
+def _batch(t: torch.Tensor, name: str, dev: int, B: int) -> int:
+    _need_on(t, name, dev)
+    if t.dtype != torch.int32 or t.shape != (B,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor of {B} entries, got {t.dtype} {tuple(t.shape)}")
     return t.data_ptr()
-
-
-def _pages_workspace(cache: KVCache, B: int, workspace, stream):
-    need = int(_cache_pages_ws(B, cache._c.pages))
-    if workspace is None:
-        with _on(stream):
-            workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=cache.k.device)
-    _need(workspace, "workspace")
-    return workspace, workspace.numel() * workspace.element_size()
 
 
 def cache_pages_workspace_bytes(B: int, pages: int) -> int:
     return int(_cache_pages_ws(B, pages))
 
 
+@functools.lru_cache(maxsize=1024)
+def cache_attend_workspace_bytes(T: int, Hq: int, Hkv: int, Dh: int) -> int:
+    return int(_cache_attend_ws(T, Hq, Hkv, Dh))
+
+
+def _workspace(workspace, need: int, like: torch.Tensor, dev: int, stream):
+    if workspace is None:
+        workspace = _new(like, (max(need, 1),), torch.uint8, stream)
+        return workspace, need
+    _need_on(workspace, "workspace", dev)
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
 def cache_reserve(cache: KVCache, slots: torch.Tensor, n_new: torch.Tensor, workspace: Optional[torch.Tensor] = None,
                   stream=None) -> None:
     """Room for n_new[b] more tokens of slots[b] (int32, on the device), once for all layers; lens grow
     (ring_attn_cache_reserve).  Too few pages, or a slot out of range: device_status()."""
-    ref = cache._at()
-    B = slots.shape[0]
-    s, n = _batch(slots, "slots", cache), _batch(n_new, "n_new", cache, B)
-    ws, size = _pages_workspace(cache, B, workspace, stream)
-    _check(_cache_reserve(ref, s, n, B, ws.data_ptr(), size, _stream(stream)), "ring_attn_cache_reserve")
+    dev, B = cache._at(), slots.shape[0]
+    s, n = _batch(slots, "slots", dev, B), _batch(n_new, "n_new", dev, B)
+    ws, size = _workspace(workspace, cache_pages_workspace_bytes(B, cache._c.pages), cache.k, dev, stream)
+    _check(_cache_reserve(cache._ref, s, n, B, ws.data_ptr(), size, _raw_stream(stream, dev)), "ring_attn_cache_reserve")
 
 
 def cache_append(cache: KVCache, layer: int, slots: torch.Tensor, n_new: Optional[torch.Tensor], k: torch.Tensor,
                  v: torch.Tensor, stream=None) -> None:
     """Writes the last n_new[b] tokens (None: T) of slots[b] into one layer: k, v [B, heads, T, Dh] bf16,
     views with a contiguous last dimension included (ring_attn_cache_append)."""
-    ref = cache._at()
+    dev = cache._at()
+    k_st = _need_rows(k, "k", dev, torch.bfloat16)
+    v_st = _need_rows(v, "v", dev, torch.bfloat16, k.shape)
     B, H, T, Dh = k.shape
     if H != cache._c.heads or Dh != cache._c.head_dim:
         raise ValueError(f"k must be [B, {cache._c.heads}, T, {cache._c.head_dim}], got {tuple(k.shape)}")
-    _need_rows(k, "k", torch.bfloat16)
-    _need_rows(v, "v", torch.bfloat16, k.shape)
-    s = _batch(slots, "slots", cache, B)
-    n = None if n_new is None else _batch(n_new, "n_new", cache, B)
-    code = _cache_append(ref, layer, s, n, B, T, k.data_ptr(), (_ll * 3)(*k.stride()[:3]), v.data_ptr(),
-                         (_ll * 3)(*v.stride()[:3]), _stream(stream))
+    s = _batch(slots, "slots", dev, B)
+    n = None if n_new is None else _batch(n_new, "n_new", dev, B)
+    code = _cache_append(cache._ref, layer, s, n, B, T, k.data_ptr(), _strides(*k_st), v.data_ptr(), _strides(*v_st),
+                         _raw_stream(stream, dev))
     _check(code, "ring_attn_cache_append")
 
 
@@ -583,23 +608,19 @@ def cache_read(cache: KVCache, layer: int, slots: torch.Tensor, length: int, sta
                stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """One layer's keys and values, exact in bf16, [B, heads, length, Dh]: positions start[b] (None: 0) ..
     of slots[b], zero where the sequence holds none (ring_attn_cache_read)."""
-    ref = cache._at()
-    B = slots.shape[0]
-    s = _batch(slots, "slots", cache)
-    at = None if start is None else _batch(start, "start", cache, B)
+    dev, B = cache._at(), slots.shape[0]
+    s = _batch(slots, "slots", dev, B)
+    at = None if start is None else _batch(start, "start", dev, B)
     shape = (B, cache._c.heads, length, cache._c.head_dim)
-    with _on(stream):
-        k = torch.empty(shape, dtype=torch.bfloat16, device=cache.k.device) if k is None else k
-        v = torch.empty(shape, dtype=torch.bfloat16, device=cache.k.device) if v is None else v
-    _need(k, "k", torch.bfloat16, shape)
-    _need(v, "v", torch.bfloat16, shape)
-    _check(_cache_read(ref, layer, s, at, B, length, k.data_ptr(), v.data_ptr(), _stream(stream)),
+    if k is None:
+        k = _new(cache.k, shape, torch.bfloat16, stream)
+    if v is None:
+        v = _new(cache.k, shape, torch.bfloat16, stream)
+    _need_dense(k, "k", dev, torch.bfloat16, shape)
+    _need_dense(v, "v", dev, torch.bfloat16, shape)
+    _check(_cache_read(cache._ref, layer, s, at, B, length, k.data_ptr(), v.data_ptr(), _raw_stream(stream, dev)),
            "ring_attn_cache_read")
     return k, v
-
-
-def cache_attend_workspace_bytes(T: int, Hq: int, Hkv: int, Dh: int) -> int:
-    return int(_cache_attend_ws(T, Hq, Hkv, Dh))
 
 
 def cache_attend(cache: KVCache, layer: int, slots: torch.Tensor, n_new: Optional[torch.Tensor], q: torch.Tensor,
@@ -610,28 +631,28 @@ def cache_attend(cache: KVCache, layer: int, slots: torch.Tensor, n_new: Optiona
     (ring_attn_cache_attend): q [B, Hq, T, Dh] bf16, views with a contiguous last dimension included, Hq a
     multiple of the cache's heads.  Returns (o [B, Hq, T, Dh] bf16 or float32, lse [B, Hq, T] float32) as
     fwd() does; a float32 o is one part for merge()."""
-    ref = cache._at()
-    _need_rows(q, "q", torch.bfloat16)
+    dev = cache._at()
+    q_st = _need_rows(q, "q", dev, torch.bfloat16)
     B, Hq, T, Dh = q.shape
-    if Dh != cache._c.head_dim or Hq % cache._c.heads:
-        raise ValueError(f"q must be [B, a multiple of {cache._c.heads}, T, {cache._c.head_dim}], got {tuple(q.shape)}")
-    if out_dtype not in (torch.bfloat16, torch.float32):
+    heads = cache._c.heads
+    if Dh != cache._c.head_dim or Hq % heads:
+        raise ValueError(f"q must be [B, a multiple of {heads}, T, {cache._c.head_dim}], got {tuple(q.shape)}")
+    if out_dtype != torch.bfloat16 and out_dtype != torch.float32:
         raise ValueError("out_dtype must be bfloat16 or float32")
-    s = _batch(slots, "slots", cache, B)
-    n = None if n_new is None else _batch(n_new, "n_new", cache, B)
-    with _on(stream):
-        if workspace is None:
-            workspace = torch.empty(max(cache_attend_workspace_bytes(T, Hq, cache._c.heads, Dh), 1), dtype=torch.uint8,
-                                    device=q.device)
-        out = torch.empty((B, Hq, T, Dh), dtype=out_dtype, device=q.device) if out is None else out
-        lse = torch.empty((B, Hq, T), dtype=torch.float32, device=q.device) if lse is None else lse
-    _need(workspace, "workspace")
-    _need(out, "out", out_dtype, (B, Hq, T, Dh))
-    _need(lse, "lse", torch.float32, (B, Hq, T))
-    code = _cache_attend(ref, layer, s, n, B, T, Hq, q.data_ptr(), (_ll * 3)(*q.stride()[:3]),
-                         float(scale) if scale else 0.0, 1 if causal else 0, out.data_ptr(),
-                         RA_BF16 if out_dtype == torch.bfloat16 else RA_F32, lse.data_ptr(), workspace.data_ptr(),
-                         workspace.numel() * workspace.element_size(), _stream(stream))
+    s = _batch(slots, "slots", dev, B)
+    n = None if n_new is None else _batch(n_new, "n_new", dev, B)
+    ws, size = _workspace(workspace, cache_attend_workspace_bytes(T, Hq, heads, Dh), q, dev, stream)
+    if out is None:
+        out = _new(q, (B, Hq, T, Dh), out_dtype, stream)
+    else:
+        _need_dense(out, "out", dev, out_dtype, (B, Hq, T, Dh))
+    if lse is None:
+        lse = _new(q, (B, Hq, T), torch.float32, stream)
+    else:
+        _need_dense(lse, "lse", dev, torch.float32, (B, Hq, T))
+    code = _cache_attend(cache._ref, layer, s, n, B, T, Hq, q.data_ptr(), _strides(*q_st), float(scale) if scale else 0.0,
+                         bool(causal), out.data_ptr(), RA_BF16 if out_dtype == torch.bfloat16 else RA_F32,
+                         lse.data_ptr(), ws.data_ptr(), size, _raw_stream(stream, dev))
     _check(code, "ring_attn_cache_attend")
     return out, lse
 
@@ -640,21 +661,19 @@ def cache_fork(cache: KVCache, src: torch.Tensor, dst: torch.Tensor, workspace: 
                stream=None) -> None:
     """The empty slots dst[b] share the pages of src[b] from here on (ring_attn_cache_fork); a page that
     both hold is copied when cache_reserve() makes room in it."""
-    ref = cache._at()
-    B = src.shape[0]
-    a, d = _batch(src, "src", cache), _batch(dst, "dst", cache, B)
-    ws, size = _pages_workspace(cache, B, workspace, stream)
-    _check(_cache_fork(ref, a, d, B, ws.data_ptr(), size, _stream(stream)), "ring_attn_cache_fork")
+    dev, B = cache._at(), src.shape[0]
+    a, d = _batch(src, "src", dev, B), _batch(dst, "dst", dev, B)
+    ws, size = _workspace(workspace, cache_pages_workspace_bytes(B, cache._c.pages), cache.k, dev, stream)
+    _check(_cache_fork(cache._ref, a, d, B, ws.data_ptr(), size, _raw_stream(stream, dev)), "ring_attn_cache_fork")
 
 
 def cache_trim(cache: KVCache, slots: torch.Tensor, keep: Optional[torch.Tensor] = None, stream=None) -> None:
     """Keeps the first keep[b] tokens of slots[b] (None: 0, the sequence is freed) and gives up the pages
     behind them (ring_attn_cache_trim)."""
-    ref = cache._at()
-    B = slots.shape[0]
-    s = _batch(slots, "slots", cache)
-    n = None if keep is None else _batch(keep, "keep", cache, B)
-    _check(_cache_trim(ref, s, n, B, _stream(stream)), "ring_attn_cache_trim")
+    dev, B = cache._at(), slots.shape[0]
+    s = _batch(slots, "slots", dev, B)
+    n = None if keep is None else _batch(keep, "keep", dev, B)
+    _check(_cache_trim(cache._ref, s, n, B, _raw_stream(stream, dev)), "ring_attn_cache_trim")
 
 
 def cache_free(cache: KVCache, slots: torch.Tensor, stream=None) -> None:
@@ -664,10 +683,9 @@ def cache_free(cache: KVCache, slots: torch.Tensor, stream=None) -> None:
 
 def cache_compact(cache: KVCache, workspace: Optional[torch.Tensor] = None, stream=None) -> None:
     """Moves the pages in use to the lowest page numbers, all layers (ring_attn_cache_compact)."""
-    ref = cache._at()
-    ws, size = _pages_workspace(cache, 0, workspace, stream)
-    _check(_cache_compact(ref, ws.data_ptr(), size, _stream(stream)), "ring_attn_cache_compact")
-
+    dev = cache._at()
+    ws, size = _workspace(workspace, cache_pages_workspace_bytes(0, cache._c.pages), cache.k, dev, stream)
+    _check(_cache_compact(cache._ref, ws.data_ptr(), size, _raw_stream(stream, dev)), "ring_attn_cache_compact")
 
 
 def bwd_noalloc_max_bytes() -> int:
