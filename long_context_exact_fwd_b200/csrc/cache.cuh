@@ -68,5 +68,15 @@ __device__ __forceinline__ bool named_before(const int* slots, int b, int slot) 
   return __syncthreads_or(dup) != 0;
 }
 
+// The last i in [0, n) with first[i] <= x (first[] is a prefix sum, first[0] = 0).
+__device__ __forceinline__ int find_row(const int* first, int n, int x) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (first[mid] <= x) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
 }  // namespace cache
 }  // namespace ra

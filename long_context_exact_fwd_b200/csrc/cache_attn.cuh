@@ -565,26 +565,25 @@ __global__ void __launch_bounds__(AT_THREADS, AT_PER_SM) attend_kernel(const Att
   if (threadIdx.x == 0) p.split[blockIdx.x] = mine_split;
 }
 
-// Joins the parts of the segments that attend_kernel left split: block (c, j) rows 8 j .. 8 j + 7 of the
-// segment that starts in its block c, JOIN_WARPS warps a row, each lane 4 columns of every
-// JOIN_WARPS-th part.  Parts are added in an order that only the lengths fix.  Bound: latency of
+// Joins the parts of the segments that the kernel before left split: block (c, j) has the j-th lot of
+// 32 / WARPS rows of the segment that starts in its block c, WARPS warps a row, each lane 4 columns of
+// every WARPS-th part.  Parts are added in an order that only the lengths fix.  Bound: latency of
 // three dependent reads; one block alone doing this at the end of its stretch cost 0.6 us per part.
-constexpr int JOIN_WARPS = 4;
-constexpr int JOIN_THREADS = 8 * JOIN_WARPS * 32;
+constexpr int JOIN_THREADS = 1024;
 
-template <int HD, int NT>
-__global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const AttendParams p) {
-  constexpr int ROWS = 8 * NT, GROUPS = HD / 4;
-  __shared__ float4 s_o[8][JOIN_WARPS][GROUPS];
-  __shared__ float2 s_ml[8][JOIN_WARPS];
+template <int HD, int ROWS, int WARPS>
+__global__ void __launch_bounds__(JOIN_THREADS, 1) join_kernel(const AttendParams p) {
+  constexpr int GROUPS = HD / 4, LOT = 32 / WARPS;
+  __shared__ float4 s_o[LOT][WARPS][GROUPS];
+  __shared__ float2 s_ml[LOT][WARPS];
   asm volatile("griddepcontrol.wait;" ::: "memory");   // the parts are complete
   const int c0 = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int4 d = p.split[c0];
   if (d.x < 0) return;
   const int c1 = d.x, b = d.y, h = d.z;
   const int row0 = d.w * ROWS, rows = min(ROWS, (p.n_new ? p.n_new[b] : p.T) * p.g - row0);
-  const int rr = warp / JOIN_WARPS, w = warp % JOIN_WARPS;
-  const int r = blockIdx.y * 8 + rr;
+  const int rr = warp / WARPS, w = warp % WARPS;
+  const int r = blockIdx.y * LOT + rr;
   const long long step = 2ll * ROWS * (HD + 4);
   // part of block c0: its second place; of a block behind it: the first
   const float* second = p.part + (2ll * c0 + 1) * ROWS * (HD + 4) + r * (HD + 4);
@@ -593,8 +592,8 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const AttendParams p
   const int n = c1 - c0 + 1;
   float m = -INFINITY, z = 0.f;
   float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int k0 = w; k0 < n; k0 += 32 * JOIN_WARPS) {   // 32 parts of this warp at a time, one per lane
-    const int k = k0 + lane * JOIN_WARPS;
+  for (int k0 = w; k0 < n; k0 += 32 * WARPS) {   // 32 parts of this warp at a time, one per lane
+    const int k = k0 + lane * WARPS;
     const float2 ml = k < n ? *reinterpret_cast<const float2*>(part(k) + HD) : make_float2(-INFINITY, 0.f);
     float mk = ml.x;
 #pragma unroll
@@ -610,12 +609,12 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const AttendParams p
 #pragma unroll
     for (int i = 16; i; i >>= 1) zs += __shfl_xor_sync(0xffffffffu, zs, i);
     z += zs;
-    const int here = min(32, (n - k0 + JOIN_WARPS - 1) / JOIN_WARPS);
+    const int here = min(32, (n - k0 + WARPS - 1) / WARPS);
 #pragma unroll 8
     for (int j = 0; j < here; ++j) {
       const float fj = __shfl_sync(0xffffffffu, f, j);
       if (lane < GROUPS && (seen >> j & 1u)) {
-        const float4 y = *reinterpret_cast<const float4*>(part(k0 + j * JOIN_WARPS) + 4 * lane);
+        const float4 y = *reinterpret_cast<const float4*>(part(k0 + j * WARPS) + 4 * lane);
         a = make_float4(fmaf(y.x, fj, a.x), fmaf(y.y, fj, a.y), fmaf(y.z, fj, a.z), fmaf(y.w, fj, a.w));
       }
     }
@@ -626,11 +625,11 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const AttendParams p
   if (w || lane >= GROUPS || r >= rows) return;
   m = -INFINITY;
 #pragma unroll
-  for (int i = 0; i < JOIN_WARPS; ++i) m = fmaxf(m, s_ml[rr][i].x);
+  for (int i = 0; i < WARPS; ++i) m = fmaxf(m, s_ml[rr][i].x);
   z = 0.f;
   a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-  for (int i = 0; i < JOIN_WARPS; ++i) {
+  for (int i = 0; i < WARPS; ++i) {
     const float2 ml = s_ml[rr][i];
     if (ml.y == 0.f) continue;
     const float f = ml.x == m ? 1.f : ex2_approx(ml.x - m);

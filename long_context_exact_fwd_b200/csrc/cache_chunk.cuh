@@ -1,0 +1,733 @@
+// Attention of many new queries per sequence (a chunk of a prompt) over the 8-bit paged cache.
+//
+// Same result as attend_kernel (cache_attn.cuh), for row counts where the products bound: both run
+// on tcgen05 with accumulators in tensor memory, as in fwd_kernel (fwd_sm100.cuh), whose issue order
+// and softmax this keeps:
+//   O0 += P0(j-1) V(j-1);  S0 = Q0 K(j)^T;  O1 += P1(j-1) V(j-1);  S1 = Q1 K(j)^T.
+// An item is 256 rows of one kv head (row = t * g + head): two 128-row tiles.  Roles of the 12 warps:
+//   0-3, 4-7  softmax of tile 0 and 1 (thread = row = TMEM lane),
+//   8         tensor memory and the MMA issue (one thread),
+//   9-11      converters: Q rows to fp16; codes, brought by bulk copies into the upper half of a stage,
+//             to fp16 tiles over the whole of it (read to registers, a barrier of the three, written).
+// The operands are fp16: codes are exact in it (one conversion instruction per two; as bf16 the
+// scale would have to be multiplied in), a query row is scaled to its range by a power of two.
+// The scales never touch the tiles: a page's key scale multiplies its 16-column groups of scores, and
+// its value scale, a power of two, is added to the exponent of P relative to the largest so far:
+//   w_j = 2^(x_j - ref + dv_j + 7),   l += 2^-(dv_j + 7) w_j,   dv_j = e_j - e_max <= 0.
+// Work is cut as in attend_kernel: one line of 128-key tiles over all items, equal stretches, parts
+// joined by join_kernel.
+#pragma once
+#include "cache_attn.cuh"
+
+namespace ra {
+namespace cache {
+
+constexpr int CH_BM = 128, CH_BN = 128, CH_ROWS = 256, CH_STAGES = 4;
+constexpr int CH_THREADS = 384;
+constexpr int CH_WARP_MMA = 8, CH_CONV_WARPS = 3;
+constexpr uint32_t CH_REGS_LAUNCH = 168, CH_REGS_SOFTMAX = 200, CH_REGS_OTHER = 104;
+static_assert(2 * (CH_REGS_SOFTMAX - CH_REGS_LAUNCH) <= CH_REGS_LAUNCH - CH_REGS_OTHER, "register split exceeds the pool");
+constexpr int CH_MAX_CTAS = 160;      // blocks that the workspace has room for (one per SM)
+constexpr int CH_START = 3;          // what starting and ending an item costs, in tiles
+constexpr int CH_LEAST = 4;          // tiles of a stretch, at least
+constexpr int CH_P_LOG2 = 7;         // P is held at 2^7 times its value
+constexpr float CH_DV_MIN = -100.f;  // below, P's fp16 is 0 whatever follows
+
+// Scale constants of one key tile: groups of 16 keys.
+struct alignas(16) ChScales {
+  float k[8];        // key scale
+  float add[8];      // dv + 7
+  float fac[8];      // 2^-(dv + 7)
+  float rescale;     // what O has to be multiplied by for the new e_max (1: nothing)
+  float unit;        // 2^(e_max - 7): true value of O's unit
+  float pad[2];
+};
+
+template <int HD>
+struct ChLayout {
+  static constexpr int SUB = HD / 64;
+  static constexpr int SUB_BYTES = 128 * 128;
+  static constexpr int TILE_BYTES = SUB * SUB_BYTES;
+  static constexpr int Q_OFF = 0;
+  static constexpr int KV_OFF = 2 * TILE_BYTES;
+  static constexpr int BAR_OFF = KV_OFF + CH_STAGES * TILE_BYTES;
+  static constexpr int B_Q_FULL = 0, B_Q_EMPTY = 1, B_KV_FULL = 2, B_KV_EMPTY = B_KV_FULL + CH_STAGES,
+                       B_RAW = B_KV_EMPTY + CH_STAGES, B_S_FULL = B_RAW + CH_STAGES, B_P_READY = B_S_FULL + 2, B_O_FINAL = B_P_READY + 2,
+                       B_DRAIN = B_O_FINAL + 2, NUM_BARS = B_DRAIN + 1;
+  static constexpr int MISC_OFF = BAR_OFF + NUM_BARS * 8;        // TMEM base, abort flag
+  static constexpr int SCALE_OFF = (MISC_OFF + 8 + 15) / 16 * 16;
+  static constexpr int QSCALE_OFF = SCALE_OFF + 4 * sizeof(ChScales);   // [3][256] floats
+  static constexpr int NAN_OFF = QSCALE_OFF + 3 * CH_ROWS * 4;          // [3][8 warps][HD + 4] ints, HD a flag
+  static constexpr int BATCH_OFF = NAN_OFF + 3 * 8 * (HD + 4) * 4;      // prefix [B + 1], slot, len, n [B]
+  static int bytes(int B) { return BATCH_OFF + (4 * B + 1) * 4 + 1024; }
+  __host__ __device__ static constexpr uint32_t s_col(int t) { return 128u * t; }
+  __host__ __device__ static constexpr uint32_t o_col(int t) { return 256u + uint32_t(HD) * t; }
+};
+
+// fp16 x fp16 -> fp32 (formats 0), otherwise as idesc_bf16_f32.
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, int a_mn_major, int b_mn_major) {
+  return (1u << 4) | (uint32_t(a_mn_major) << 15) | (uint32_t(b_mn_major) << 16) | (uint32_t(N >> 3) << 17) |
+         (uint32_t(M >> 4) << 24);
+}
+
+// The line of work as every role walks it: items (b, h, i) in order, each CH_START places and then
+// its key tiles; a block has places [line0, line1).
+struct ChWalk {
+  const AttendParams* p;
+  const int* batch;            // shared memory: prefix [B + 1], slots, lengths, new tokens [B]
+  int b, h, i;                 // the current item
+  int first;                   // place of its first tile
+  int x, line1;
+  int nt, t0, t1;              // its tiles, and this block's [t0, t1)
+
+  __device__ __forceinline__ int slot() const { return batch[p->B + 1 + b]; }
+  __device__ __forceinline__ int len() const { return batch[2 * p->B + 1 + b]; }
+  __device__ __forceinline__ int n() const { return batch[3 * p->B + 1 + b]; }
+  // keys that row r (of the sequence) sees
+  __device__ __forceinline__ int limit(int r) const {
+    const int l = len();
+    return p->causal ? max(0, min(l, l - n() + r / p->g + 1)) : l;
+  }
+  __device__ __forceinline__ static int tiles(int len, int n, int g, int causal, int i) {
+    const int last = min((i + 1) * CH_ROWS, n * g) - 1;
+    const int lim = causal ? max(0, min(len, len - n + last / g + 1)) : len;
+    return max(1, (lim + CH_BN - 1) / CH_BN);
+  }
+  __device__ __forceinline__ void here() {
+    nt = tiles(len(), n(), p->g, p->causal, i);
+    t0 = max(0, x - first);
+    t1 = min(nt, line1 - first);
+  }
+  // Goes on to this block's next piece (the first call: the one it stands on); false at the end.
+  __device__ __forceinline__ bool next(bool begin) {
+    if (!begin) step();
+    for (;;) {
+      if (x >= line1) return false;
+      here();
+      if (t0 < t1) return true;
+      step();
+    }
+  }
+  __device__ __forceinline__ void step() {
+    x = first + nt;
+    first = x + CH_START;
+    if (++i * CH_ROWS >= n() * p->g) {
+      i = 0;
+      if (++h == p->c.heads) {
+        h = 0;
+        do ++b;
+        while (b < p->B && n() == 0);
+        if (b == p->B) x = line1;   // behind the last item
+      }
+    }
+  }
+};
+
+// ------------------------------------------------------------------ converters (3 warps)
+template <int HD>
+__device__ void ch_convert(const AttendParams& p, ChWalk w, uint8_t* smem, uint32_t sbase, volatile int* abort_flag) {
+  using L = ChLayout<HD>;
+  const Pool& c = p.c;
+  const int lane = threadIdx.x & 31, cw = (threadIdx.x >> 5) - (CH_WARP_MMA + 1);
+  const uint32_t bars = sbase + L::BAR_OFF;
+  auto bar = [&](int i) { return bars + 8u * i; };
+  // A tile is 16 * SUB groups of 8 tokens x 64 columns, 16 codes a lane; a warp has every third.
+  constexpr int GROUPS = 16 * L::SUB, PER = (GROUPS + CH_CONV_WARPS - 1) / CH_CONV_WARPS;
+  constexpr uint32_t LOT = 16 * HD;                      // bytes of 16 tokens' codes
+  int stage = 0, scale_slot = 0, piece = 0;
+  uint32_t phase = 0, q_phase = 0;
+  ChScales* scales = reinterpret_cast<ChScales*>(smem + L::SCALE_OFF);
+  for (bool go = w.next(true); go; go = w.next(false), piece = piece == 2 ? 0 : piece + 1) {
+    const int slot = w.slot(), len = w.len(), h = w.h;
+    const int row0 = w.i * CH_ROWS, rows = min(CH_ROWS, w.n() * p.g - row0);
+    const int* table = c.table + static_cast<long long>(slot) * c.max_pages;
+    const int lim_min = w.limit(row0), lim_max = w.limit(row0 + rows - 1);
+    // page of each 16-token lot of a tile, in lanes 0-7 (and again in 8-15 ..), -1: none
+    auto look_up = [&](int tile) {
+      const int tok = tile * CH_BN + (lane & 7) * 16;
+      int pid = -1;
+      if (tok < len) {
+        pid = table[tok >> p.page_shift];
+        if (pid < 0 || pid >= c.pages) {
+          record_status(RA_ERR_PAGES);
+          pid = -1;
+        }
+      }
+      return pid;
+    };
+    // The codes of one tile's keys or values on their way into the upper half of stage `st`, a bulk
+    // copy per lot (first warp).  The stage has to be empty.
+    auto fetch = [&](int pids, int tile, int kv, int st) {
+      const unsigned there = __ballot_sync(0xffffffffu, pids >= 0) & 0xffu;
+      if (lane == 0) mbar_arrive_expect_tx(bar(L::B_RAW + st), __popc(there) * LOT);
+      __syncwarp();
+      if (lane < 8 && pids >= 0)
+        bulk_load(sbase + L::KV_OFF + st * L::TILE_BYTES + L::TILE_BYTES / 2 + lane * LOT,
+                  (kv ? c.v : c.k) + ((static_cast<long long>(pids) * c.heads + h) * c.page +
+                                      ((tile * CH_BN + lane * 16) & (c.page - 1))) * HD,
+                  LOT, bar(L::B_RAW + st));
+    };
+    int pid = look_up(w.t0);
+
+    // ---- Q: 16 (HD 128) or 8 lanes a row, 8 elements a lane
+    if (!named_bar_and(1, CH_CONV_WARPS * 32, mbar_wait(bar(L::B_Q_EMPTY), q_phase ^ 1u, abort_flag))) return;
+    {
+      constexpr int LANES = HD / 8, AT_ONCE = 32 / LANES;   // rows per warp step
+      const int col = lane % LANES, sub_row = lane / LANES;
+      float* q_scale = reinterpret_cast<float*>(smem + L::QSCALE_OFF) + piece * CH_ROWS;
+#pragma unroll 2
+      for (int r0 = cw * AT_ONCE; r0 < CH_ROWS; r0 += CH_CONV_WARPS * AT_ONCE) {
+        const int r = r0 + sub_row;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (r < rows) {
+          const int row = row0 + r, t = row / p.g, hq = h * p.g + row - t * p.g;
+          v = *reinterpret_cast<const uint4*>(p.q + w.b * p.qb + hq * p.qh + t * p.qt + col * 8);
+        }
+        const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+        float amax = 0.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float lo = fabsf(__uint_as_float(in[k] << 16)), hi = fabsf(__uint_as_float(in[k] & 0xffff0000u));
+          amax = fmaxf(amax, fmaxf(lo <= 3.4028234663852886e38f ? lo : 0.f, hi <= 3.4028234663852886e38f ? hi : 0.f));
+        }
+#pragma unroll
+        for (int d = LANES / 2; d; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
+        const int up = amax > 0.f ? min(max(14 - exponent_of(amax), -113), 126) : 0;   // amax -> [2^14, 2^15)
+        const float f = two_to(up);
+        uint32_t out[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          out[k] = pack_half2(__uint_as_float(in[k] << 16) * f, __uint_as_float(in[k] & 0xffff0000u) * f);
+        const int tile = r >> 7, rr = r & 127;
+        *reinterpret_cast<uint4*>(smem + L::Q_OFF + tile * L::TILE_BYTES + (col >> 3) * L::SUB_BYTES + rr * 128 +
+                                  (((col & 7) ^ (rr & 7)) << 4)) = make_uint4(out[0], out[1], out[2], out[3]);
+        if (col == 0) q_scale[r] = p.scale_log2 * two_to(-up);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(L::B_Q_FULL));
+      q_phase ^= 1u;
+    }
+
+    // ---- K and V tiles: while one is converted, the next one's codes are on their way
+    const int sub_tok = lane >> 2, c4 = lane & 3;
+    auto scales_of = [&](int pids, float& k1, float& v1) {   // none: no key of the lot is seen
+      k1 = 1.f;
+      v1 = 0.f;
+      if (cw == 0 && pids >= 0) {
+        k1 = c.k_scale[static_cast<long long>(pids) * c.heads + h];
+        v1 = c.v_scale[static_cast<long long>(pids) * c.heads + h];
+      }
+    };
+    float sk, sv;
+    scales_of(pid, sk, sv);
+    bool ok = true;
+    if (cw == 0) {
+      ok = __all_sync(0xffffffffu, mbar_wait(bar(L::B_KV_EMPTY + stage), phase ^ 1u, abort_flag));
+      if (ok) fetch(pid, w.t0, 0, stage);
+    }
+    float v_max = 0.f;                                   // largest value scale so far
+    for (int tile = w.t0; tile < w.t1; ++tile) {
+      const int tok0 = tile * CH_BN;
+      const bool more = tile + 1 < w.t1;
+      const int pid_next = more ? look_up(tile + 1) : -1;
+      const bool diagonal = lim_max > lim_min && tok0 + CH_BN > lim_min;
+      const unsigned lots = __ballot_sync(0xffffffffu, pid >= 0) & 0xffu;
+#pragma unroll 1
+      for (int kv = 0; kv < 2; ++kv) {
+        const int next_stage = stage + 1 == CH_STAGES ? 0 : stage + 1;
+        const uint32_t next_phase = next_stage ? phase : phase ^ 1u;
+        bool fetched = false;
+        if (cw == 0 && ok && (kv == 0 || more)) {
+          ok = __all_sync(0xffffffffu, mbar_wait(bar(L::B_KV_EMPTY + next_stage), next_phase ^ 1u, abort_flag));
+          if (ok) fetch(kv ? pid_next : pid, kv ? tile + 1 : tile, kv ^ 1, next_stage);
+          fetched = ok;
+        }
+        ok = ok && mbar_wait(bar(L::B_RAW + stage), phase, abort_flag);
+        if (kv == 0 && cw == 0) {                        // this tile's scale constants
+          float top = sv;
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+          const float all = fmaxf(v_max, top);
+          ChScales* s = scales + scale_slot;
+          if (lane < 8) {
+            const float dv = sv > 0.f ? fmaxf(static_cast<float>(exponent_of(sv) - exponent_of(all)), CH_DV_MIN) : CH_DV_MIN;
+            s->k[lane] = sk;
+            s->add[lane] = dv + CH_P_LOG2;
+            s->fac[lane] = two_to(-static_cast<int>(dv) - CH_P_LOG2);
+          }
+          if (lane == 0) {
+            s->rescale = all > v_max ? (v_max > 0.f ? v_max / all : 0.f) : 1.f;
+            s->unit = all > 0.f ? two_to(max(exponent_of(all) - CH_P_LOG2, -126)) : 0.f;
+          }
+          v_max = all;
+          if (more) scales_of(pid_next, sk, sv);
+        }
+        uint8_t* stage_at = smem + L::KV_OFF + stage * L::TILE_BYTES;
+        const uint8_t* raw = stage_at + L::TILE_BYTES / 2 + sub_tok * HD + c4 * 16;
+        uint4 x[PER];
+        bool odd = false;
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
+          const int group = cw + CH_CONV_WARPS * k, t8 = group & 15;   // the same in the whole warp
+          x[k] = make_uint4(0, 0, 0, 0);
+          if (group < GROUPS && (lots >> (t8 >> 1) & 1u) && tok0 + t8 * 8 + sub_tok < len)
+            x[k] = *reinterpret_cast<const uint4*>(raw + t8 * 8 * HD + (group >> 4) * 64);
+          if (kv && diagonal) odd |= has_nan_code(x[k].x) | has_nan_code(x[k].y) | has_nan_code(x[k].z) | has_nan_code(x[k].w);
+        }
+        // everyone has the codes (or everyone gives up): the tile may be written over them
+        if (!named_bar_and(1, CH_CONV_WARPS * 32, ok)) {
+          if (cw == 0) {                                 // copies under way land before the block can end
+            drain_wait(bar(L::B_RAW + stage), phase);
+            if (fetched) drain_wait(bar(L::B_RAW + next_stage), next_phase);
+          }
+          return;
+        }
+        uint8_t* dst = stage_at + sub_tok * 128;
+        // rows 8 apart share their place in the swizzle: token t's is t & 7 = sub_tok
+        const int at0 = ((2 * c4) ^ sub_tok) << 4, at1 = ((2 * c4 + 1) ^ sub_tok) << 4;
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
+          const int group = cw + CH_CONV_WARPS * k;
+          if (group < GROUPS) {
+            uint8_t* row = dst + (group >> 4) * L::SUB_BYTES + (group & 15) * 1024;
+            *reinterpret_cast<uint4*>(row + at0) =
+                make_uint4(codes_to_half2(static_cast<uint16_t>(x[k].x)), codes_to_half2(static_cast<uint16_t>(x[k].x >> 16)),
+                           codes_to_half2(static_cast<uint16_t>(x[k].y)), codes_to_half2(static_cast<uint16_t>(x[k].y >> 16)));
+            *reinterpret_cast<uint4*>(row + at1) =
+                make_uint4(codes_to_half2(static_cast<uint16_t>(x[k].z)), codes_to_half2(static_cast<uint16_t>(x[k].z >> 16)),
+                           codes_to_half2(static_cast<uint16_t>(x[k].w)), codes_to_half2(static_cast<uint16_t>(x[k].w >> 16)));
+          }
+        }
+        // A NaN among values that some rows of the item do not see must not reach them through 0 * NaN:
+        // it becomes 0 in the tile, and is put back into the rows that see it at the end.
+        if (odd) {
+#pragma unroll 1
+          for (int k = 0; k < PER; ++k) {
+            const int group = cw + CH_CONV_WARPS * k;
+            const int t = tok0 + (group & 15) * 8 + sub_tok;
+            if (group >= GROUPS || t >= len) continue;
+            const int pg = table[t >> p.page_shift];
+            if (pg < 0 || pg >= c.pages) continue;
+            const uint8_t* codes = c.v + ((static_cast<long long>(pg) * c.heads + h) * c.page + (t & (c.page - 1))) * HD +
+                                   (group >> 4) * 64 + c4 * 16;
+#pragma unroll 1
+            for (int z = 0; z < 16; ++z) {
+              if ((codes[z] & 0x7fu) != 0x7fu) continue;
+              *reinterpret_cast<uint16_t*>(dst + (group >> 4) * L::SUB_BYTES + (group & 15) * 1024 +
+                                           (z < 8 ? at0 : at1) + (z & 7) * 2) = 0;
+#pragma unroll 1
+              for (int sw = 0; sw < 8; ++sw) {           // each softmax warp has its own list, and clears it
+                int* nans = reinterpret_cast<int*>(smem + L::NAN_OFF) + (piece * 8 + sw) * (HD + 4);
+                atomicMin(nans + (group >> 4) * 64 + c4 * 16 + z, t);
+                nans[HD] = 1;
+              }
+            }
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(L::B_KV_FULL + stage));
+        stage = next_stage;
+        if (!stage) phase ^= 1u;
+      }
+      pid = pid_next;
+      scale_slot = (scale_slot + 1) & 3;
+    }
+  }
+}
+
+// ------------------------------------------------------------------ MMA issue (1 thread)
+template <int HD>
+__device__ __forceinline__ void ch_issue_qk(uint32_t sbase, uint32_t tmem, int t, int kstage) {
+  using L = ChLayout<HD>;
+  constexpr uint32_t IDESC = idesc_f16_f32(CH_BM, CH_BN, 0, 0);
+  const uint32_t qa = sbase + L::Q_OFF + t * L::TILE_BYTES;
+  const uint32_t ka = sbase + L::KV_OFF + kstage * L::TILE_BYTES;
+#pragma unroll
+  for (int kk = 0; kk < HD / 16; ++kk) {
+    const uint32_t off = (kk >> 2) * L::SUB_BYTES + (kk & 3) * 32;
+    umma_ss(tmem + L::s_col(t), sdesc_sw128(qa + off, 16, 1024), sdesc_sw128(ka + off, 16, 1024), IDESC, kk > 0 ? 1u : 0u);
+  }
+}
+template <int HD>
+__device__ __forceinline__ void ch_issue_pv(uint32_t sbase, uint32_t tmem, int t, int vstage, bool accumulate) {
+  using L = ChLayout<HD>;
+  constexpr uint32_t IDESC = idesc_f16_f32(CH_BM, HD, 0, 1);
+  const uint32_t va = sbase + L::KV_OFF + vstage * L::TILE_BYTES;
+#pragma unroll
+  for (int kk = 0; kk < CH_BN / 16; ++kk)
+    umma_ts(tmem + L::o_col(t), tmem + L::s_col(t) + kk * 8, sdesc_sw128(va + kk * 2048, L::SUB_BYTES, 1024), IDESC,
+            (accumulate || kk > 0) ? 1u : 0u);
+}
+
+template <int HD>
+__device__ void ch_issue(ChWalk w, uint32_t sbase, uint32_t tmem, volatile int* abort_flag) {
+  using L = ChLayout<HD>;
+  const uint32_t bars = sbase + L::BAR_OFF;
+  auto bar = [&](int i) { return bars + 8u * i; };
+  int stage = 0;
+  uint32_t phase = 0, q_phase = 0, p_phase[2] = {0, 0};
+  auto advance = [&] {
+    if (++stage == CH_STAGES) {
+      stage = 0;
+      phase ^= 1u;
+    }
+  };
+  bool ok = true;
+  for (bool go = w.next(true); go && ok; go = w.next(false)) {
+    if (!mbar_wait(bar(L::B_Q_FULL), q_phase, abort_flag)) break;
+    q_phase ^= 1u;
+    tc_fence_after();
+    int vprev = 0, n = 0;
+    for (int tile = w.t0; tile < w.t1; ++tile, ++n) {
+      const int ks = stage;
+      if (!mbar_wait(bar(L::B_KV_FULL + ks), phase, abort_flag)) { ok = false; break; }
+      advance();
+      tc_fence_after();
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        if (n > 0) {
+          if (!mbar_wait(bar(L::B_P_READY + t), p_phase[t], abort_flag)) { ok = false; break; }
+          p_phase[t] ^= 1u;
+          tc_fence_after();
+          ch_issue_pv<HD>(sbase, tmem, t, vprev, n > 1);
+          if (t == 1) tc_commit(bar(L::B_KV_EMPTY + vprev));
+        }
+        ch_issue_qk<HD>(sbase, tmem, t, ks);
+        tc_commit(bar(L::B_S_FULL + t));
+      }
+      if (!ok) break;
+      tc_commit(bar(L::B_KV_EMPTY + ks));
+      const int vs = stage;
+      if (!mbar_wait(bar(L::B_KV_FULL + vs), phase, abort_flag)) { ok = false; break; }
+      advance();
+      tc_fence_after();
+      vprev = vs;
+    }
+    if (!ok) break;
+    tc_commit(bar(L::B_Q_EMPTY));
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      if (!mbar_wait(bar(L::B_P_READY + t), p_phase[t], abort_flag)) { ok = false; break; }
+      p_phase[t] ^= 1u;
+      tc_fence_after();
+      ch_issue_pv<HD>(sbase, tmem, t, vprev, n > 1);
+      tc_commit(bar(L::B_O_FINAL + t));
+    }
+    if (!ok) break;
+    tc_commit(bar(L::B_KV_EMPTY + vprev));
+  }
+  tc_commit(bar(L::B_DRAIN));
+  drain_wait(bar(L::B_DRAIN), 0);
+}
+
+// ------------------------------------------------------------------ softmax (128 threads a tile)
+// Scores to log2 units: row and key scale.  Never 0, which would turn a masked -inf into NaN (scores of
+// such scales are 0 in any case).
+__device__ __forceinline__ float ch_factor(float row_scale, float key_scale) {
+  return fmaxf(row_scale * key_scale, 1.17549435e-38f);
+}
+
+template <int HD>
+__device__ void ch_softmax(int t, const AttendParams& p, ChWalk w, int per, uint8_t* smem, uint32_t sbase, uint32_t tmem,
+                           volatile int* abort_flag) {
+  using L = ChLayout<HD>;
+  const uint32_t bars = sbase + L::BAR_OFF;
+  auto bar = [&](int i) { return bars + 8u * i; };
+  const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3, row = quarter * 32 + lane;
+  const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+  const uint32_t tS = lane_base + L::s_col(t), tO = lane_base + L::o_col(t);
+  const ChScales* scales = reinterpret_cast<const ChScales*>(smem + L::SCALE_OFF);
+  uint32_t s_phase = 0, o_phase = 0;
+  int scale_slot = 0, piece = 0;
+  for (bool go = w.next(true); go; go = w.next(false), piece = piece == 2 ? 0 : piece + 1) {
+    const int row0 = w.i * CH_ROWS, rows = min(CH_ROWS, w.n() * p.g - row0);
+    const int r = t * CH_BM + row;                 // within the item
+    const bool row_ok = r < rows;
+    const int lim = row_ok ? w.limit(row0 + r) : w.len();
+    const int lim_first = w.limit(row0 + min(t * CH_BM, rows - 1));
+    float m_ref = -INFINITY, l = 0.f, unit = 0.f, row_scale = 0.f;
+    int n = 0;
+    for (int tile = w.t0; tile < w.t1; ++tile, ++n) {
+      if (!__all_sync(0xffffffffu, mbar_wait(bar(L::B_S_FULL + t), s_phase, abort_flag))) return;
+      s_phase ^= 1u;
+      tc_fence_after();
+      if (n == 0) row_scale = *(reinterpret_cast<const float*>(smem + L::QSCALE_OFF) + piece * CH_ROWS + r);
+      uint32_t s[CH_BN];
+#pragma unroll
+      for (int c = 0; c < CH_BN / 32; ++c) tmem_ld32(tS + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&s[32 * c]));
+      tmem_ld_wait();
+      const ChScales* sc = scales + scale_slot;
+      scale_slot = (scale_slot + 1) & 3;
+      const int k0 = tile * CH_BN;
+      if (k0 + CH_BN > lim_first) {
+        const int left = lim - k0;
+#pragma unroll
+        for (int c = 0; c < CH_BN; ++c)
+          if (c >= left) s[c] = __float_as_uint(-INFINITY);
+      }
+      float m_tile = -INFINITY;
+#pragma unroll
+      for (int g1 = 0; g1 < 8; ++g1) {
+        float a = -INFINITY, b = -INFINITY;
+#pragma unroll
+        for (int c = 16 * g1; c < 16 * g1 + 16; c += 4) {
+          a = fmax3(a, __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+          b = fmax3(b, __uint_as_float(s[c + 2]), __uint_as_float(s[c + 3]));
+        }
+        m_tile = fmaxf(m_tile, fmaxf(a, b) * ch_factor(row_scale, sc->k[g1]));
+      }
+      const float m_new = fmaxf(m_ref, m_tile);
+      const float fv = sc->rescale;
+      const bool raise = m_new > m_ref + AT_RAISE;
+      const float alpha = raise ? (m_ref == -INFINITY ? 0.f : ex2_approx(m_ref - m_new)) : 1.f;
+      if (n > 0 && (fv != 1.f || __any_sync(0xffffffffu, raise))) {
+        const float f = alpha * fv;
+#pragma unroll 1
+        for (int c = 0; c < HD / 16; ++c) {
+          uint32_t o[16];
+          tmem_ld16(tO + 16 * c, o);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+          tmem_st16(tO + 16 * c, o);
+        }
+        tmem_st_wait();
+      }
+      if (raise) {
+        l *= alpha;
+        m_ref = m_new;
+      }
+      const float neg_ref = (m_ref == -INFINITY) ? 0.f : -m_ref;
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh) {
+        uint32_t pk[32];
+#pragma unroll
+        for (int g1 = 0; g1 < 4; ++g1) {
+          const float k1 = ch_factor(row_scale, sc->k[4 * hh + g1]), a1 = neg_ref + sc->add[4 * hh + g1];
+          const float2 k2 = make_float2(k1, k1), a2 = make_float2(a1, a1);
+          float2 acc = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            const int at = 64 * hh + 16 * g1 + 2 * c;
+            const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[at]), __uint_as_float(s[at + 1])), k2, a2);
+            float2 e;
+            e.x = ex2_approx(x.x);
+            e.y = ex2_approx(x.y);
+            acc = __fadd2_rn(acc, e);
+            pk[8 * g1 + c] = pack_half2(e.x, e.y);
+          }
+          l = fmaf(acc.x + acc.y, sc->fac[4 * hh + g1], l);
+        }
+        tmem_st32(tS + 32 * hh, pk);
+      }
+      if (tile + 1 == w.t1) unit = sc->unit;
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(bar(L::B_P_READY + t));
+    }
+    if (!__all_sync(0xffffffffu, mbar_wait(bar(L::B_O_FINAL + t), o_phase, abort_flag))) return;
+    o_phase ^= 1u;
+    tc_fence_after();
+    // ---- epilogue
+    const bool whole = w.t0 == 0 && w.t1 == w.nt;
+    const int c0 = w.first / per, c1 = (w.first + w.nt - 1) / per;
+    if (!whole && static_cast<int>(blockIdx.x) == c0 && threadIdx.x == 0) p.split[blockIdx.x] = make_int4(c1, w.b, w.h, w.i);
+    int* nans = reinterpret_cast<int*>(smem + L::NAN_OFF) + (piece * 8 + (threadIdx.x >> 5)) * (HD + 4);
+    const bool any_nan = *reinterpret_cast<volatile int*>(nans + HD) != 0;
+    const int gr = row0 + r, tt = gr / p.g, hq = w.h * p.g + gr - tt * p.g;
+    const long long at = (static_cast<long long>(w.b) * p.c.heads * p.g + hq) * p.T + tt;
+    float* part = p.part + (static_cast<long long>(2 * blockIdx.x + (static_cast<int>(blockIdx.x) == c0 ? 1 : 0)) * CH_ROWS + r) * (HD + 4);
+    const float inv = l > 0.f ? 1.f / l : l;     // nothing seen: 0; NaN stays
+    const float f = whole ? inv * unit : unit;
+#pragma unroll 1
+    for (int c = 0; c < HD / 16; ++c) {
+      uint32_t o[16];
+      tmem_ld16(tO + 16 * c, o);
+      tmem_ld_wait();
+      float y[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) y[i] = l == 0.f ? 0.f : __uint_as_float(o[i]) * f;
+      if (any_nan) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (nans[16 * c + i] < lim) y[i] = __uint_as_float(0x7fffffffu);
+      }
+      if (row_ok) {
+        if (!whole || p.o_f32) {
+          float4* dst = reinterpret_cast<float4*>(whole ? static_cast<float*>(p.o) + at * HD + 16 * c : part + 16 * c);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) dst[i] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+        } else {
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) + at * HD + 16 * c);
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            dst[i] = make_uint4(pack_bf16x2(y[8 * i], y[8 * i + 1]), pack_bf16x2(y[8 * i + 2], y[8 * i + 3]),
+                                pack_bf16x2(y[8 * i + 4], y[8 * i + 5]), pack_bf16x2(y[8 * i + 6], y[8 * i + 7]));
+        }
+      }
+    }
+    if (row_ok) {
+      if (whole)
+        p.lse[at] = l == 0.f ? -INFINITY : (m_ref + log2f(l)) * 0.69314718055994531f;
+      else
+        *reinterpret_cast<float2*>(part + HD) = make_float2(m_ref, l);
+    }
+    if (any_nan) {                               // the same in the whole warp: clear for three pieces on
+      __syncwarp();
+      for (int i = lane; i < HD; i += 32) nans[i] = INT_MAX;
+      if (lane == 0) nans[HD] = 0;
+    }
+  }
+}
+
+// ------------------------------------------------------------------ kernel
+template <int HD>
+__global__ void __launch_bounds__(CH_THREADS, 1) chunk_kernel(const AttendParams p) {
+  using L = ChLayout<HD>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + L::MISC_OFF);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::MISC_OFF + 4);
+  int* prefix = reinterpret_cast<int*>(smem + L::BATCH_OFF);
+  int *s_slot = prefix + p.B + 1, *s_len = s_slot + p.B, *s_n = s_len + p.B;
+  __shared__ int s_start[4];
+  const Pool& c = p.c;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    const uint32_t bars = sbase + L::BAR_OFF;
+    for (int i = 0; i < L::NUM_BARS; ++i) {
+      const bool conv = i == L::B_Q_FULL || (i >= L::B_KV_FULL && i < L::B_KV_FULL + CH_STAGES);
+      const bool p_ready = i >= L::B_P_READY && i < L::B_P_READY + 2;
+      mbar_init(bars + 8u * i, conv ? CH_CONV_WARPS : p_ready ? CH_BM : 1);
+    }
+    *abort_flag = 0;
+    p.split[blockIdx.x] = make_int4(-1, 0, 0, 0);   // unless a piece of this block says otherwise
+    fence_mbar_init();
+  }
+  if (warp == CH_WARP_MMA) {
+    tmem_alloc(smem_u32(tmem_holder), 512);
+    tmem_relinquish();
+  }
+  for (int i = threadIdx.x; i < 24 * (HD + 4); i += CH_THREADS)
+    reinterpret_cast<int*>(smem + L::NAN_OFF)[i] = i % (HD + 4) < HD ? INT_MAX : 0;
+  // ---- the batch: lengths, and the places that each sequence takes on the line (a warp a sequence)
+  for (int b = warp; b < p.B; b += CH_THREADS / 32) {
+    const int slot = p.slots[b];
+    int len = 0, n = 0;
+    if (slot >= 0 && slot < c.slots) {
+      len = c.lens[slot];
+      n = p.n_new ? p.n_new[b] : p.T;
+      if (n < 0 || n > p.T || len < 0 || len > c.max_pages * static_cast<long long>(c.page)) {
+        if (blockIdx.x == 0 && lane == 0) record_status(RA_ERR_PAGES);
+        n = 0;
+      }
+    } else if (slot != -1 && blockIdx.x == 0 && lane == 0) {
+      record_status(RA_ERR_PAGES);
+    }
+    const int items = (n * p.g + CH_ROWS - 1) / CH_ROWS;
+    int sum = 0;
+    for (int i = lane; i < items; i += 32) sum += ChWalk::tiles(len, n, p.g, p.causal, i) + CH_START;
+    sum = __reduce_add_sync(0xffffffffu, sum);
+    if (lane == 0) {
+      s_slot[b] = slot;
+      s_len[b] = len;
+      s_n[b] = n;
+      prefix[b] = sum;                             // per head, for now
+    }
+  }
+  __syncthreads();
+  if (warp == 0) {                                 // prefix sums over the batch, times the heads
+    int carry = 0;
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+      const int b = b0 + lane;
+      const int w = b < p.B ? prefix[b] * c.heads : 0;
+      int s = w;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, s, d);
+        if (lane >= d) s += y;
+      }
+      __syncwarp();
+      if (b < p.B) prefix[b] = carry + s - w;
+      carry += __shfl_sync(0xffffffffu, s, 31);
+    }
+    if (lane == 0) prefix[p.B] = carry;
+  }
+  __syncthreads();
+  const int total = prefix[p.B];
+  const int per = max((total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x), CH_LEAST);
+  const int line0 = static_cast<int>(min(static_cast<long long>(total), static_cast<long long>(blockIdx.x) * per));
+  const int line1 = min(total, line0 + per);
+  if (warp == 0 && line0 < line1) {                // the item that this block's stretch starts in
+    const int b = find_row(prefix, p.B, line0);
+    const int per_head = (prefix[b + 1] - prefix[b]) / c.heads;
+    const int h = (line0 - prefix[b]) / per_head;
+    const int rest = line0 - prefix[b] - h * per_head;
+    const int items = (s_n[b] * p.g + CH_ROWS - 1) / CH_ROWS;
+    int done = 0, at = 0;
+    for (int i0 = 0;; i0 += 32) {
+      const int w = i0 + lane < items ? ChWalk::tiles(s_len[b], s_n[b], p.g, p.causal, i0 + lane) + CH_START : 0;
+      int s = w;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, s, d);
+        if (lane >= d) s += y;
+      }
+      const unsigned behind = __ballot_sync(0xffffffffu, i0 + lane < items && done + s > rest);
+      if (behind || i0 + 32 >= items) {
+        const int k = behind ? __ffs(behind) - 1 : 0;
+        at = i0 + k;
+        done += __shfl_sync(0xffffffffu, s - w, k);
+        break;
+      }
+      done += __shfl_sync(0xffffffffu, s, 31);
+    }
+    if (lane == 0) {
+      s_start[0] = b;
+      s_start[1] = h;
+      s_start[2] = at;
+      s_start[3] = prefix[b] + h * per_head + done + CH_START;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+  ChWalk w;
+  w.p = &p;
+  w.batch = prefix;
+  w.x = line0;
+  w.line1 = line1;
+  w.b = line0 < line1 ? s_start[0] : 0;
+  w.h = line0 < line1 ? s_start[1] : 0;
+  w.i = line0 < line1 ? s_start[2] : 0;
+  w.first = line0 < line1 ? s_start[3] : 0;
+  w.nt = w.t0 = w.t1 = 0;
+
+  if (warp >= 8) {
+    regs_lower<CH_REGS_OTHER>();
+    if (warp == CH_WARP_MMA) {
+      if (lane == 0) ch_issue<HD>(w, sbase, tmem, abort_flag);
+      __syncwarp();
+    } else {
+      ch_convert<HD>(p, w, smem, sbase, abort_flag);
+    }
+  } else {
+    regs_raise<CH_REGS_SOFTMAX>();
+    ch_softmax<HD>(warp >> 2, p, w, per, smem, sbase, tmem, abort_flag);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == CH_WARP_MMA) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+}  // namespace cache
+}  // namespace ra

@@ -3,6 +3,7 @@
 #pragma once
 #include "cache.cuh"
 #include "cache_attn.cuh"
+#include "cache_chunk.cuh"
 #include "cache_io.cuh"
 #include "cache_pages.cuh"
 
@@ -64,50 +65,79 @@ int copy_grid(const rc::Pool& c, long long pairs, int sm_count) {
   return static_cast<int>(units < 1 ? 1 : (units < most ? units : most));
 }
 
-// Rows per block of the attention kernel: as few blocks as 8 * NT rows allow, the narrowest that do.
+// Which kernel a call's rows per kv head (T * g) take: 0 is chunk_kernel; otherwise attend_kernel with
+// blocks of 8 * nt rows, as few blocks as 24 rows allow and the narrowest that do.
+#ifndef RA_CHUNK_ROWS
+#define RA_CHUNK_ROWS 64
+#endif
 constexpr int AT_MAX_NT = 3;
 int attend_nt(long long rows) {
+  if (rows >= RA_CHUNK_ROWS) return 0;
   const long long blocks = (rows + 8 * AT_MAX_NT - 1) / (8 * AT_MAX_NT);
   return static_cast<int>((rows + 8 * blocks - 1) / (8 * blocks));
 }
 
-template <int HD, int NT>
-int attend_launch(const rc::AttendParams& p, DevInfo* di, int grid, cudaStream_t stream) {
-  const int smem = rc::AttLayout<HD>::bytes(p.B);
-  std::atomic<bool>& set = di->attend_attr[HD == 128 ? 0 : 1][NT - 1];
-  if (!set) {
-    const cudaError_t e = cudaFuncSetAttribute(rc::attend_kernel<HD, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               rc::AttLayout<HD>::bytes(rc::MAX_BATCH));
-    if (e != cudaSuccess) return cuda_fail(static_cast<int>(e), "cudaFuncSetAttribute(cache attention smem)");
-    set = true;
-  }
-  rc::attend_kernel<HD, NT><<<grid, rc::AT_THREADS, smem, stream>>>(p);
-  const int st = launch_status();
-  if (st != RA_OK) return st;
-  // The join is set up while attend_kernel runs and waits in the kernel for its end.
+// The join is set up while the kernel before it runs, and waits in the kernel for its end.
+template <int HD, int ROWS, int WARPS>
+int join_launch(const rc::AttendParams& p, int grid, cudaStream_t stream) {
   cudaLaunchAttribute early;
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   early.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid, NT);
+  cfg.gridDim = dim3(grid, ROWS * WARPS / 32);
   cfg.blockDim = dim3(rc::JOIN_THREADS);
   cfg.stream = stream;
   cfg.attrs = &early;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, rc::join_kernel<HD, NT>, p);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, rc::join_kernel<HD, ROWS, WARPS>, p);
   if (e != cudaSuccess) return cuda_fail(static_cast<int>(e), "cudaLaunchKernelEx(cache attention join)");
   return launch_status();
 }
 
+// Shared memory of a kernel, set once per device.
+template <typename K>
+int attend_smem(std::atomic<bool>& set, K kernel, int most) {
+  if (set) return RA_OK;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+  if (e != cudaSuccess) return cuda_fail(static_cast<int>(e), "cudaFuncSetAttribute(cache attention smem)");
+  set = true;
+  return RA_OK;
+}
+
+template <int HD, int NT>
+int attend_launch(const rc::AttendParams& p, DevInfo* di, cudaStream_t stream) {
+  int st = attend_smem(di->attend_attr[HD == 128 ? 0 : 1][NT - 1], rc::attend_kernel<HD, NT>,
+                       rc::AttLayout<HD>::bytes(rc::MAX_BATCH));
+  if (st != RA_OK) return st;
+  const int want = rc::AT_PER_SM * di->sm_count;
+  const int grid = want < rc::AT_MAX_CTAS ? want : rc::AT_MAX_CTAS;
+  rc::attend_kernel<HD, NT><<<grid, rc::AT_THREADS, rc::AttLayout<HD>::bytes(p.B), stream>>>(p);
+  if ((st = launch_status()) != RA_OK) return st;
+  return join_launch<HD, 8 * NT, 4>(p, grid, stream);
+}
+
 template <int HD>
-int attend_nt_launch(int nt, const rc::AttendParams& p, DevInfo* di, int grid, cudaStream_t stream) {
-  if (nt == 1) return attend_launch<HD, 1>(p, di, grid, stream);
-  if (nt == 2) return attend_launch<HD, 2>(p, di, grid, stream);
-  return attend_launch<HD, 3>(p, di, grid, stream);
+int chunk_launch(const rc::AttendParams& p, DevInfo* di, cudaStream_t stream) {
+  int st = attend_smem(di->attend_attr[HD == 128 ? 0 : 1][AT_MAX_NT], rc::chunk_kernel<HD>,
+                       rc::ChLayout<HD>::bytes(rc::MAX_BATCH));
+  if (st != RA_OK) return st;
+  const int grid = di->sm_count < rc::CH_MAX_CTAS ? di->sm_count : rc::CH_MAX_CTAS;
+  rc::chunk_kernel<HD><<<grid, rc::CH_THREADS, rc::ChLayout<HD>::bytes(p.B), stream>>>(p);
+  if ((st = launch_status()) != RA_OK) return st;
+  return join_launch<HD, rc::CH_ROWS, 1>(p, grid, stream);
+}
+
+template <int HD>
+int attend_dispatch(int nt, const rc::AttendParams& p, DevInfo* di, cudaStream_t stream) {
+  if (nt == 0) return chunk_launch<HD>(p, di, stream);
+  if (nt == 1) return attend_launch<HD, 1>(p, di, stream);
+  if (nt == 2) return attend_launch<HD, 2>(p, di, stream);
+  return attend_launch<HD, 3>(p, di, stream);
 }
 
 size_t attend_part_bytes(int nt, int Dh) {
-  return align256(static_cast<size_t>(2 * rc::AT_MAX_CTAS) * 8 * nt * (Dh + 4) * sizeof(float));
+  const size_t parts = nt ? 2ull * rc::AT_MAX_CTAS * 8 * nt : 2ull * rc::CH_MAX_CTAS * rc::CH_ROWS;
+  return align256(parts * (Dh + 4) * sizeof(float));
 }
 
 }  // namespace
@@ -196,10 +226,11 @@ int ring_attn_cache_attend(const ra_cache* cache, int layer, const int* slots, c
   const long long rows = static_cast<long long>(T) * p.g;
   if (rows > INT_MAX / 2) return RA_ERR_SHAPE;
   const int nt = attend_nt(rows);
-  p.n_blocks = static_cast<int>((rows + 8 * nt - 1) / (8 * nt));
-  // the line of tiles is numbered in int
-  const double tiles = std::ceil(static_cast<double>(p.c.max_pages) * p.c.page / rc::AT_TILE) + rc::AT_START;
-  if (tiles * p.c.heads * p.n_blocks * B > INT_MAX / 2) return RA_ERR_SHAPE;
+  // rows per block, and the line of places, which is numbered in int
+  const int block = nt ? 8 * nt : rc::CH_ROWS, tile = nt ? rc::AT_TILE : rc::CH_BN, start = nt ? rc::AT_START : rc::CH_START;
+  p.n_blocks = static_cast<int>((rows + block - 1) / block);
+  const double places = std::ceil(static_cast<double>(p.c.max_pages) * p.c.page / tile) + start;
+  if (places * p.c.heads * p.n_blocks * B > INT_MAX / 2) return RA_ERR_SHAPE;
   if ((st = pages_check_ws(workspace, workspace_bytes, ring_attn_cache_attend_workspace_size(T, Hq, p.c.heads, p.c.Dh))) != RA_OK)
     return st;
   DevInfo* di = dev_info(&st);
@@ -220,9 +251,7 @@ int ring_attn_cache_attend(const ra_cache* cache, int layer, const int* slots, c
   const float sc = (scale > 0.f && std::isfinite(scale)) ? scale : 1.0f / std::sqrt(static_cast<float>(p.c.Dh));
   p.scale_log2 = sc * 1.4426950408889634f;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int want = rc::AT_PER_SM * di->sm_count;
-  const int grid = want < rc::AT_MAX_CTAS ? want : rc::AT_MAX_CTAS;
-  return p.c.Dh == 128 ? attend_nt_launch<128>(nt, p, di, grid, s) : attend_nt_launch<64>(nt, p, di, grid, s);
+  return p.c.Dh == 128 ? attend_dispatch<128>(nt, p, di, s) : attend_dispatch<64>(nt, p, di, s);
 }
 
 size_t ring_attn_cache_pages_workspace_size(int B, int pages) {

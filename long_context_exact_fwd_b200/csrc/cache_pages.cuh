@@ -55,16 +55,6 @@ __device__ __forceinline__ int block_scan(int x, int* warp_sum, int& total) {
   return r;
 }
 
-// The last i in [0, n) with first[i] <= x (first[] is a prefix sum, first[0] = 0).
-__device__ __forceinline__ int find_row(const int* first, int n, int x) {
-  int lo = 0, hi = n;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (first[mid] <= x) lo = mid; else hi = mid;
-  }
-  return lo;
-}
-
 // Pages with refs == 0 (want_free) or > 0, in ascending order from page `from`, into list[0 ..
 // limit); returns how many were written.
 __device__ __forceinline__ int list_pages(const int* refs, int from, int to, bool want_free, int limit, int* list,
