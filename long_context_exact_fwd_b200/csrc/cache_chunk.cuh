@@ -7,8 +7,8 @@
 // An item is 256 rows of one kv head (row = t * g + head): two 128-row tiles.  Roles of the 12 warps:
 //   0-3, 4-7  softmax of tile 0 and 1 (thread = row = TMEM lane),
 //   8         tensor memory and the MMA issue (one thread),
-//   9-11      converters: Q rows to fp16; codes, brought by bulk copies into the upper half of a stage,
-//             to fp16 tiles over the whole of it (read to registers, a barrier of the three, written).
+//   9         fetches codes by bulk copies into a stage as soon as it is free,
+//   10, 11    convert: Q rows to fp16, and the codes to the stage's fp16 tile, in place.
 // The operands are fp16: codes are exact in it (one conversion instruction per two; as bf16 the
 // scale would have to be multiplied in), a query row is scaled to its range by a power of two.
 // The scales never touch the tiles: a page's key scale multiplies its 16-column groups of scores, and
@@ -24,7 +24,7 @@ namespace cache {
 
 constexpr int CH_BM = 128, CH_BN = 128, CH_ROWS = 256, CH_STAGES = 4;
 constexpr int CH_THREADS = 384;
-constexpr int CH_WARP_MMA = 8, CH_CONV_WARPS = 3;
+constexpr int CH_WARP_MMA = 8, CH_WARP_FETCH = 9, CH_WARP_CONV = 10, CH_CONV_WARPS = 2;
 constexpr uint32_t CH_REGS_LAUNCH = 168, CH_REGS_SOFTMAX = 200, CH_REGS_OTHER = 104;
 static_assert(2 * (CH_REGS_SOFTMAX - CH_REGS_LAUNCH) <= CH_REGS_LAUNCH - CH_REGS_OTHER, "register split exceeds the pool");
 constexpr int CH_MAX_CTAS = 160;      // blocks that the workspace has room for (one per SM)
@@ -50,7 +50,8 @@ struct ChLayout {
   static constexpr int TILE_BYTES = SUB * SUB_BYTES;
   static constexpr int Q_OFF = 0;
   static constexpr int KV_OFF = 2 * TILE_BYTES;
-  static constexpr int BAR_OFF = KV_OFF + CH_STAGES * TILE_BYTES;
+  static constexpr int RAW_OFF = KV_OFF + CH_STAGES * TILE_BYTES;
+  static constexpr int BAR_OFF = RAW_OFF + (HD == 128 ? 0 : CH_STAGES * CH_BN * HD);
   static constexpr int B_Q_FULL = 0, B_Q_EMPTY = 1, B_KV_FULL = 2, B_KV_EMPTY = B_KV_FULL + CH_STAGES,
                        B_RAW = B_KV_EMPTY + CH_STAGES, B_S_FULL = B_RAW + CH_STAGES, B_P_READY = B_S_FULL + 2, B_O_FINAL = B_P_READY + 2,
                        B_DRAIN = B_O_FINAL + 2, NUM_BARS = B_DRAIN + 1;
@@ -60,6 +61,11 @@ struct ChLayout {
   static constexpr int NAN_OFF = QSCALE_OFF + 3 * CH_ROWS * 4;          // [3][8 warps][HD + 4] ints, HD a flag
   static constexpr int BATCH_OFF = NAN_OFF + 3 * 8 * (HD + 4) * 4;      // prefix [B + 1], slot, len, n [B]
   static int bytes(int B) { return BATCH_OFF + (4 * B + 1) * 4 + 1024; }
+  // Where a stage's codes arrive: the second half of the stage, which is where the same tokens' second
+  // 64-column block goes (HD 128); a place of their own (HD 64, where a stage has room for both).
+  __host__ __device__ static constexpr int raw(int stage) {
+    return HD == 128 ? KV_OFF + stage * TILE_BYTES + TILE_BYTES / 2 : RAW_OFF + stage * (CH_BN * HD);
+  }
   __host__ __device__ static constexpr uint32_t s_col(int t) { return 128u * t; }
   __host__ __device__ static constexpr uint32_t o_col(int t) { return 256u + uint32_t(HD) * t; }
 };
@@ -123,128 +129,51 @@ struct ChWalk {
   }
 };
 
-// ------------------------------------------------------------------ converters (3 warps)
+// ------------------------------------------------------------------ fetching (1 warp)
+// Page of each 16-token lot of a key tile, in lanes 0-7 (and again in 8-15 ..); -1: none.
+__device__ __forceinline__ int ch_pages(const AttendParams& p, const int* table, int len, int tile) {
+  const int tok = tile * CH_BN + (threadIdx.x & 7) * 16;
+  if (tok >= len) return -1;
+  const int pid = table[tok >> p.page_shift];
+  if (pid >= 0 && pid < p.c.pages) return pid;
+  record_status(RA_ERR_PAGES);
+  return -1;
+}
+
+// Codes of every key and value tile into the upper half of its stage, a bulk copy per 16 tokens, and
+// the tile's scale constants.
 template <int HD>
-__device__ void ch_convert(const AttendParams& p, ChWalk w, uint8_t* smem, uint32_t sbase, volatile int* abort_flag) {
+__device__ void ch_fetch(const AttendParams& p, ChWalk w, uint8_t* smem, uint32_t sbase, volatile int* abort_flag) {
   using L = ChLayout<HD>;
   const Pool& c = p.c;
-  const int lane = threadIdx.x & 31, cw = (threadIdx.x >> 5) - (CH_WARP_MMA + 1);
+  const int lane = threadIdx.x & 31;
   const uint32_t bars = sbase + L::BAR_OFF;
   auto bar = [&](int i) { return bars + 8u * i; };
-  // A tile is 16 * SUB groups of 8 tokens x 64 columns, 16 codes a lane; a warp has every third.
-  constexpr int GROUPS = 16 * L::SUB, PER = (GROUPS + CH_CONV_WARPS - 1) / CH_CONV_WARPS;
   constexpr uint32_t LOT = 16 * HD;                      // bytes of 16 tokens' codes
-  int stage = 0, scale_slot = 0, piece = 0;
-  uint32_t phase = 0, q_phase = 0;
+  int stage = 0, scale_slot = 0;
+  uint32_t phase = 0, armed = 0, armed_parity = 0;       // per stage: ever armed, parity of the last time
   ChScales* scales = reinterpret_cast<ChScales*>(smem + L::SCALE_OFF);
-  for (bool go = w.next(true); go; go = w.next(false), piece = piece == 2 ? 0 : piece + 1) {
-    const int slot = w.slot(), len = w.len(), h = w.h;
-    const int row0 = w.i * CH_ROWS, rows = min(CH_ROWS, w.n() * p.g - row0);
-    const int* table = c.table + static_cast<long long>(slot) * c.max_pages;
-    const int lim_min = w.limit(row0), lim_max = w.limit(row0 + rows - 1);
-    // page of each 16-token lot of a tile, in lanes 0-7 (and again in 8-15 ..), -1: none
-    auto look_up = [&](int tile) {
-      const int tok = tile * CH_BN + (lane & 7) * 16;
-      int pid = -1;
-      if (tok < len) {
-        pid = table[tok >> p.page_shift];
-        if (pid < 0 || pid >= c.pages) {
-          record_status(RA_ERR_PAGES);
-          pid = -1;
-        }
-      }
-      return pid;
-    };
-    // The codes of one tile's keys or values on their way into the upper half of stage `st`, a bulk
-    // copy per lot (first warp).  The stage has to be empty.
-    auto fetch = [&](int pids, int tile, int kv, int st) {
-      const unsigned there = __ballot_sync(0xffffffffu, pids >= 0) & 0xffu;
-      if (lane == 0) mbar_arrive_expect_tx(bar(L::B_RAW + st), __popc(there) * LOT);
-      __syncwarp();
-      if (lane < 8 && pids >= 0)
-        bulk_load(sbase + L::KV_OFF + st * L::TILE_BYTES + L::TILE_BYTES / 2 + lane * LOT,
-                  (kv ? c.v : c.k) + ((static_cast<long long>(pids) * c.heads + h) * c.page +
-                                      ((tile * CH_BN + lane * 16) & (c.page - 1))) * HD,
-                  LOT, bar(L::B_RAW + st));
-    };
-    int pid = look_up(w.t0);
-
-    // ---- Q: 16 (HD 128) or 8 lanes a row, 8 elements a lane
-    if (!named_bar_and(1, CH_CONV_WARPS * 32, mbar_wait(bar(L::B_Q_EMPTY), q_phase ^ 1u, abort_flag))) return;
-    {
-      constexpr int LANES = HD / 8, AT_ONCE = 32 / LANES;   // rows per warp step
-      const int col = lane % LANES, sub_row = lane / LANES;
-      float* q_scale = reinterpret_cast<float*>(smem + L::QSCALE_OFF) + piece * CH_ROWS;
-#pragma unroll 2
-      for (int r0 = cw * AT_ONCE; r0 < CH_ROWS; r0 += CH_CONV_WARPS * AT_ONCE) {
-        const int r = r0 + sub_row;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (r < rows) {
-          const int row = row0 + r, t = row / p.g, hq = h * p.g + row - t * p.g;
-          v = *reinterpret_cast<const uint4*>(p.q + w.b * p.qb + hq * p.qh + t * p.qt + col * 8);
-        }
-        const uint32_t in[4] = {v.x, v.y, v.z, v.w};
-        float amax = 0.f;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float lo = fabsf(__uint_as_float(in[k] << 16)), hi = fabsf(__uint_as_float(in[k] & 0xffff0000u));
-          amax = fmaxf(amax, fmaxf(lo <= 3.4028234663852886e38f ? lo : 0.f, hi <= 3.4028234663852886e38f ? hi : 0.f));
-        }
-#pragma unroll
-        for (int d = LANES / 2; d; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
-        const int up = amax > 0.f ? min(max(14 - exponent_of(amax), -113), 126) : 0;   // amax -> [2^14, 2^15)
-        const float f = two_to(up);
-        uint32_t out[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          out[k] = pack_half2(__uint_as_float(in[k] << 16) * f, __uint_as_float(in[k] & 0xffff0000u) * f);
-        const int tile = r >> 7, rr = r & 127;
-        *reinterpret_cast<uint4*>(smem + L::Q_OFF + tile * L::TILE_BYTES + (col >> 3) * L::SUB_BYTES + rr * 128 +
-                                  (((col & 7) ^ (rr & 7)) << 4)) = make_uint4(out[0], out[1], out[2], out[3]);
-        if (col == 0) q_scale[r] = p.scale_log2 * two_to(-up);
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(L::B_Q_FULL));
-      q_phase ^= 1u;
-    }
-
-    // ---- K and V tiles: while one is converted, the next one's codes are on their way
-    const int sub_tok = lane >> 2, c4 = lane & 3;
-    auto scales_of = [&](int pids, float& k1, float& v1) {   // none: no key of the lot is seen
-      k1 = 1.f;
-      v1 = 0.f;
-      if (cw == 0 && pids >= 0) {
-        k1 = c.k_scale[static_cast<long long>(pids) * c.heads + h];
-        v1 = c.v_scale[static_cast<long long>(pids) * c.heads + h];
-      }
-    };
-    float sk, sv;
-    scales_of(pid, sk, sv);
-    bool ok = true;
-    if (cw == 0) {
-      ok = __all_sync(0xffffffffu, mbar_wait(bar(L::B_KV_EMPTY + stage), phase ^ 1u, abort_flag));
-      if (ok) fetch(pid, w.t0, 0, stage);
-    }
+  bool ok = true;
+  for (bool go = w.next(true); go && ok; go = w.next(false)) {
+    const int len = w.len(), h = w.h;
+    const int* table = c.table + static_cast<long long>(w.slot()) * c.max_pages;
+    int pid = ch_pages(p, table, len, w.t0);
     float v_max = 0.f;                                   // largest value scale so far
-    for (int tile = w.t0; tile < w.t1; ++tile) {
-      const int tok0 = tile * CH_BN;
-      const bool more = tile + 1 < w.t1;
-      const int pid_next = more ? look_up(tile + 1) : -1;
-      const bool diagonal = lim_max > lim_min && tok0 + CH_BN > lim_min;
-      const unsigned lots = __ballot_sync(0xffffffffu, pid >= 0) & 0xffu;
-#pragma unroll 1
+    for (int tile = w.t0; tile < w.t1 && ok; ++tile) {
+      float sk = 1.f, sv = 0.f;                          // none: no key of the lot is seen
+      if (pid >= 0) {
+        sk = c.k_scale[static_cast<long long>(pid) * c.heads + h];
+        sv = c.v_scale[static_cast<long long>(pid) * c.heads + h];
+      }
+      const int pid_next = tile + 1 < w.t1 ? ch_pages(p, table, len, tile + 1) : -1;
+      const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, pid >= 0) & 0xffu) * LOT;
+      const long long at = ((static_cast<long long>(max(pid, 0)) * c.heads + h) * c.page +
+                            ((tile * CH_BN + (lane & 7) * 16) & (c.page - 1))) * HD;
+#pragma unroll
       for (int kv = 0; kv < 2; ++kv) {
-        const int next_stage = stage + 1 == CH_STAGES ? 0 : stage + 1;
-        const uint32_t next_phase = next_stage ? phase : phase ^ 1u;
-        bool fetched = false;
-        if (cw == 0 && ok && (kv == 0 || more)) {
-          ok = __all_sync(0xffffffffu, mbar_wait(bar(L::B_KV_EMPTY + next_stage), next_phase ^ 1u, abort_flag));
-          if (ok) fetch(kv ? pid_next : pid, kv ? tile + 1 : tile, kv ^ 1, next_stage);
-          fetched = ok;
-        }
-        ok = ok && mbar_wait(bar(L::B_RAW + stage), phase, abort_flag);
-        if (kv == 0 && cw == 0) {                        // this tile's scale constants
+        ok = ok && __all_sync(0xffffffffu, mbar_wait(bar(L::B_KV_EMPTY + stage), phase ^ 1u, abort_flag));
+        if (!ok) break;
+        if (kv == 0) {                                   // before this tile's keys can be multiplied
           float top = sv;
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
@@ -262,65 +191,163 @@ __device__ void ch_convert(const AttendParams& p, ChWalk w, uint8_t* smem, uint3
             s->unit = all > 0.f ? two_to(max(exponent_of(all) - CH_P_LOG2, -126)) : 0.f;
           }
           v_max = all;
-          if (more) scales_of(pid_next, sk, sv);
+          scale_slot = (scale_slot + 1) & 3;
+          __syncwarp();
         }
-        uint8_t* stage_at = smem + L::KV_OFF + stage * L::TILE_BYTES;
-        const uint8_t* raw = stage_at + L::TILE_BYTES / 2 + sub_tok * HD + c4 * 16;
-        uint4 x[PER];
+        if (lane == 0) mbar_arrive_expect_tx(bar(L::B_RAW + stage), bytes);   // releases the constants, too
+        __syncwarp();
+        if (lane < 8 && pid >= 0)
+          bulk_load(sbase + L::raw(stage) + lane * LOT, (kv ? c.v : c.k) + at, LOT,
+                    bar(L::B_RAW + stage));
+        armed |= 1u << stage;
+        armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
+        if (++stage == CH_STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      pid = pid_next;
+    }
+  }
+  // the copies land before the block can end (they have, unless a wait gave up)
+  for (int i = 0; i < CH_STAGES; ++i)
+    if (armed >> i & 1u) drain_wait(bar(L::B_RAW + i), armed_parity >> i & 1u);
+}
+
+// ------------------------------------------------------------------ converting (2 warps)
+template <int HD>
+__device__ void ch_convert(const AttendParams& p, ChWalk w, uint8_t* smem, uint32_t sbase, volatile int* abort_flag) {
+  using L = ChLayout<HD>;
+  const Pool& c = p.c;
+  const int lane = threadIdx.x & 31, cw = (threadIdx.x >> 5) - CH_WARP_CONV;
+  const uint32_t bars = sbase + L::BAR_OFF;
+  auto bar = [&](int i) { return bars + 8u * i; };
+  int stage = 0, piece = 0;
+  uint32_t phase = 0, q_phase = 0;
+  for (bool go = w.next(true); go; go = w.next(false), piece = piece == 2 ? 0 : piece + 1) {
+    const int len = w.len(), h = w.h;
+    const int row0 = w.i * CH_ROWS, rows = min(CH_ROWS, w.n() * p.g - row0);
+    const int* table = c.table + static_cast<long long>(w.slot()) * c.max_pages;
+    const int lim_min = w.limit(row0), lim_max = w.limit(row0 + rows - 1);
+
+    // ---- Q: 16 (HD 128) or 8 lanes a row, 8 elements a lane
+    if (!__all_sync(0xffffffffu, mbar_wait(bar(L::B_Q_EMPTY), q_phase ^ 1u, abort_flag))) return;
+    {
+      // Rows arrive as bf16 where their fp16 will stand; each lane then converts what it fetched.
+      constexpr int LANES = HD / 8, AT_ONCE = 32 / LANES, STRIDE = CH_CONV_WARPS * AT_ONCE;
+      const int col = lane % LANES, first = cw * AT_ONCE + lane / LANES;
+      float* q_scale = reinterpret_cast<float*>(smem + L::QSCALE_OFF) + piece * CH_ROWS;
+      auto place = [&](int r) {
+        return L::Q_OFF + (r >> 7) * L::TILE_BYTES + (col >> 3) * L::SUB_BYTES + (r & 127) * 128 + (((col & 7) ^ (r & 7)) << 4);
+      };
+      const __nv_bfloat16* q = p.q + w.b * p.qb + static_cast<long long>(h) * p.g * p.qh + col * 8;
+#pragma unroll 2
+      for (int r = first; r < CH_ROWS; r += STRIDE) {
+        const int row = row0 + min(r, rows - 1), t = row / p.g;
+        cp_async16(sbase + place(r), q + (row - t * p.g) * p.qh + t * p.qt, r < rows);
+      }
+      cp_async_commit();
+      cp_async_wait<0>();
+#pragma unroll 4
+      for (int r = first; r < CH_ROWS; r += STRIDE) {
+        uint4* at = reinterpret_cast<uint4*>(smem + place(r));
+        const uint4 v = *at;
+        const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+        float amax = 0.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float lo = fabsf(__uint_as_float(in[k] << 16)), hi = fabsf(__uint_as_float(in[k] & 0xffff0000u));
+          amax = fmaxf(amax, fmaxf(lo <= 3.4028234663852886e38f ? lo : 0.f, hi <= 3.4028234663852886e38f ? hi : 0.f));
+        }
+#pragma unroll
+        for (int d = LANES / 2; d; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
+        const int up = amax > 0.f ? min(max(14 - exponent_of(amax), -113), 126) : 0;   // amax -> [2^14, 2^15)
+        const float f = two_to(up);
+        uint32_t out[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          out[k] = pack_half2(__uint_as_float(in[k] << 16) * f, __uint_as_float(in[k] & 0xffff0000u) * f);
+        *at = make_uint4(out[0], out[1], out[2], out[3]);
+        if (col == 0) q_scale[r] = p.scale_log2 * two_to(-up);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(L::B_Q_FULL));
+      q_phase ^= 1u;
+    }
+
+    // ---- K and V tiles: HD / 16 lanes a token, 16 codes a lane, AT_ONCE tokens a warp step
+    constexpr int LANES = HD / 16, AT_ONCE = 32 / LANES, STEPS = CH_BN / (AT_ONCE * CH_CONV_WARPS);
+    const int col = lane % LANES, tok = cw * AT_ONCE + lane / LANES, sub = col >> 2, c4 = col & 3;
+    // Token t's row of a 64-column block lies at t * 128, its 16-byte chunks exchanged by t & 7.  The
+    // lanes of the second block write their two chunks in the other order, so that eight lanes of one
+    // token meet all banks.
+    const int at0 = ((2 * c4 + sub) ^ (tok & 7)) << 4, at1 = ((2 * c4 + 1 - sub) ^ (tok & 7)) << 4;
+    static_assert(AT_ONCE * CH_CONV_WARPS % 8 == 0, "a lane's tokens share their place in the swizzle");
+    int pid = ch_pages(p, table, len, w.t0);
+    for (int tile = w.t0; tile < w.t1; ++tile) {
+      const int tok0 = tile * CH_BN;
+      const unsigned lots = __ballot_sync(0xffffffffu, pid >= 0) & 0xffu;   // lots that have a page
+      const bool full = lots == 0xffu && tok0 + CH_BN <= len;
+      const bool diagonal = lim_max > lim_min && tok0 + CH_BN > lim_min;
+      if (tile + 1 < w.t1) pid = ch_pages(p, table, len, tile + 1);
+#pragma unroll 1
+      for (int kv = 0; kv < 2; ++kv) {
+        if (!__all_sync(0xffffffffu, mbar_wait(bar(L::B_RAW + stage), phase, abort_flag))) return;
+        const uint8_t* raw = smem + L::raw(stage) + tok * HD + col * 16;
+        uint8_t* dst = smem + L::KV_OFF + stage * L::TILE_BYTES + sub * L::SUB_BYTES + tok * 128;
         bool odd = false;
+        // Rolled up: unrolled over the tile, this loop and the softmax's did not fit the instruction
+        // cache together, and every role ran at less than half its speed.
+#pragma unroll 1
+        for (int k0 = 0; k0 < STEPS; k0 += 4) {
+          uint4 x[4];
 #pragma unroll
-        for (int k = 0; k < PER; ++k) {
-          const int group = cw + CH_CONV_WARPS * k, t8 = group & 15;   // the same in the whole warp
-          x[k] = make_uint4(0, 0, 0, 0);
-          if (group < GROUPS && (lots >> (t8 >> 1) & 1u) && tok0 + t8 * 8 + sub_tok < len)
-            x[k] = *reinterpret_cast<const uint4*>(raw + t8 * 8 * HD + (group >> 4) * 64);
-          if (kv && diagonal) odd |= has_nan_code(x[k].x) | has_nan_code(x[k].y) | has_nan_code(x[k].z) | has_nan_code(x[k].w);
-        }
-        // everyone has the codes (or everyone gives up): the tile may be written over them
-        if (!named_bar_and(1, CH_CONV_WARPS * 32, ok)) {
-          if (cw == 0) {                                 // copies under way land before the block can end
-            drain_wait(bar(L::B_RAW + stage), phase);
-            if (fetched) drain_wait(bar(L::B_RAW + next_stage), next_phase);
+          for (int k = 0; k < 4; ++k)
+            x[k] = *reinterpret_cast<const uint4*>(raw + (k0 + k) * (AT_ONCE * CH_CONV_WARPS) * HD);
+          __syncwarp();   // HD 128: a token's second block is written where its codes were
+          if (!full || diagonal) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int t = tok + (k0 + k) * (AT_ONCE * CH_CONV_WARPS);
+              // what lies behind the end, or was not fetched, is 0
+              if (!(lots >> (t >> 4) & 1u) || tok0 + t >= len) x[k] = make_uint4(0, 0, 0, 0);
+              odd |= kv && diagonal &&
+                     (has_nan_code(x[k].x) || has_nan_code(x[k].y) || has_nan_code(x[k].z) || has_nan_code(x[k].w));
+            }
           }
-          return;
-        }
-        uint8_t* dst = stage_at + sub_tok * 128;
-        // rows 8 apart share their place in the swizzle: token t's is t & 7 = sub_tok
-        const int at0 = ((2 * c4) ^ sub_tok) << 4, at1 = ((2 * c4 + 1) ^ sub_tok) << 4;
 #pragma unroll
-        for (int k = 0; k < PER; ++k) {
-          const int group = cw + CH_CONV_WARPS * k;
-          if (group < GROUPS) {
-            uint8_t* row = dst + (group >> 4) * L::SUB_BYTES + (group & 15) * 1024;
-            *reinterpret_cast<uint4*>(row + at0) =
-                make_uint4(codes_to_half2(static_cast<uint16_t>(x[k].x)), codes_to_half2(static_cast<uint16_t>(x[k].x >> 16)),
-                           codes_to_half2(static_cast<uint16_t>(x[k].y)), codes_to_half2(static_cast<uint16_t>(x[k].y >> 16)));
-            *reinterpret_cast<uint4*>(row + at1) =
-                make_uint4(codes_to_half2(static_cast<uint16_t>(x[k].z)), codes_to_half2(static_cast<uint16_t>(x[k].z >> 16)),
-                           codes_to_half2(static_cast<uint16_t>(x[k].w)), codes_to_half2(static_cast<uint16_t>(x[k].w >> 16)));
+          for (int k = 0; k < 4; ++k) {
+            const uint4 lo = make_uint4(
+                codes_to_half2(static_cast<uint16_t>(x[k].x)), codes_to_half2(static_cast<uint16_t>(x[k].x >> 16)),
+                codes_to_half2(static_cast<uint16_t>(x[k].y)), codes_to_half2(static_cast<uint16_t>(x[k].y >> 16)));
+            const uint4 hi = make_uint4(
+                codes_to_half2(static_cast<uint16_t>(x[k].z)), codes_to_half2(static_cast<uint16_t>(x[k].z >> 16)),
+                codes_to_half2(static_cast<uint16_t>(x[k].w)), codes_to_half2(static_cast<uint16_t>(x[k].w >> 16)));
+            uint8_t* row = dst + (k0 + k) * (AT_ONCE * CH_CONV_WARPS) * 128;
+            *reinterpret_cast<uint4*>(row + at0) = HD == 128 && sub ? hi : lo;
+            *reinterpret_cast<uint4*>(row + at1) = HD == 128 && sub ? lo : hi;
           }
         }
         // A NaN among values that some rows of the item do not see must not reach them through 0 * NaN:
         // it becomes 0 in the tile, and is put back into the rows that see it at the end.
         if (odd) {
 #pragma unroll 1
-          for (int k = 0; k < PER; ++k) {
-            const int group = cw + CH_CONV_WARPS * k;
-            const int t = tok0 + (group & 15) * 8 + sub_tok;
-            if (group >= GROUPS || t >= len) continue;
+          for (int k = 0; k < STEPS; ++k) {
+            const int t_in = tok + k * (AT_ONCE * CH_CONV_WARPS), t = tok0 + t_in;
+            if (t >= len) continue;
             const int pg = table[t >> p.page_shift];
             if (pg < 0 || pg >= c.pages) continue;
-            const uint8_t* codes = c.v + ((static_cast<long long>(pg) * c.heads + h) * c.page + (t & (c.page - 1))) * HD +
-                                   (group >> 4) * 64 + c4 * 16;
+            const uint8_t* codes = c.v + ((static_cast<long long>(pg) * c.heads + h) * c.page + (t & (c.page - 1))) * HD + col * 16;
 #pragma unroll 1
             for (int z = 0; z < 16; ++z) {
               if ((codes[z] & 0x7fu) != 0x7fu) continue;
-              *reinterpret_cast<uint16_t*>(dst + (group >> 4) * L::SUB_BYTES + (group & 15) * 1024 +
-                                           (z < 8 ? at0 : at1) + (z & 7) * 2) = 0;
+              const int chunk = (2 * c4 + (z >> 3)) ^ (tok & 7);
+              *reinterpret_cast<uint16_t*>(dst + k * (AT_ONCE * CH_CONV_WARPS) * 128 + (chunk << 4) + (z & 7) * 2) = 0;
 #pragma unroll 1
               for (int sw = 0; sw < 8; ++sw) {           // each softmax warp has its own list, and clears it
                 int* nans = reinterpret_cast<int*>(smem + L::NAN_OFF) + (piece * 8 + sw) * (HD + 4);
-                atomicMin(nans + (group >> 4) * 64 + c4 * 16 + z, t);
+                atomicMin(nans + col * 16 + z, t);
                 nans[HD] = 1;
               }
             }
@@ -329,11 +356,11 @@ __device__ void ch_convert(const AttendParams& p, ChWalk w, uint8_t* smem, uint3
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(L::B_KV_FULL + stage));
-        stage = next_stage;
-        if (!stage) phase ^= 1u;
+        if (++stage == CH_STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
       }
-      pid = pid_next;
-      scale_slot = (scale_slot + 1) & 3;
     }
   }
 }
@@ -714,6 +741,8 @@ __global__ void __launch_bounds__(CH_THREADS, 1) chunk_kernel(const AttendParams
     if (warp == CH_WARP_MMA) {
       if (lane == 0) ch_issue<HD>(w, sbase, tmem, abort_flag);
       __syncwarp();
+    } else if (warp == CH_WARP_FETCH) {
+      ch_fetch<HD>(p, w, smem, sbase, abort_flag);
     } else {
       ch_convert<HD>(p, w, smem, sbase, abort_flag);
     }
