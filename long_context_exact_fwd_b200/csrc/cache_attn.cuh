@@ -565,15 +565,15 @@ __global__ void __launch_bounds__(AT_THREADS, AT_PER_SM) attend_kernel(const Att
   if (threadIdx.x == 0) p.split[blockIdx.x] = mine_split;
 }
 
-// Joins the parts of the segments that the kernel before left split: block (c, j) has the j-th lot of
-// 32 / WARPS rows of the segment that starts in its block c, WARPS warps a row, each lane 4 columns of
-// every WARPS-th part.  Parts are added in an order that only the lengths fix.  Bound: latency of
+// Joins the parts of the segments that the kernel before left split: block (c, j) has rows
+// 8 j .. 8 j + 7 of the segment that starts in its block c, JOIN_WARPS warps a row, each lane 4 columns
+// of every JOIN_WARPS-th part.  Parts are added in an order that only the lengths fix.  Bound: latency of
 // three dependent reads; one block alone doing this at the end of its stretch cost 0.6 us per part.
-constexpr int JOIN_THREADS = 1024;
+constexpr int JOIN_THREADS = 1024, JOIN_WARPS = 4;
 
-template <int HD, int ROWS, int WARPS>
+template <int HD, int ROWS>
 __global__ void __launch_bounds__(JOIN_THREADS, 1) join_kernel(const AttendParams p) {
-  constexpr int GROUPS = HD / 4, LOT = 32 / WARPS;
+  constexpr int GROUPS = HD / 4, WARPS = JOIN_WARPS, LOT = 32 / WARPS;
   __shared__ float4 s_o[LOT][WARPS][GROUPS];
   __shared__ float2 s_ml[LOT][WARPS];
   asm volatile("griddepcontrol.wait;" ::: "memory");   // the parts are complete

@@ -5,19 +5,20 @@
 // and softmax this keeps:
 //   O0 += P0(j-1) V(j-1);  S0 = Q0 K(j)^T;  O1 += P1(j-1) V(j-1);  S1 = Q1 K(j)^T.
 // An item is 256 rows of one kv head (row = t * g + head): two 128-row tiles.  Roles of the 12 warps:
-//   0-3, 4-7  softmax of tile 0 and 1 (thread = row = TMEM lane),
+//   0-3, 4-7  softmax of tile 0 and 1 (thread = row = TMEM lane); before it, the row's query to fp16,
 //   8         tensor memory and the MMA issue (one thread),
 //   9         fetches codes by bulk copies into a stage as soon as it is free,
-//   10, 11    convert: Q rows to fp16, and the codes to the stage's fp16 tile, in place.
+//   10, 11    convert the codes to the stage's fp16 tile, in place.
 // The operands are fp16: codes are exact in it (one conversion instruction per two; as bf16 the
 // scale would have to be multiplied in), a query row is scaled to its range by a power of two.
 // The scales never touch the tiles: a page's key scale multiplies its 16-column groups of scores, and
 // its value scale, a power of two, is added to the exponent of P relative to the largest so far:
 //   w_j = 2^(x_j - ref + dv_j + 7),   l += 2^-(dv_j + 7) w_j,   dv_j = e_j - e_max <= 0.
 // Work is cut as in attend_kernel: one line of 128-key tiles over all items, equal stretches, parts
-// joined by join_kernel.
+// joined by chunk_join_kernel.
 #pragma once
 #include "cache_attn.cuh"
+#include "cache_io.cuh"
 
 namespace ra {
 namespace cache {
@@ -57,8 +58,7 @@ struct ChLayout {
                        B_DRAIN = B_O_FINAL + 2, NUM_BARS = B_DRAIN + 1;
   static constexpr int MISC_OFF = BAR_OFF + NUM_BARS * 8;        // TMEM base, abort flag
   static constexpr int SCALE_OFF = (MISC_OFF + 8 + 15) / 16 * 16;
-  static constexpr int QSCALE_OFF = SCALE_OFF + 4 * sizeof(ChScales);   // [3][256] floats
-  static constexpr int NAN_OFF = QSCALE_OFF + 3 * CH_ROWS * 4;          // [3][8 warps][HD + 4] ints, HD a flag
+  static constexpr int NAN_OFF = SCALE_OFF + 4 * sizeof(ChScales);              // [3][8 warps][HD + 4] ints, HD a flag
   static constexpr int BATCH_OFF = NAN_OFF + 3 * 8 * (HD + 4) * 4;      // prefix [B + 1], slot, len, n [B]
   static int bytes(int B) { return BATCH_OFF + (4 * B + 1) * 4 + 1024; }
   // Where a stage's codes arrive: the second half of the stage, which is where the same tokens' second
@@ -223,58 +223,12 @@ __device__ void ch_convert(const AttendParams& p, ChWalk w, uint8_t* smem, uint3
   const uint32_t bars = sbase + L::BAR_OFF;
   auto bar = [&](int i) { return bars + 8u * i; };
   int stage = 0, piece = 0;
-  uint32_t phase = 0, q_phase = 0;
+  uint32_t phase = 0;
   for (bool go = w.next(true); go; go = w.next(false), piece = piece == 2 ? 0 : piece + 1) {
     const int len = w.len(), h = w.h;
     const int row0 = w.i * CH_ROWS, rows = min(CH_ROWS, w.n() * p.g - row0);
     const int* table = c.table + static_cast<long long>(w.slot()) * c.max_pages;
     const int lim_min = w.limit(row0), lim_max = w.limit(row0 + rows - 1);
-
-    // ---- Q: 16 (HD 128) or 8 lanes a row, 8 elements a lane
-    if (!__all_sync(0xffffffffu, mbar_wait(bar(L::B_Q_EMPTY), q_phase ^ 1u, abort_flag))) return;
-    {
-      // Rows arrive as bf16 where their fp16 will stand; each lane then converts what it fetched.
-      constexpr int LANES = HD / 8, AT_ONCE = 32 / LANES, STRIDE = CH_CONV_WARPS * AT_ONCE;
-      const int col = lane % LANES, first = cw * AT_ONCE + lane / LANES;
-      float* q_scale = reinterpret_cast<float*>(smem + L::QSCALE_OFF) + piece * CH_ROWS;
-      auto place = [&](int r) {
-        return L::Q_OFF + (r >> 7) * L::TILE_BYTES + (col >> 3) * L::SUB_BYTES + (r & 127) * 128 + (((col & 7) ^ (r & 7)) << 4);
-      };
-      const __nv_bfloat16* q = p.q + w.b * p.qb + static_cast<long long>(h) * p.g * p.qh + col * 8;
-#pragma unroll 2
-      for (int r = first; r < CH_ROWS; r += STRIDE) {
-        const int row = row0 + min(r, rows - 1), t = row / p.g;
-        cp_async16(sbase + place(r), q + (row - t * p.g) * p.qh + t * p.qt, r < rows);
-      }
-      cp_async_commit();
-      cp_async_wait<0>();
-#pragma unroll 4
-      for (int r = first; r < CH_ROWS; r += STRIDE) {
-        uint4* at = reinterpret_cast<uint4*>(smem + place(r));
-        const uint4 v = *at;
-        const uint32_t in[4] = {v.x, v.y, v.z, v.w};
-        float amax = 0.f;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float lo = fabsf(__uint_as_float(in[k] << 16)), hi = fabsf(__uint_as_float(in[k] & 0xffff0000u));
-          amax = fmaxf(amax, fmaxf(lo <= 3.4028234663852886e38f ? lo : 0.f, hi <= 3.4028234663852886e38f ? hi : 0.f));
-        }
-#pragma unroll
-        for (int d = LANES / 2; d; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
-        const int up = amax > 0.f ? min(max(14 - exponent_of(amax), -113), 126) : 0;   // amax -> [2^14, 2^15)
-        const float f = two_to(up);
-        uint32_t out[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          out[k] = pack_half2(__uint_as_float(in[k] << 16) * f, __uint_as_float(in[k] & 0xffff0000u) * f);
-        *at = make_uint4(out[0], out[1], out[2], out[3]);
-        if (col == 0) q_scale[r] = p.scale_log2 * two_to(-up);
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(L::B_Q_FULL));
-      q_phase ^= 1u;
-    }
 
     // ---- K and V tiles: HD / 16 lanes a token, 16 codes a lane, AT_ONCE tokens a warp step
     constexpr int LANES = HD / 16, AT_ONCE = 32 / LANES, STEPS = CH_BN / (AT_ONCE * CH_CONV_WARPS);
@@ -457,6 +411,42 @@ __device__ __forceinline__ float ch_factor(float row_scale, float key_scale) {
   return fmaxf(row_scale * key_scale, 1.17549435e-38f);
 }
 
+// This thread's query row of the piece that `w` stands on, as fp16 at the row's own power of two, into its
+// place in shared memory; returns the factor from its scores to log2 units (before the key scale).
+template <int HD>
+__device__ __forceinline__ float ch_load_q(int t, const AttendParams& p, const ChWalk& w, uint8_t* smem, uint32_t full_bar) {
+  using L = ChLayout<HD>;
+  const int row = threadIdx.x & 127;
+  const int at = w.i * CH_ROWS + t * CH_BM + row;
+  uint4 v[HD / 8];
+#pragma unroll
+  for (int i = 0; i < HD / 8; ++i) v[i] = make_uint4(0, 0, 0, 0);
+  if (at < w.n() * p.g) {
+    const int tt = at / p.g;
+    const uint4* q = reinterpret_cast<const uint4*>(p.q + w.b * p.qb + (static_cast<long long>(w.h) * p.g + at - tt * p.g) * p.qh + tt * p.qt);
+#pragma unroll
+    for (int i = 0; i < HD / 8; ++i) v[i] = q[i];
+  }
+  // magnitudes order like their bits; what is not finite does not count
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < HD / 8; ++i)
+    for (uint32_t x : {v[i].x, v[i].y, v[i].z, v[i].w}) top = __vmaxu2(top, finite_bits(x));
+  const float amax = __uint_as_float(max(top >> 16, top & 0xffffu) << 16);
+  const int up = amax > 0.f ? min(max(14 - exponent_of(amax), -113), 126) : 0;   // amax -> [2^14, 2^15)
+  const float f = two_to(up);
+  auto half2_of = [&](uint32_t x) { return pack_half2(__uint_as_float(x << 16) * f, __uint_as_float(x & 0xffff0000u) * f); };
+  uint8_t* dst = smem + L::Q_OFF + t * L::TILE_BYTES + row * 128;
+#pragma unroll
+  for (int i = 0; i < HD / 8; ++i)
+    *reinterpret_cast<uint4*>(dst + (i >> 3) * L::SUB_BYTES + (((i & 7) ^ (row & 7)) << 4)) =
+        make_uint4(half2_of(v[i].x), half2_of(v[i].y), half2_of(v[i].z), half2_of(v[i].w));
+  fence_proxy_async_smem();
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(full_bar);
+  return p.scale_log2 * two_to(-up);
+}
+
 template <int HD>
 __device__ void ch_softmax(int t, const AttendParams& p, ChWalk w, int per, uint8_t* smem, uint32_t sbase, uint32_t tmem,
                            volatile int* abort_flag) {
@@ -467,21 +457,22 @@ __device__ void ch_softmax(int t, const AttendParams& p, ChWalk w, int per, uint
   const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
   const uint32_t tS = lane_base + L::s_col(t), tO = lane_base + L::o_col(t);
   const ChScales* scales = reinterpret_cast<const ChScales*>(smem + L::SCALE_OFF);
-  uint32_t s_phase = 0, o_phase = 0;
+  uint32_t s_phase = 0, o_phase = 0, q_phase = 1;
   int scale_slot = 0, piece = 0;
-  for (bool go = w.next(true); go; go = w.next(false), piece = piece == 2 ? 0 : piece + 1) {
+  bool go = w.next(true);
+  float row_scale = go ? ch_load_q<HD>(t, p, w, smem, bar(L::B_Q_FULL)) : 0.f;
+  for (; go; piece = piece == 2 ? 0 : piece + 1) {
     const int row0 = w.i * CH_ROWS, rows = min(CH_ROWS, w.n() * p.g - row0);
     const int r = t * CH_BM + row;                 // within the item
     const bool row_ok = r < rows;
     const int lim = row_ok ? w.limit(row0 + r) : w.len();
     const int lim_first = w.limit(row0 + min(t * CH_BM, rows - 1));
-    float m_ref = -INFINITY, l = 0.f, unit = 0.f, row_scale = 0.f;
+    float m_ref = -INFINITY, l = 0.f, unit = 0.f;
     int n = 0;
     for (int tile = w.t0; tile < w.t1; ++tile, ++n) {
       if (!__all_sync(0xffffffffu, mbar_wait(bar(L::B_S_FULL + t), s_phase, abort_flag))) return;
       s_phase ^= 1u;
       tc_fence_after();
-      if (n == 0) row_scale = *(reinterpret_cast<const float*>(smem + L::QSCALE_OFF) + piece * CH_ROWS + r);
       uint32_t s[CH_BN];
 #pragma unroll
       for (int c = 0; c < CH_BN / 32; ++c) tmem_ld32(tS + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&s[32 * c]));
@@ -529,16 +520,16 @@ __device__ void ch_softmax(int t, const AttendParams& p, ChWalk w, int per, uint
       }
       const float neg_ref = (m_ref == -INFINITY) ? 0.f : -m_ref;
 #pragma unroll
-      for (int hh = 0; hh < 2; ++hh) {
-        uint32_t pk[32];
+      for (int hh = 0; hh < 4; ++hh) {             // 32 keys -> 16 packed columns
+        uint32_t pk[16];
 #pragma unroll
-        for (int g1 = 0; g1 < 4; ++g1) {
-          const float k1 = ch_factor(row_scale, sc->k[4 * hh + g1]), a1 = neg_ref + sc->add[4 * hh + g1];
+        for (int g1 = 0; g1 < 2; ++g1) {
+          const float k1 = ch_factor(row_scale, sc->k[2 * hh + g1]), a1 = neg_ref + sc->add[2 * hh + g1];
           const float2 k2 = make_float2(k1, k1), a2 = make_float2(a1, a1);
           float2 acc = make_float2(0.f, 0.f);
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
-            const int at = 64 * hh + 16 * g1 + 2 * c;
+            const int at = 32 * hh + 16 * g1 + 2 * c;
             const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[at]), __uint_as_float(s[at + 1])), k2, a2);
             float2 e;
             e.x = ex2_approx(x.x);
@@ -546,14 +537,22 @@ __device__ void ch_softmax(int t, const AttendParams& p, ChWalk w, int per, uint
             acc = __fadd2_rn(acc, e);
             pk[8 * g1 + c] = pack_half2(e.x, e.y);
           }
-          l = fmaf(acc.x + acc.y, sc->fac[4 * hh + g1], l);
+          l = fmaf(acc.x + acc.y, sc->fac[2 * hh + g1], l);
         }
-        tmem_st32(tS + 32 * hh, pk);
+        tmem_st16(tS + 16 * hh, pk);
       }
       if (tile + 1 == w.t1) unit = sc->unit;
       tmem_st_wait();
       tc_fence_before();
       mbar_arrive(bar(L::B_P_READY + t));
+    }
+    // the next piece's queries, so that its products can start under this one's end
+    ChWalk after = w;
+    go = after.next(false);
+    if (go) {
+      if (!__all_sync(0xffffffffu, mbar_wait(bar(L::B_Q_EMPTY), q_phase ^ 1u, abort_flag))) return;
+      q_phase ^= 1u;
+      row_scale = ch_load_q<HD>(t, p, after, smem, bar(L::B_Q_FULL));
     }
     if (!__all_sync(0xffffffffu, mbar_wait(bar(L::B_O_FINAL + t), o_phase, abort_flag))) return;
     o_phase ^= 1u;
@@ -566,7 +565,9 @@ __device__ void ch_softmax(int t, const AttendParams& p, ChWalk w, int per, uint
     const bool any_nan = *reinterpret_cast<volatile int*>(nans + HD) != 0;
     const int gr = row0 + r, tt = gr / p.g, hq = w.h * p.g + gr - tt * p.g;
     const long long at = (static_cast<long long>(w.b) * p.c.heads * p.g + hq) * p.T + tt;
-    float* part = p.part + (static_cast<long long>(2 * blockIdx.x + (static_cast<int>(blockIdx.x) == c0 ? 1 : 0)) * CH_ROWS + r) * (HD + 4);
+    // a part: [HD / 4][256 rows][4], so that a warp's rows make whole lines, then m and l [256 rows][2]
+    float4* part = reinterpret_cast<float4*>(p.part) +
+                   static_cast<long long>(2 * blockIdx.x + (static_cast<int>(blockIdx.x) == c0 ? 1 : 0)) * CH_ROWS * (HD / 4 + 1) + r;
     const float inv = l > 0.f ? 1.f / l : l;     // nothing seen: 0; NaN stays
     const float f = whole ? inv * unit : unit;
 #pragma unroll 1
@@ -583,8 +584,12 @@ __device__ void ch_softmax(int t, const AttendParams& p, ChWalk w, int per, uint
           if (nans[16 * c + i] < lim) y[i] = __uint_as_float(0x7fffffffu);
       }
       if (row_ok) {
-        if (!whole || p.o_f32) {
-          float4* dst = reinterpret_cast<float4*>(whole ? static_cast<float*>(p.o) + at * HD + 16 * c : part + 16 * c);
+        if (!whole) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            part[(4 * c + i) * CH_ROWS] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+        } else if (p.o_f32) {
+          float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.o) + at * HD + 16 * c);
 #pragma unroll
           for (int i = 0; i < 4; ++i) dst[i] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
         } else {
@@ -600,13 +605,14 @@ __device__ void ch_softmax(int t, const AttendParams& p, ChWalk w, int per, uint
       if (whole)
         p.lse[at] = l == 0.f ? -INFINITY : (m_ref + log2f(l)) * 0.69314718055994531f;
       else
-        *reinterpret_cast<float2*>(part + HD) = make_float2(m_ref, l);
+        *reinterpret_cast<float2*>(part + HD / 4 * CH_ROWS) = make_float2(m_ref, l);
     }
     if (any_nan) {                               // the same in the whole warp: clear for three pieces on
       __syncwarp();
       for (int i = lane; i < HD; i += 32) nans[i] = INT_MAX;
       if (lane == 0) nans[HD] = 0;
     }
+    w = after;
   }
 }
 
@@ -628,9 +634,9 @@ __global__ void __launch_bounds__(CH_THREADS, 1) chunk_kernel(const AttendParams
   if (threadIdx.x == 0) {
     const uint32_t bars = sbase + L::BAR_OFF;
     for (int i = 0; i < L::NUM_BARS; ++i) {
-      const bool conv = i == L::B_Q_FULL || (i >= L::B_KV_FULL && i < L::B_KV_FULL + CH_STAGES);
+      const bool conv = i >= L::B_KV_FULL && i < L::B_KV_FULL + CH_STAGES;
       const bool p_ready = i >= L::B_P_READY && i < L::B_P_READY + 2;
-      mbar_init(bars + 8u * i, conv ? CH_CONV_WARPS : p_ready ? CH_BM : 1);
+      mbar_init(bars + 8u * i, i == L::B_Q_FULL ? 8 : conv ? CH_CONV_WARPS : p_ready ? CH_BM : 1);
     }
     *abort_flag = 0;
     p.split[blockIdx.x] = make_int4(-1, 0, 0, 0);   // unless a piece of this block says otherwise
@@ -756,6 +762,55 @@ __global__ void __launch_bounds__(CH_THREADS, 1) chunk_kernel(const AttendParams
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+}
+
+// Joins the parts that chunk_kernel left: block (c, x, y) has rows 32 y .. of the segment that starts in its
+// block c, a row a lane, column group CHJ_WARPS x + warp a warp, all reads whole lines.
+constexpr int CHJ_WARPS = 8;
+
+template <int HD>
+__global__ void __launch_bounds__(CHJ_WARPS * 32) chunk_join_kernel(const AttendParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // the parts are complete
+  const int c0 = blockIdx.x;
+  const int4 d = p.split[c0];
+  if (d.x < 0) return;
+  const int n = d.x - c0 + 1, b = d.y, h = d.z, row0 = d.w * CH_ROWS;
+  const int r = blockIdx.y * 32 + (threadIdx.x & 31), group = blockIdx.z * CHJ_WARPS + (threadIdx.x >> 5);
+  if (r >= min(CH_ROWS, (p.n_new ? p.n_new[b] : p.T) * p.g - row0)) return;
+  constexpr long long PART = static_cast<long long>(CH_ROWS) * (HD / 4 + 1);
+  const float4* parts = reinterpret_cast<const float4*>(p.part) + r;
+  // part of block c0: its second place; of a block behind it: the first
+  auto at = [&](int k) { return parts + (k ? 2ll * (c0 + k) : 2ll * c0 + 1) * PART; };
+  float m = -INFINITY, z = 0.f;
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+  constexpr int LOT = 8;                               // parts read together
+  for (int k0 = 0; k0 < n; k0 += LOT) {
+    float2 ml[LOT];
+    float4 y[LOT];
+#pragma unroll
+    for (int k = 0; k < LOT; ++k) {
+      ml[k] = make_float2(-INFINITY, 0.f);
+      if (k0 + k < n) {
+        ml[k] = *reinterpret_cast<const float2*>(at(k0 + k) + HD / 4 * CH_ROWS);
+        y[k] = at(k0 + k)[group * CH_ROWS];
+      }
+    }
+    float top = m;
+#pragma unroll
+    for (int k = 0; k < LOT; ++k) top = fmaxf(top, ml[k].x);
+    const float old = m == top ? 1.f : ex2_approx(m - top);   // nothing yet: 0, or both -inf
+    m = top;
+    z *= old;
+    a = make_float4(a.x * old, a.y * old, a.z * old, a.w * old);
+#pragma unroll
+    for (int k = 0; k < LOT; ++k) {
+      if (ml[k].y == 0.f) continue;                    // saw nothing, or no part
+      const float f = ml[k].x == m ? 1.f : ex2_approx(ml[k].x - m);
+      z += ml[k].y * f;
+      a = make_float4(fmaf(y[k].x, f, a.x), fmaf(y[k].y, f, a.y), fmaf(y[k].z, f, a.z), fmaf(y[k].w, f, a.w));
+    }
+  }
+  store_row<HD>(p, b, h, row0 + r, 4 * group, m, z, a);
 }
 
 }  // namespace cache

@@ -78,18 +78,17 @@ int attend_nt(long long rows) {
 }
 
 // The join is set up while the kernel before it runs, and waits in the kernel for its end.
-template <int HD, int ROWS, int WARPS>
-int join_launch(const rc::AttendParams& p, int grid, cudaStream_t stream) {
+int join_launch(void (*kernel)(rc::AttendParams), const rc::AttendParams& p, dim3 grid, int threads, cudaStream_t stream) {
   cudaLaunchAttribute early;
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   early.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid, ROWS * WARPS / 32);
-  cfg.blockDim = dim3(rc::JOIN_THREADS);
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
   cfg.stream = stream;
   cfg.attrs = &early;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, rc::join_kernel<HD, ROWS, WARPS>, p);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
   if (e != cudaSuccess) return cuda_fail(static_cast<int>(e), "cudaLaunchKernelEx(cache attention join)");
   return launch_status();
 }
@@ -113,7 +112,7 @@ int attend_launch(const rc::AttendParams& p, DevInfo* di, cudaStream_t stream) {
   const int grid = want < rc::AT_MAX_CTAS ? want : rc::AT_MAX_CTAS;
   rc::attend_kernel<HD, NT><<<grid, rc::AT_THREADS, rc::AttLayout<HD>::bytes(p.B), stream>>>(p);
   if ((st = launch_status()) != RA_OK) return st;
-  return join_launch<HD, 8 * NT, 4>(p, grid, stream);
+  return join_launch(rc::join_kernel<HD, 8 * NT>, p, dim3(grid, NT), rc::JOIN_THREADS, stream);
 }
 
 template <int HD>
@@ -124,7 +123,7 @@ int chunk_launch(const rc::AttendParams& p, DevInfo* di, cudaStream_t stream) {
   const int grid = di->sm_count < rc::CH_MAX_CTAS ? di->sm_count : rc::CH_MAX_CTAS;
   rc::chunk_kernel<HD><<<grid, rc::CH_THREADS, rc::ChLayout<HD>::bytes(p.B), stream>>>(p);
   if ((st = launch_status()) != RA_OK) return st;
-  return join_launch<HD, rc::CH_ROWS, 1>(p, grid, stream);
+  return join_launch(rc::chunk_join_kernel<HD>, p, dim3(grid, rc::CH_ROWS / 32, HD / 4 / rc::CHJ_WARPS), rc::CHJ_WARPS * 32, stream);
 }
 
 template <int HD>
