@@ -41,7 +41,8 @@ struct alignas(16) ChScales {
   float fac[8];      // 2^-(dv + 7)
   float rescale;     // what O has to be multiplied by for the new e_max (1: nothing)
   float unit;        // 2^(e_max - 7): true value of O's unit
-  float pad[2];
+  unsigned lots;     // of the tile's eight, those that have a page
+  unsigned pad;
 };
 
 template <int HD>
@@ -166,7 +167,8 @@ __device__ void ch_fetch(const AttendParams& p, ChWalk w, uint8_t* smem, uint32_
         sv = c.v_scale[static_cast<long long>(pid) * c.heads + h];
       }
       const int pid_next = tile + 1 < w.t1 ? ch_pages(p, table, len, tile + 1) : -1;
-      const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, pid >= 0) & 0xffu) * LOT;
+      const unsigned lots = __ballot_sync(0xffffffffu, pid >= 0) & 0xffu;
+      const uint32_t bytes = __popc(lots) * LOT;
       const long long at = ((static_cast<long long>(max(pid, 0)) * c.heads + h) * c.page +
                             ((tile * CH_BN + (lane & 7) * 16) & (c.page - 1))) * HD;
 #pragma unroll
@@ -189,6 +191,7 @@ __device__ void ch_fetch(const AttendParams& p, ChWalk w, uint8_t* smem, uint32_
           if (lane == 0) {
             s->rescale = all > v_max ? (v_max > 0.f ? v_max / all : 0.f) : 1.f;
             s->unit = all > 0.f ? two_to(max(exponent_of(all) - CH_P_LOG2, -126)) : 0.f;
+            s->lots = lots;
           }
           v_max = all;
           scale_slot = (scale_slot + 1) & 3;
@@ -222,7 +225,8 @@ __device__ void ch_convert(const AttendParams& p, ChWalk w, uint8_t* smem, uint3
   const int lane = threadIdx.x & 31, cw = (threadIdx.x >> 5) - CH_WARP_CONV;
   const uint32_t bars = sbase + L::BAR_OFF;
   auto bar = [&](int i) { return bars + 8u * i; };
-  int stage = 0, piece = 0;
+  const ChScales* scales = reinterpret_cast<const ChScales*>(smem + L::SCALE_OFF);
+  int stage = 0, scale_slot = 0, piece = 0;
   uint32_t phase = 0;
   for (bool go = w.next(true); go; go = w.next(false), piece = piece == 2 ? 0 : piece + 1) {
     const int len = w.len(), h = w.h;
@@ -238,29 +242,35 @@ __device__ void ch_convert(const AttendParams& p, ChWalk w, uint8_t* smem, uint3
     // token meet all banks.
     const int at0 = ((2 * c4 + sub) ^ (tok & 7)) << 4, at1 = ((2 * c4 + 1 - sub) ^ (tok & 7)) << 4;
     static_assert(AT_ONCE * CH_CONV_WARPS % 8 == 0, "a lane's tokens share their place in the swizzle");
-    int pid = ch_pages(p, table, len, w.t0);
     for (int tile = w.t0; tile < w.t1; ++tile) {
       const int tok0 = tile * CH_BN;
-      const unsigned lots = __ballot_sync(0xffffffffu, pid >= 0) & 0xffu;   // lots that have a page
-      const bool full = lots == 0xffu && tok0 + CH_BN <= len;
       const bool diagonal = lim_max > lim_min && tok0 + CH_BN > lim_min;
-      if (tile + 1 < w.t1) pid = ch_pages(p, table, len, tile + 1);
+      unsigned lots = 0;
 #pragma unroll 1
       for (int kv = 0; kv < 2; ++kv) {
         if (!__all_sync(0xffffffffu, mbar_wait(bar(L::B_RAW + stage), phase, abort_flag))) return;
+        if (kv == 0) lots = scales[scale_slot].lots;
+        const bool plain = lots == 0xffu && tok0 + CH_BN <= len && !diagonal;
         const uint8_t* raw = smem + L::raw(stage) + tok * HD + col * 16;
         uint8_t* dst = smem + L::KV_OFF + stage * L::TILE_BYTES + sub * L::SUB_BYTES + tok * 128;
         bool odd = false;
+        uint4 next[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) next[k] = *reinterpret_cast<const uint4*>(raw + k * (AT_ONCE * CH_CONV_WARPS) * HD);
         // Rolled up: unrolled over the tile, this loop and the softmax's did not fit the instruction
         // cache together, and every role ran at less than half its speed.
 #pragma unroll 1
         for (int k0 = 0; k0 < STEPS; k0 += 4) {
           uint4 x[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            x[k] = *reinterpret_cast<const uint4*>(raw + (k0 + k) * (AT_ONCE * CH_CONV_WARPS) * HD);
+          for (int k = 0; k < 4; ++k) x[k] = next[k];
+          if (k0 + 4 < STEPS) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              next[k] = *reinterpret_cast<const uint4*>(raw + (k0 + 4 + k) * (AT_ONCE * CH_CONV_WARPS) * HD);
+          }
           __syncwarp();   // HD 128: a token's second block is written where its codes were
-          if (!full || diagonal) {
+          if (!plain) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const int t = tok + (k0 + k) * (AT_ONCE * CH_CONV_WARPS);
@@ -315,6 +325,7 @@ __device__ void ch_convert(const AttendParams& p, ChWalk w, uint8_t* smem, uint3
           phase ^= 1u;
         }
       }
+      scale_slot = (scale_slot + 1) & 3;
     }
   }
 }
