@@ -29,11 +29,14 @@ namespace ra {
 namespace cache {
 
 constexpr int AT_WARPS = 4;
-constexpr int AT_PER_SM = 2;         // blocks per SM: one joins its warps while the other streams
+// Blocks per SM (one joins its warps while the others stream) and stages of a warp's ring, by the
+// registers that NT takes.  Measured (32 contexts up to 16K, NT 1 / 16 contexts, 16 rows, NT 2): 2 blocks
+// of 3 stages 98.9 / 51.7 us, 3 of 2 94.8 / 57.8 (spills).
+__host__ __device__ constexpr int at_per_sm(int nt) { return nt == 1 ? 3 : 2; }
+__host__ __device__ constexpr int at_stages(int nt) { return nt == 1 ? 2 : 3; }
 constexpr int AT_THREADS = AT_WARPS * 32;
 constexpr int AT_TILE = 32;          // tokens of a warp's tile
-constexpr int AT_STAGES = 3;
-constexpr int AT_MAX_CTAS = 320;     // blocks that the workspace has room for (AT_PER_SM per SM)
+constexpr int AT_MAX_SMS = 160;      // SMs that the workspace has room for
 // What starting and joining a stretch costs, in tiles: it counts in a block's share.  Measured for 32
 // contexts of 16 to 16384 tokens, 8 heads: 0 115.8 us, 8 102.2, 16 98.7, 24 100.4.
 constexpr int AT_START = 16;
@@ -55,13 +58,14 @@ struct AttendParams {
   float scale_log2;
 };
 
-template <int HD>
+template <int HD, int NT>
 struct AttLayout {
+  static constexpr int STAGES = at_stages(NT);
   static constexpr int KV = AT_TILE * HD;              // bytes of a tile's keys
   static constexpr int STAGE = 2 * KV;
-  static constexpr int RING = AT_STAGES * STAGE;       // per warp
+  static constexpr int RING = STAGES * STAGE;          // per warp
   static constexpr int SCALES = AT_WARPS * RING;       // [warp][stage][4] floats
-  static constexpr int ML = SCALES + AT_WARPS * AT_STAGES * 16;   // [warp][rows][2] floats, rows <= 32
+  static constexpr int ML = SCALES + AT_WARPS * STAGES * 16;   // [warp][rows][2] floats, rows <= 32
   static constexpr int NANS = ML + AT_WARPS * 32 * 8;  // [HD] ints
   static constexpr int PREFIX = NANS + HD * 4;         // [B + 1] ints, then slots [B], lengths [B]
   static int bytes(int B) { return PREFIX + (3 * B + 1) * 4; }
@@ -137,16 +141,16 @@ __device__ __forceinline__ void store_row(const AttendParams& p, int b, int h, i
 }
 
 template <int HD, int NT>
-__global__ void __launch_bounds__(AT_THREADS, AT_PER_SM) attend_kernel(const AttendParams p) {
-  using L = AttLayout<HD>;
-  constexpr int ROWS = 8 * NT;
+__global__ void __launch_bounds__(AT_THREADS, at_per_sm(NT)) attend_kernel(const AttendParams p) {
+  using L = AttLayout<HD, NT>;
+  constexpr int ROWS = 8 * NT, STAGES = L::STAGES;
   constexpr int KS = HD / 16;          // k steps of a score, and 16-column blocks of a head
   extern __shared__ __align__(128) uint8_t smem[];
   const Pool& c = p.c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gr = lane >> 2, gc = lane & 3;
   const uint32_t ring = smem_u32(smem) + warp * L::RING;
   uint8_t* ring_ptr = smem + warp * L::RING;
-  float* scales = reinterpret_cast<float*>(smem + L::SCALES) + warp * AT_STAGES * 4;
+  float* scales = reinterpret_cast<float*>(smem + L::SCALES) + warp * STAGES * 4;
   const uint32_t scales_u = smem_u32(scales);
   float* s_ml = reinterpret_cast<float*>(smem + L::ML);
   int* s_nan = reinterpret_cast<int*>(smem + L::NANS);
@@ -198,6 +202,7 @@ __global__ void __launch_bounds__(AT_THREADS, AT_PER_SM) attend_kernel(const Att
   const int line0 = min(static_cast<long long>(total), static_cast<long long>(blockIdx.x) * per);
   const int line1 = min(total, line0 + per);
 
+  asm volatile("griddepcontrol.launch_dependents;");   // the join can take what the SMs have left, and wait
   int4 mine_split = make_int4(-1, 0, 0, 0);
   for (int x = line0; x < line1;) {
     // ---- which sequence, head and row block
@@ -250,7 +255,7 @@ __global__ void __launch_bounds__(AT_THREADS, AT_PER_SM) attend_kernel(const Att
     };
     auto fetch = [&](int i) {                 // tile i into its stage; the next one's pages on the way
       if (i < count) {
-        const int tile = first + i * AT_WARPS, stage = i % AT_STAGES;
+        const int tile = first + i * AT_WARPS, stage = i % STAGES;
         const int pid0 = next_pid0, pid1 = next_pid1;
         const int in_page = (tile * AT_TILE) & (c.page - 1);
         const long long at0 = ((static_cast<long long>(max(pid0, 0)) * c.heads + h) * c.page + in_page) * HD;
@@ -285,7 +290,7 @@ __global__ void __launch_bounds__(AT_THREADS, AT_PER_SM) attend_kernel(const Att
     };
     look_up(0);
 #pragma unroll
-    for (int i = 0; i < AT_STAGES - 1; ++i) fetch(i);
+    for (int i = 0; i < STAGES - 1; ++i) fetch(i);
 
     // ---- queries as B fragments: column gr of block j is row j * 8 + gr, head columns gc * HD / 4 ..
     uint32_t qf[NT][KS][2];
@@ -348,10 +353,10 @@ __global__ void __launch_bounds__(AT_THREADS, AT_PER_SM) attend_kernel(const Att
     float v_ref = 0.f;                        // largest value scale so far; O is in units of it
 
     for (int i = 0; i < count; ++i) {
-      cp_async_wait<AT_STAGES - 2>();
+      cp_async_wait<STAGES - 2>();
       __syncwarp();
-      fetch(i + AT_STAGES - 1);
-      const int tile = first + i * AT_WARPS, stage = i % AT_STAGES, tok0 = tile * AT_TILE;
+      fetch(i + STAGES - 1);
+      const int tile = first + i * AT_WARPS, stage = i % STAGES, tok0 = tile * AT_TILE;
       const uint32_t kst = ring + stage * L::STAGE, vst = kst + L::KV;
       const float4 sc = *reinterpret_cast<const float4*>(scales + stage * 4);
 
@@ -565,15 +570,13 @@ __global__ void __launch_bounds__(AT_THREADS, AT_PER_SM) attend_kernel(const Att
   if (threadIdx.x == 0) p.split[blockIdx.x] = mine_split;
 }
 
-// Joins the parts of the segments that the kernel before left split: block (c, j) has rows
-// 8 j .. 8 j + 7 of the segment that starts in its block c, JOIN_WARPS warps a row, each lane 4 columns
-// of every JOIN_WARPS-th part.  Parts are added in an order that only the lengths fix.  Bound: latency of
-// three dependent reads; one block alone doing this at the end of its stretch cost 0.6 us per part.
-constexpr int JOIN_THREADS = 1024, JOIN_WARPS = 4;
-
-template <int HD, int ROWS>
-__global__ void __launch_bounds__(JOIN_THREADS, 1) join_kernel(const AttendParams p) {
-  constexpr int GROUPS = HD / 4, WARPS = JOIN_WARPS, LOT = 32 / WARPS;
+// Joins the parts of the segments that the kernel before left split: block (c, j) has rows LOT j .. of the
+// segment that starts in its block c, WARPS warps a row, each lane 4 columns of every WARPS-th part.  Parts
+// are added in an order that only the lengths fix.  Bound: latency of three dependent reads; one block
+// alone doing this at the end of its stretch cost 0.6 us per part.
+template <int HD, int ROWS, int LOT, int WARPS>
+__global__ void __launch_bounds__(LOT * WARPS * 32) join_kernel(const AttendParams p) {
+  constexpr int GROUPS = HD / 4;
   __shared__ float4 s_o[LOT][WARPS][GROUPS];
   __shared__ float2 s_ml[LOT][WARPS];
   asm volatile("griddepcontrol.wait;" ::: "memory");   // the parts are complete

@@ -741,6 +741,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1) chunk_kernel(const AttendParams
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  asm volatile("griddepcontrol.launch_dependents;");   // the join can be set up, and wait
   const uint32_t tmem = *tmem_holder;
   ChWalk w;
   w.p = &p;

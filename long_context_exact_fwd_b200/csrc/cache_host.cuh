@@ -106,13 +106,16 @@ int attend_smem(std::atomic<bool>& set, K kernel, int most) {
 template <int HD, int NT>
 int attend_launch(const rc::AttendParams& p, DevInfo* di, cudaStream_t stream) {
   int st = attend_smem(di->attend_attr[HD == 128 ? 0 : 1][NT - 1], rc::attend_kernel<HD, NT>,
-                       rc::AttLayout<HD>::bytes(rc::MAX_BATCH));
+                       rc::AttLayout<HD, NT>::bytes(rc::MAX_BATCH));
   if (st != RA_OK) return st;
-  const int want = rc::AT_PER_SM * di->sm_count;
-  const int grid = want < rc::AT_MAX_CTAS ? want : rc::AT_MAX_CTAS;
-  rc::attend_kernel<HD, NT><<<grid, rc::AT_THREADS, rc::AttLayout<HD>::bytes(p.B), stream>>>(p);
+  const int grid = rc::at_per_sm(NT) * (di->sm_count < rc::AT_MAX_SMS ? di->sm_count : rc::AT_MAX_SMS);
+  rc::attend_kernel<HD, NT><<<grid, rc::AT_THREADS, rc::AttLayout<HD, NT>::bytes(p.B), stream>>>(p);
   if ((st = launch_status()) != RA_OK) return st;
-  return join_launch(rc::join_kernel<HD, 8 * NT>, p, dim3(grid, NT), rc::JOIN_THREADS, stream);
+  // Few segments have many parts each: 16 warps a row instead of 4.  The whole call, 4 against 16: one segment of
+  // 128K tokens (444 parts) 36.4 and 24.0 us; eight of them 53.7 and 54.5; 16 of 777 tokens 10.5 and 13.8.
+  if (static_cast<long long>(p.B) * p.c.heads * p.n_blocks <= 4)
+    return join_launch(rc::join_kernel<HD, 8 * NT, 1, 16>, p, dim3(grid, 8 * NT), 512, stream);
+  return join_launch(rc::join_kernel<HD, 8 * NT, 2, 4>, p, dim3(grid, 4 * NT), 256, stream);
 }
 
 template <int HD>
@@ -135,7 +138,7 @@ int attend_dispatch(int nt, const rc::AttendParams& p, DevInfo* di, cudaStream_t
 }
 
 size_t attend_part_bytes(int nt, int Dh) {
-  const size_t parts = nt ? 2ull * rc::AT_MAX_CTAS * 8 * nt : 2ull * rc::CH_MAX_CTAS * rc::CH_ROWS;
+  const size_t parts = nt ? 2ull * rc::at_per_sm(nt) * rc::AT_MAX_SMS * 8 * nt : 2ull * rc::CH_MAX_CTAS * rc::CH_ROWS;
   return align256(parts * (Dh + 4) * sizeof(float));
 }
 
@@ -206,7 +209,7 @@ int ring_attn_cache_read(const ra_cache* cache, int layer, const int* slots, con
 size_t ring_attn_cache_attend_workspace_size(int T, int Hq, int Hkv, int Dh) {
   if (T <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || (Dh != 64 && Dh != 128)) return 0;
   const int nt = attend_nt(static_cast<long long>(T) * (Hq / Hkv));
-  return attend_part_bytes(nt, Dh) + align256(rc::AT_MAX_CTAS * sizeof(int4));
+  return attend_part_bytes(nt, Dh) + align256(3 * rc::AT_MAX_SMS * sizeof(int4))   /* blocks: at_per_sm per SM, at most 3 */;
 }
 
 int ring_attn_cache_attend(const ra_cache* cache, int layer, const int* slots, const int* n_new, int B, int T, int Hq,
