@@ -172,12 +172,12 @@ int ring_attn_cache_append(const ra_cache* cache, int layer, const int* slots, c
   const dim3 grid(static_cast<unsigned>(most), p.c.heads, 2 * B);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int units = p.c.page * p.c.Dh / rc::UNIT;
-  if (units <= rc::IO_THREADS)
-    rc::append_kernel<1><<<grid, rc::IO_THREADS, 0, s>>>(p);
-  else if (units <= 2 * rc::IO_THREADS)
-    rc::append_kernel<2><<<grid, rc::IO_THREADS, 0, s>>>(p);
-  else
-    rc::append_kernel<4><<<grid, rc::IO_THREADS, 0, s>>>(p);
+  void (*kernel)(rc::AppendParams) = units <= rc::AP_THREADS       ? rc::append_kernel<1>
+                                     : units <= 2 * rc::AP_THREADS ? rc::append_kernel<2>
+                                     : units <= 4 * rc::AP_THREADS ? rc::append_kernel<4>
+                                     : units <= 8 * rc::AP_THREADS ? rc::append_kernel<8>
+                                                                   : rc::append_kernel<16>;
+  kernel<<<grid, rc::AP_THREADS, 0, s>>>(p);
   return launch_status();
 }
 

@@ -14,7 +14,10 @@ namespace ra {
 namespace cache {
 
 constexpr int IO_THREADS = 256;
-constexpr int UNIT = 16;      // elements of a thread's unit: 32 bytes of bf16, 16 of codes
+// Elements of a thread's unit: 16 bytes of bf16, 8 of codes, so that a warp's accesses are whole lines on
+// both sides (32 and 16 bytes a thread left half of every sector out: reading back the 8K prompt took 41 us
+// against 33).
+constexpr int UNIT = 8;
 
 struct AppendParams {
   Pool c;                      // one layer
@@ -22,10 +25,6 @@ struct AppendParams {
   long long kb, kh, kt, vb, vh, vt;
   const int *slots, *n_new;    // n_new null: T
   int T;
-};
-
-struct Elems {
-  uint4 a, b;                  // 16 bf16
 };
 
 __device__ __forceinline__ void unpack2(uint32_t w, float& lo, float& hi) {
@@ -58,9 +57,8 @@ __device__ __forceinline__ uint32_t quantise4(uint32_t w0, uint32_t w1, float in
   return floats_to_codes(x[0], x[1]) | (floats_to_codes(x[2], x[3]) << 16);
 }
 template <bool EXACT_RANGE>
-__device__ __forceinline__ uint4 quantise16(const Elems& x, float inv) {
-  return make_uint4(quantise4<EXACT_RANGE>(x.a.x, x.a.y, inv), quantise4<EXACT_RANGE>(x.a.z, x.a.w, inv),
-                    quantise4<EXACT_RANGE>(x.b.x, x.b.y, inv), quantise4<EXACT_RANGE>(x.b.z, x.b.w, inv));
+__device__ __forceinline__ uint2 quantise8(const uint4& x, float inv) {
+  return make_uint2(quantise4<EXACT_RANGE>(x.x, x.y, inv), quantise4<EXACT_RANGE>(x.z, x.w, inv));
 }
 __device__ __forceinline__ uint32_t restate4(uint32_t codes, float f) {
   const float2 a = half2_to_float2(codes_to_half2(static_cast<uint16_t>(codes)));
@@ -68,9 +66,11 @@ __device__ __forceinline__ uint32_t restate4(uint32_t codes, float f) {
   return floats_to_codes(a.x * f, a.y * f) | (floats_to_codes(b.x * f, b.y * f) << 16);
 }
 
-// NU: units per thread, ceil(page * Dh / UNIT / IO_THREADS).
+// NU: units per thread, ceil(page * Dh / UNIT / AP_THREADS).  Few threads with many units each: what a warp
+// spends on finding its page and on the maximum is half of its instructions at 32 elements a lane.
+constexpr int AP_THREADS = 128;
 template <int NU>
-__global__ void __launch_bounds__(IO_THREADS) append_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(AP_THREADS) append_kernel(const AppendParams p) {
   const Pool& c = p.c;
   const int b = blockIdx.z >> 1, kv = blockIdx.z & 1, h = blockIdx.y;
   const int slot = p.slots[b];
@@ -87,8 +87,9 @@ __global__ void __launch_bounds__(IO_THREADS) append_kernel(const AppendParams p
     if (reports) record_status(RA_ERR_PAGES);
     return;
   }
-  const int j = p0 / c.page + blockIdx.x;         // the page's place in the table
-  const long long at0 = static_cast<long long>(j) * c.page;
+  const int page_shift = 31 - __clz(c.page);
+  const int j = (p0 >> page_shift) + blockIdx.x;  // the page's place in the table
+  const long long at0 = static_cast<long long>(j) << page_shift;
   if (n == 0 || at0 >= len) return;
   const int pid = c.table[static_cast<long long>(slot) * c.max_pages + j];
   bool bad = pid < 0 || pid >= c.pages;
@@ -104,21 +105,18 @@ __global__ void __launch_bounds__(IO_THREADS) append_kernel(const AppendParams p
   float* scale = (kv ? c.v_scale : c.k_scale) + static_cast<long long>(pid) * c.heads + h;
   const int skip = max(0, static_cast<int>(p0 - at0));                       // older tokens in the page
   const int end = static_cast<int>(min(static_cast<long long>(c.page), len - at0));
-  const int row_shift = c.Dh == 128 ? 3 : 2;      // units of a row: 8 or 4
+  const int row_shift = c.Dh == 128 ? 4 : 3;      // units of a row: 16 or 8
   src += (at0 - p0) * st;
 
-  Elems x[NU];
+  const int t0 = threadIdx.x >> row_shift, t_step = AP_THREADS >> row_shift;   // unit i: token t0 + i * t_step
+  const __nv_bfloat16* from = src + t0 * st + (threadIdx.x & ((1 << row_shift) - 1)) * UNIT;
+  uint4 x[NU];
 #pragma unroll
   for (int i = 0; i < NU; ++i) {
-    const int u = threadIdx.x + i * IO_THREADS;
-    const int t = u >> row_shift;
-    if (t >= skip && t < end) {
-      const uint4* q = reinterpret_cast<const uint4*>(src + t * st + (u & ((1 << row_shift) - 1)) * UNIT);
-      x[i].a = q[0];
-      x[i].b = q[1];
-    } else {
-      x[i].a = x[i].b = make_uint4(0, 0, 0, 0);
-    }
+    const int t = t0 + i * t_step;
+    x[i] = make_uint4(0, 0, 0, 0);
+    if (t >= skip && t < end) x[i] = *reinterpret_cast<const uint4*>(from);
+    from += t_step * st;
   }
   const float old_scale = skip ? *scale : 0.f;
   // Two running magnitudes per word; whether anything is not finite shows in the plain maximum, and
@@ -126,19 +124,19 @@ __global__ void __launch_bounds__(IO_THREADS) append_kernel(const AppendParams p
   uint32_t top = 0;
 #pragma unroll
   for (int i = 0; i < NU; ++i)
-    for (uint32_t w : {x[i].a.x, x[i].a.y, x[i].a.z, x[i].a.w, x[i].b.x, x[i].b.y, x[i].b.z, x[i].b.w})
+    for (uint32_t w : {x[i].x, x[i].y, x[i].z, x[i].w})
       top = __vmaxu2(top, w & 0x7fff7fffu);
   uint32_t amax = max(top >> 16, top & 0xffffu);
   if (amax >= BF16_INF) {
     top = 0;
 #pragma unroll
     for (int i = 0; i < NU; ++i)
-      for (uint32_t w : {x[i].a.x, x[i].a.y, x[i].a.z, x[i].a.w, x[i].b.x, x[i].b.y, x[i].b.z, x[i].b.w})
+      for (uint32_t w : {x[i].x, x[i].y, x[i].z, x[i].w})
         top = __vmaxu2(top, finite_bits(w));
     amax = max(top >> 16, top & 0xffffu) | 0x10000u;
   }
   const uint32_t flag = __any_sync(0xffffffffu, amax >> 16) ? 0x10000u : 0u;
-  __shared__ unsigned s_max[IO_THREADS / 32];
+  __shared__ unsigned s_max[AP_THREADS / 32];
   const unsigned wmax = __reduce_max_sync(0xffffffffu, amax & 0xffffu) | flag;
   if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = wmax;
   if (named_before(p.slots, b, slot)) {           // barrier: s_max and every read of the old scale
@@ -147,7 +145,7 @@ __global__ void __launch_bounds__(IO_THREADS) append_kernel(const AppendParams p
   }
   unsigned m = 0, odd = 0;
 #pragma unroll
-  for (int i = 0; i < IO_THREADS / 32; ++i) {
+  for (int i = 0; i < AP_THREADS / 32; ++i) {
     m = max(m, s_max[i] & 0xffffu);
     odd |= s_max[i] >> 16;
   }
@@ -160,17 +158,27 @@ __global__ void __launch_bounds__(IO_THREADS) append_kernel(const AppendParams p
   const float inv = two_to(-e);
   const float shrink = two_to(max(e_old - e, -126));
   const bool exact_range = odd || e == E_MAX;     // the same in the whole block
+  uint2* dst = reinterpret_cast<uint2*>(codes) + threadIdx.x;
+  auto mine = [&](int i) {
+    const int t = t0 + i * t_step;
+    return t >= skip && t < end;
+  };
+  if (exact_range) {
 #pragma unroll
-  for (int i = 0; i < NU; ++i) {
-    const int u = threadIdx.x + i * IO_THREADS;
-    const int t = u >> row_shift;
-    uint4* dst = reinterpret_cast<uint4*>(codes) + u;
-    if (t >= skip && t < end) {
-      *dst = exact_range ? quantise16<true>(x[i], inv) : quantise16<false>(x[i], inv);
-    } else if (t < skip && e > e_old) {
-      const uint4 o = *dst;
-      *dst = make_uint4(restate4(o.x, shrink), restate4(o.y, shrink), restate4(o.z, shrink), restate4(o.w, shrink));
-    }
+    for (int i = 0; i < NU; ++i)
+      if (mine(i)) dst[i * AP_THREADS] = quantise8<true>(x[i], inv);
+  } else {
+#pragma unroll
+    for (int i = 0; i < NU; ++i)
+      if (mine(i)) dst[i * AP_THREADS] = quantise8<false>(x[i], inv);
+  }
+  if (e > e_old) {                                // restate what the page held before
+#pragma unroll 1
+    for (int i = 0; i < NU; ++i)
+      if (t0 + i * t_step < skip) {
+        const uint2 o = dst[i * AP_THREADS];
+        dst[i * AP_THREADS] = make_uint2(restate4(o.x, shrink), restate4(o.y, shrink));
+      }
   }
   if (threadIdx.x == 0) *scale = two_to(e);
 }
@@ -204,12 +212,12 @@ __global__ void __launch_bounds__(IO_THREADS) read_kernel(const ReadParams p) {
   const float* scales = kv ? c.v_scale : c.k_scale;
   const int col = (threadIdx.x % PER_ROW) * UNIT;
   const long long t0 = static_cast<long long>(blockIdx.x) * (READ_UNITS * IO_THREADS / PER_ROW) + threadIdx.x / PER_ROW;
-  uint4 w[READ_UNITS];
+  uint2 w[READ_UNITS];
   float s[READ_UNITS];
 #pragma unroll
   for (int i = 0; i < READ_UNITS; ++i) {
     const long long t = t0 + i * (IO_THREADS / PER_ROW), pos = start + t;
-    w[i] = make_uint4(0, 0, 0, 0);
+    w[i] = make_uint2(0, 0);
     s[i] = 0.f;
     if (t < p.length && pos >= 0 && pos < len) {
       const int pid = row[pos >> page_shift];
@@ -217,7 +225,7 @@ __global__ void __launch_bounds__(IO_THREADS) read_kernel(const ReadParams p) {
         record_status(RA_ERR_PAGES);
       } else {
         const long long ph = static_cast<long long>(pid) * c.heads + h;
-        w[i] = *reinterpret_cast<const uint4*>(codes + (((ph << page_shift) + (pos & (c.page - 1))) * HD + col));
+        w[i] = *reinterpret_cast<const uint2*>(codes + (((ph << page_shift) + (pos & (c.page - 1))) * HD + col));
         s[i] = scales[ph];
       }
     }
@@ -227,18 +235,14 @@ __global__ void __launch_bounds__(IO_THREADS) read_kernel(const ReadParams p) {
   for (int i = 0; i < READ_UNITS; ++i) {
     const long long t = t0 + i * (IO_THREADS / PER_ROW);
     if (t >= p.length) break;
-    uint32_t y[8];
-    const uint32_t in[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+    uint32_t y[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const float2 lo = half2_to_float2(codes_to_half2(static_cast<uint16_t>(in[k])));
-      const float2 hi = half2_to_float2(codes_to_half2(static_cast<uint16_t>(in[k] >> 16)));
-      y[2 * k] = pack_bf16x2(lo.x * s[i], lo.y * s[i]);
-      y[2 * k + 1] = pack_bf16x2(hi.x * s[i], hi.y * s[i]);
+      const uint32_t in = k < 2 ? w[i].x : w[i].y;
+      const float2 f = half2_to_float2(codes_to_half2(static_cast<uint16_t>(k & 1 ? in >> 16 : in)));
+      y[k] = pack_bf16x2(f.x * s[i], f.y * s[i]);
     }
-    uint4* dst = reinterpret_cast<uint4*>(out + t * HD);
-    dst[0] = make_uint4(y[0], y[1], y[2], y[3]);
-    dst[1] = make_uint4(y[4], y[5], y[6], y[7]);
+    *reinterpret_cast<uint4*>(out + t * HD) = make_uint4(y[0], y[1], y[2], y[3]);
   }
 }
 
