@@ -11,7 +11,8 @@ one, so the two overlap (§3.3).  Partial results combine through their log-sum-
 The per-block work runs in the CUDA library (ring_attn_fwd_partial / ring_attn_bwd_accumulate on
 one block pair, ring_attn_merge for the partials: each step's forward output and gradients stay
 float32 until the end); this module is host orchestration only: torch.distributed
-point-to-point sends and receives between neighbours (NCCL over NVLink on GPUs), no collective.
+point-to-point sends and receives between neighbours (NCCL over NVLink on GPUs), no collective in
+the rings.
 
 Causal masking is on global positions: block j is entirely visible to block r when j < r, masked
 per element when j == r (the kernel's own causal mask, same positions), and skipped when j > r.
@@ -34,6 +35,15 @@ sequence into 2D chunks and giving rank r chunks r and 2D - 1 - r (an early and 
 every rank the same work at every ring step: two of the four half-block pairs are visible at every
 step but the first, where three are (two of them on the diagonal).  The ring itself is unchanged;
 only which positions a rank holds, and so which half-block pairs it computes, differ.
+
+Rotary positions (rope=): a RopePlan turns this rank's Q and K by their global positions
+(ring_positions, zigzag_positions) before the first step, in one library launch; the travelling K is
+the rotated one, so every rank rotates its own block only.  The backward turns the float32 dQ and dK
+back (the gradient of the rotation) before they are rounded.
+
+Cached contexts (ring_cache_attend): each rank keeps its part of every sequence's context in an 8-bit
+cache of its own and attends to it alone; one gather of the ranks' float32 partials and the library's
+merge give the whole context's result, as §3.1 combines blocks.
 """
 from typing import Callable, Optional, Tuple
 
@@ -43,6 +53,7 @@ import torch.distributed as dist
 BlockFwd = Callable[[torch.Tensor, torch.Tensor, torch.Tensor, bool], Tuple[torch.Tensor, torch.Tensor]]
 BlockBwd = Callable[..., Tuple[torch.Tensor, torch.Tensor, torch.Tensor]]
 Merge = Callable[[torch.Tensor, torch.Tensor], Tuple[torch.Tensor, torch.Tensor]]
+Rotate = Callable[..., Tuple[torch.Tensor, torch.Tensor]]
 
 
 def _cuda_block_fwd(q, k, v, causal):
@@ -67,6 +78,32 @@ def _accumulating(block_bwd: Optional[BlockBwd]):
         dk32 += b.to(dk32.dtype)
         dv32 += c.to(dv32.dtype)
     return acc
+
+
+def _cuda_rotate(q, k, plan, pos, inverse):
+    from . import ring_attn as ra
+    return ra.rope(q, plan, k=k, pos=pos, inverse=inverse)
+
+
+def ring_positions(rank: int, world: int, c: int, device=None) -> torch.Tensor:
+    """Global positions of the c tokens that rank `rank` holds under the contiguous assignment."""
+    return torch.arange(rank * c, (rank + 1) * c, dtype=torch.int64, device=device)
+
+
+def zigzag_positions(rank: int, world: int, c: int, device=None) -> torch.Tensor:
+    """Global positions of the c tokens (two chunks of c / 2) of rank `rank`'s zig-zag shard."""
+    if c % 2:
+        raise ValueError(f"a zig-zag shard holds two equal chunks; length {c} is odd")
+    h = c // 2
+    return torch.cat([torch.arange(n * h, (n + 1) * h, dtype=torch.int64, device=device)
+                      for n in zigzag_chunks(rank, world)])
+
+
+def _rotated(q, k, rope, pos, rotate: Optional[Rotate], inverse: bool = False):
+    """(q, k) turned by `rope` at positions `pos` (a function, called only if there is a plan)."""
+    if rope is None:
+        return q, k
+    return (rotate or _cuda_rotate)(q, k, rope, pos(), inverse)
 
 
 def _cuda_merge(o_parts, lse_parts):
@@ -197,14 +234,16 @@ class _Ring:
 
 
 def ring_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: bool = True, group=None,
-             block_fwd: Optional[BlockFwd] = None, merge: Optional[Merge] = None, stats: Optional[dict] = None
-             ) -> Tuple[torch.Tensor, torch.Tensor]:
+             block_fwd: Optional[BlockFwd] = None, merge: Optional[Merge] = None, stats: Optional[dict] = None,
+             rope=None, rotate: Optional[Rotate] = None) -> Tuple[torch.Tensor, torch.Tensor]:
     """Forward of this rank's query block.  q, k, v: [B, H, c, Dh], this rank's block of the
     sequence (rank r holds positions [r c, r c + c)).  Returns (o [B, H, c, Dh], lse [B, H, c]).
+    `rope` (a RopePlan) rotates q and k by their positions first.
     Each step's partial is folded into a running result at once (_RunningMerge), so the memory
     a rank holds does not grow with the ring length.  `stats`, if given, receives
     "peak_partials": the most partials held at once."""
     ring = _Ring(group)
+    q, k = _rotated(q, k, rope, lambda: ring_positions(ring.rank, ring.world, q.shape[2], q.device), rotate)
     run = _RunningMerge(q, block_fwd, merge)
     kv = torch.stack((k, v)).contiguous()
     nxt = torch.empty_like(kv)
@@ -227,11 +266,14 @@ def ring_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: bool = T
 
 
 def ring_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor, lse: torch.Tensor,
-             do: torch.Tensor, causal: bool = True, group=None, block_bwd: Optional[BlockBwd] = None
-             ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+             do: torch.Tensor, causal: bool = True, group=None, block_bwd: Optional[BlockBwd] = None,
+             rope=None, rotate: Optional[Rotate] = None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
     """Backward of this rank's blocks, given the ring forward's o and lse.  Returns
-    (dq, dk, dv) for this rank's block, in the dtype of q."""
+    (dq, dk, dv) for this rank's block, in the dtype of q.  With `rope` as in the forward, q and k are
+    those before the rotation, and so are their gradients."""
     ring = _Ring(group)
+    pos = lambda: ring_positions(ring.rank, ring.world, q.shape[2], q.device)  # noqa: E731
+    q, k = _rotated(q, k, rope, pos, rotate)
     block_acc = _accumulating(block_bwd)
     kv = torch.stack((k, v)).contiguous()
     g = torch.zeros(kv.shape, dtype=torch.float32, device=kv.device)   # dK, dV of the block held
@@ -251,15 +293,25 @@ def ring_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor,
             g, g_n = g_n, g
     if block_bwd is None:
         _raise_on_device_status()
-    return dq.to(q.dtype), g[0].to(q.dtype), g[1].to(q.dtype)
+    dq, dk = _rotated(dq, g[0], rope, pos, rotate, True)
+    return dq.to(q.dtype), dk.to(q.dtype), g[1].to(q.dtype)
+
+
+def _rotated_blocks(q_blocks, k_blocks, rope, rotate, inverse=False, positions=ring_positions):
+    """_rotated of every rank's block."""
+    world = len(q_blocks)
+    out = [_rotated(q, k, rope, lambda r=r, q=q: positions(r, world, q.shape[2], q.device), rotate, inverse)
+           for r, (q, k) in enumerate(zip(q_blocks, k_blocks))]
+    return [q for q, _ in out], [k for _, k in out]
 
 
 def ring_fwd_emulated(q_blocks, k_blocks, v_blocks, causal: bool = True, block_fwd: Optional[BlockFwd] = None,
-                      merge: Optional[Merge] = None):
+                      merge: Optional[Merge] = None, rope=None, rotate: Optional[Rotate] = None):
     """All ranks of ring_fwd in one process, without communication: rank r's output from the
     same ring_steps schedule, the blocks taken from the lists.  For checking the block-pair
     work of a D-rank ring on one device."""
     world = len(q_blocks)
+    q_blocks, k_blocks = _rotated_blocks(q_blocks, k_blocks, rope, rotate)
     outs = []
     for r in range(world):
         run = _RunningMerge(q_blocks[r], block_fwd, merge)
@@ -270,11 +322,12 @@ def ring_fwd_emulated(q_blocks, k_blocks, v_blocks, causal: bool = True, block_f
 
 
 def ring_bwd_emulated(q_blocks, k_blocks, v_blocks, o_blocks, lse_blocks, do_blocks, causal: bool = True,
-                      block_bwd: Optional[BlockBwd] = None):
+                      block_bwd: Optional[BlockBwd] = None, rope=None, rotate: Optional[Rotate] = None):
     """All ranks of ring_bwd in one process: dQ of block r summed over its steps, dK/dV of block
     j summed over every rank that visits it (what the travelling accumulators collect)."""
     block_acc = _accumulating(block_bwd)
     world = len(q_blocks)
+    q_blocks, k_blocks = _rotated_blocks(q_blocks, k_blocks, rope, rotate)
     dq = [torch.zeros(b.shape, dtype=torch.float32, device=b.device) for b in q_blocks]
     dk = [torch.zeros(b.shape, dtype=torch.float32, device=b.device) for b in k_blocks]
     dv = [torch.zeros(b.shape, dtype=torch.float32, device=b.device) for b in v_blocks]
@@ -283,6 +336,7 @@ def ring_bwd_emulated(q_blocks, k_blocks, v_blocks, o_blocks, lse_blocks, do_blo
             block_acc(q_blocks[r], k_blocks[j], v_blocks[j], o_blocks[r], lse_blocks[r], do_blocks[r], masked,
                       dq[r], dk[j], dv[j])
     dt = q_blocks[0].dtype
+    dq, dk = _rotated_blocks(dq, dk, rope, rotate, True)
     return [x.to(dt) for x in dq], [x.to(dt) for x in dk], [x.to(dt) for x in dv]
 
 
@@ -342,11 +396,13 @@ def _kv_halves(k: torch.Tensor, v: torch.Tensor) -> torch.Tensor:
 
 
 def ring_fwd_zigzag(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: bool = True, group=None,
-                    block_fwd: Optional[BlockFwd] = None, merge: Optional[Merge] = None
-                    ) -> Tuple[torch.Tensor, torch.Tensor]:
+                    block_fwd: Optional[BlockFwd] = None, merge: Optional[Merge] = None,
+                    rope=None, rotate: Optional[Rotate] = None) -> Tuple[torch.Tensor, torch.Tensor]:
     """Forward of this rank's zig-zag shard.  q, k, v: [B, H, c, Dh], zigzag_shard of the full
-    sequence for this rank (c = S / world, even).  Returns (o, lse) in the same shard layout."""
+    sequence for this rank (c = S / world, even).  Returns (o, lse) in the same shard layout.  `rope` as
+    in ring_fwd, at the shard's positions."""
     ring = _Ring(group)
+    q, k = _rotated(q, k, rope, lambda: zigzag_positions(ring.rank, ring.world, q.shape[2], q.device), rotate)
     qh = _halves(q)
     runs = [_RunningMerge(h, block_fwd, merge) for h in qh]   # one running fold per query half
     kv = _kv_halves(k, v)
@@ -367,11 +423,14 @@ def ring_fwd_zigzag(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: b
 
 
 def ring_bwd_zigzag(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor, lse: torch.Tensor,
-                    do: torch.Tensor, causal: bool = True, group=None, block_bwd: Optional[BlockBwd] = None
-                    ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+                    do: torch.Tensor, causal: bool = True, group=None, block_bwd: Optional[BlockBwd] = None,
+                    rope=None, rotate: Optional[Rotate] = None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
     """Backward of this rank's zig-zag shard, given ring_fwd_zigzag's o and lse (all tensors in
-    the shard layout).  Returns (dq, dk, dv) in the shard layout, in the dtype of q."""
+    the shard layout).  Returns (dq, dk, dv) in the shard layout, in the dtype of q.  `rope` as in
+    ring_bwd."""
     ring = _Ring(group)
+    pos = lambda: zigzag_positions(ring.rank, ring.world, q.shape[2], q.device)  # noqa: E731
+    q, k = _rotated(q, k, rope, pos, rotate)
     block_acc = _accumulating(block_bwd)
     qh, oh, lh, dh = _halves(q), _halves(o), _halves(lse), _halves(do)
     kv = _kv_halves(k, v)
@@ -392,15 +451,17 @@ def ring_bwd_zigzag(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.
     if block_bwd is None:
         _raise_on_device_status()
     dt = q.dtype
-    return (torch.cat(dq, dim=2).to(dt), torch.cat((g[0, 0], g[1, 0]), dim=2).to(dt),
-            torch.cat((g[0, 1], g[1, 1]), dim=2).to(dt))
+    dq, dk = _rotated(torch.cat(dq, dim=2), torch.cat((g[0, 0], g[1, 0]), dim=2), rope, pos, rotate, True)
+    return dq.to(dt), dk.to(dt), torch.cat((g[0, 1], g[1, 1]), dim=2).to(dt)
 
 
 def ring_fwd_zigzag_emulated(q_shards, k_shards, v_shards, causal: bool = True,
-                             block_fwd: Optional[BlockFwd] = None, merge: Optional[Merge] = None):
+                             block_fwd: Optional[BlockFwd] = None, merge: Optional[Merge] = None, rope=None,
+                             rotate: Optional[Rotate] = None):
     """All ranks of ring_fwd_zigzag in one process, without communication: rank r's (o, lse)
     from the same zigzag_steps schedule, the shards taken from the lists."""
     world = len(q_shards)
+    q_shards, k_shards = _rotated_blocks(q_shards, k_shards, rope, rotate, positions=zigzag_positions)
     kvs = [_kv_halves(k, v) for k, v in zip(k_shards, v_shards)]
     outs = []
     for r in range(world):
@@ -415,11 +476,12 @@ def ring_fwd_zigzag_emulated(q_shards, k_shards, v_shards, causal: bool = True,
 
 
 def ring_bwd_zigzag_emulated(q_shards, k_shards, v_shards, o_shards, lse_shards, do_shards, causal: bool = True,
-                             block_bwd: Optional[BlockBwd] = None):
+                             block_bwd: Optional[BlockBwd] = None, rope=None, rotate: Optional[Rotate] = None):
     """All ranks of ring_bwd_zigzag in one process: dQ of each half summed over its pairs, dK/dV
     of each key/value half summed over every rank that visits it."""
     block_acc = _accumulating(block_bwd)
     world = len(q_shards)
+    q_shards, k_shards = _rotated_blocks(q_shards, k_shards, rope, rotate, positions=zigzag_positions)
     kvs = [_kv_halves(k, v) for k, v in zip(k_shards, v_shards)]
     gs = [torch.zeros(kv.shape, dtype=torch.float32, device=kv.device) for kv in kvs]
     dqs = []
@@ -432,5 +494,38 @@ def ring_bwd_zigzag_emulated(q_shards, k_shards, v_shards, o_shards, lse_shards,
                           gs[j][b, 1])
         dqs.append(torch.cat(dq, dim=2))
     dt = q_shards[0].dtype
-    return ([x.to(dt) for x in dqs], [torch.cat((g[0, 0], g[1, 0]), dim=2).to(dt) for g in gs],
+    dqs, dks = _rotated_blocks(dqs, [torch.cat((g[0, 0], g[1, 0]), dim=2) for g in gs], rope, rotate, True,
+                               zigzag_positions)
+    return ([x.to(dt) for x in dqs], [x.to(dt) for x in dks],
             [torch.cat((g[0, 1], g[1, 1]), dim=2).to(dt) for g in gs])
+
+
+def _cuda_cache_attend(cache, layer, slots, n_new, q, causal):
+    from . import ring_attn as ra
+    # rows of padding stay a part of weight 0
+    o = torch.zeros(q.shape, dtype=torch.float32, device=q.device)
+    lse = torch.full(q.shape[:3], float("-inf"), dtype=torch.float32, device=q.device)
+    return ra.cache_attend(cache, layer, slots, n_new, q, causal=causal, out_dtype=torch.float32, out=o, lse=lse)
+
+
+def ring_cache_attend(cache, layer: int, slots: torch.Tensor, n_new: Optional[torch.Tensor], q: torch.Tensor,
+                      newest: bool, group=None, attend: Optional[Callable] = None, merge: Optional[Merge] = None
+                      ) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Attention of new tokens over contexts that are cut across the ranks: rank r's `cache` holds, in
+    slots[b], a part of sequence b's keys and values, and every rank has the same q [B, H, T, Dh].
+    `newest` says whether this rank's part ends with the new tokens themselves (exactly one rank: there
+    the queries are masked by position); the other ranks' parts lie before them and are seen whole, so
+    their n_new only says which rows exist.  Returns (o, lse) of the whole contexts, on every rank."""
+    o, lse = (attend or _cuda_cache_attend)(cache, layer, slots, n_new, q, newest)
+    world = dist.get_world_size(group) if dist.is_initialized() else 1
+    if world > 1:
+        os, lses = [torch.empty_like(o) for _ in range(world)], [torch.empty_like(lse) for _ in range(world)]
+        dist.all_gather(os, o, group=group)
+        dist.all_gather(lses, lse, group=group)
+        o_parts, lse_parts = torch.stack(os), torch.stack(lses)
+    else:
+        o_parts, lse_parts = o.unsqueeze(0), lse.unsqueeze(0)
+    out = (merge or _cuda_merge)(o_parts, lse_parts)
+    if attend is None and merge is None:
+        _raise_on_device_status()
+    return out
