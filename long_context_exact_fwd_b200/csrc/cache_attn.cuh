@@ -158,6 +158,7 @@ __global__ void __launch_bounds__(AT_THREADS, at_per_sm(NT)) attend_kernel(const
   int *s_slot = s_prefix + p.B + 1, *s_len = s_slot + p.B;
   __shared__ int s_warp[AT_WARPS];
 
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // what ran before on the stream is complete
   // ---- the line: for each (head, row block) of a sequence AT_START places, then its tiles
   int total = 0;
   for (int b0 = 0; b0 < p.B; b0 += AT_THREADS) {
@@ -580,6 +581,7 @@ __global__ void __launch_bounds__(LOT * WARPS * 32) join_kernel(const AttendPara
   __shared__ float4 s_o[LOT][WARPS][GROUPS];
   __shared__ float2 s_ml[LOT][WARPS];
   asm volatile("griddepcontrol.wait;" ::: "memory");   // the parts are complete
+  asm volatile("griddepcontrol.launch_dependents;");
   const int c0 = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int4 d = p.split[c0];
   if (d.x < 0) return;

@@ -650,6 +650,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1) chunk_kernel(const AttendParams
       mbar_init(bars + 8u * i, i == L::B_Q_FULL ? 8 : conv ? CH_CONV_WARPS : p_ready ? CH_BM : 1);
     }
     *abort_flag = 0;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     p.split[blockIdx.x] = make_int4(-1, 0, 0, 0);   // unless a piece of this block says otherwise
     fence_mbar_init();
   }
@@ -659,6 +660,7 @@ __global__ void __launch_bounds__(CH_THREADS, 1) chunk_kernel(const AttendParams
   }
   for (int i = threadIdx.x; i < 24 * (HD + 4); i += CH_THREADS)
     reinterpret_cast<int*>(smem + L::NAN_OFF)[i] = i % (HD + 4) < HD ? INT_MAX : 0;
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // what ran before on the stream is complete
   // ---- the batch: lengths, and the places that each sequence takes on the line (a warp a sequence)
   for (int b = warp; b < p.B; b += CH_THREADS / 32) {
     const int slot = p.slots[b];
@@ -783,6 +785,7 @@ constexpr int CHJ_WARPS = 8;
 template <int HD>
 __global__ void __launch_bounds__(CHJ_WARPS * 32) chunk_join_kernel(const AttendParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");   // the parts are complete
+  asm volatile("griddepcontrol.launch_dependents;");
   const int c0 = blockIdx.x;
   const int4 d = p.split[c0];
   if (d.x < 0) return;

@@ -77,19 +77,22 @@ int attend_nt(long long rows) {
   return static_cast<int>((rows + 8 * blocks - 1) / (8 * blocks));
 }
 
-// The join is set up while the kernel before it runs, and waits in the kernel for its end.
-int join_launch(void (*kernel)(rc::AttendParams), const rc::AttendParams& p, dim3 grid, int threads, cudaStream_t stream) {
+// A launch that may be set up while the kernel before it on the stream still runs; the kernel waits for that
+// one's end (griddepcontrol.wait) before it touches memory.
+int launch_behind(void (*kernel)(rc::AttendParams), const rc::AttendParams& p, dim3 grid, int threads, int smem,
+                  cudaStream_t stream) {
   cudaLaunchAttribute early;
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   early.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cfg.attrs = &early;
   cfg.numAttrs = 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
-  if (e != cudaSuccess) return cuda_fail(static_cast<int>(e), "cudaLaunchKernelEx(cache attention join)");
+  if (e != cudaSuccess) return cuda_fail(static_cast<int>(e), "cudaLaunchKernelEx(cache attention)");
   return launch_status();
 }
 
@@ -109,13 +112,13 @@ int attend_launch(const rc::AttendParams& p, DevInfo* di, cudaStream_t stream) {
                        rc::AttLayout<HD, NT>::bytes(rc::MAX_BATCH));
   if (st != RA_OK) return st;
   const int grid = rc::at_per_sm(NT) * (di->sm_count < rc::AT_MAX_SMS ? di->sm_count : rc::AT_MAX_SMS);
-  rc::attend_kernel<HD, NT><<<grid, rc::AT_THREADS, rc::AttLayout<HD, NT>::bytes(p.B), stream>>>(p);
-  if ((st = launch_status()) != RA_OK) return st;
+  st = launch_behind(rc::attend_kernel<HD, NT>, p, dim3(grid), rc::AT_THREADS, rc::AttLayout<HD, NT>::bytes(p.B), stream);
+  if (st != RA_OK) return st;
   // Few segments have many parts each: 16 warps a row instead of 4.  The whole call, 4 against 16: one segment of
   // 128K tokens (444 parts) 36.4 and 24.0 us; eight of them 53.7 and 54.5; 16 of 777 tokens 10.5 and 13.8.
   if (static_cast<long long>(p.B) * p.c.heads * p.n_blocks <= 4)
-    return join_launch(rc::join_kernel<HD, 8 * NT, 1, 16>, p, dim3(grid, 8 * NT), 512, stream);
-  return join_launch(rc::join_kernel<HD, 8 * NT, 2, 4>, p, dim3(grid, 4 * NT), 256, stream);
+    return launch_behind(rc::join_kernel<HD, 8 * NT, 1, 16>, p, dim3(grid, 8 * NT), 512, 0, stream);
+  return launch_behind(rc::join_kernel<HD, 8 * NT, 2, 4>, p, dim3(grid, 4 * NT), 256, 0, stream);
 }
 
 template <int HD>
@@ -124,9 +127,10 @@ int chunk_launch(const rc::AttendParams& p, DevInfo* di, cudaStream_t stream) {
                        rc::ChLayout<HD>::bytes(rc::MAX_BATCH));
   if (st != RA_OK) return st;
   const int grid = di->sm_count < rc::CH_MAX_CTAS ? di->sm_count : rc::CH_MAX_CTAS;
-  rc::chunk_kernel<HD><<<grid, rc::CH_THREADS, rc::ChLayout<HD>::bytes(p.B), stream>>>(p);
-  if ((st = launch_status()) != RA_OK) return st;
-  return join_launch(rc::chunk_join_kernel<HD>, p, dim3(grid, rc::CH_ROWS / 32, HD / 4 / rc::CHJ_WARPS), rc::CHJ_WARPS * 32, stream);
+  st = launch_behind(rc::chunk_kernel<HD>, p, dim3(grid), rc::CH_THREADS, rc::ChLayout<HD>::bytes(p.B), stream);
+  if (st != RA_OK) return st;
+  return launch_behind(rc::chunk_join_kernel<HD>, p, dim3(grid, rc::CH_ROWS / 32, HD / 4 / rc::CHJ_WARPS), rc::CHJ_WARPS * 32, 0,
+                       stream);
 }
 
 template <int HD>
