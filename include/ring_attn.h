@@ -315,7 +315,7 @@ RA_API int ring_attn_merge_ex(const float* o_parts, const float* lse_parts, int 
  *              dimension; q_strides = {in b, h, s, out b, h, s} in elements, host memory.  In place
  *              (same address and strides) is allowed, any other overlap of q and q_out is refused.
  *   k, k_out   the same with Hk heads, or NULL, NULL with Hk = 0.  q_out and k_out must not share
- *              elements (interleaved rows of one buffer are fine).
+ *              elements, nor lie over the other's input (interleaved rows of one buffer are fine).
  *   steps      [rot / 2] device, theta_i / (2 pi) in units of 2^-64 turn (mod 2^64): position * step
  *              mod 2^64 is the phase, exact at any position.
  *   rot        rotated columns, even, 2 .. Dh; Dh even, at most 1024.
@@ -407,8 +407,10 @@ RA_API int ring_attn_cache_read(const ra_cache* cache, int layer, const int* slo
  *             are left as they were; a query that sees nothing has o = 0, lse = -inf.
  *   workspace ring_attn_cache_attend_workspace_size bytes, 256-byte aligned, of this call alone while
  *             it runs; contents on entry do not matter.
- * exp(s - lse) is rounded to fp16 (11 bits) before it multiplies v; sums are float32.  Two
- * launches.
+ * o must not overlap q (RA_ERR_ARG).  exp(s - lse) is rounded to fp16 (11 bits) before it multiplies v, value
+ * scales are applied relative to the largest met (values below 2^-39 of a context's largest are lost to it);
+ * sums are float32.  Calls with 64 rows and more per head (T * Hq / heads) run on tcgen05.  Two launches; a
+ * bounded wait that gave up leaves RA_ERR_TIMEOUT in the device status word.
  */
 RA_API size_t ring_attn_cache_attend_workspace_size(int T, int Hq, int Hkv, int Dh);
 RA_API int ring_attn_cache_attend(const ra_cache* cache, int layer, const int* slots, const int* n_new, int B, int T,
@@ -473,7 +475,7 @@ RA_API unsigned long long ring_attn_launch_count(void);
 
 /*
  * ring_attn_device_status -- synchronises `stream`, returns the device status word
- * (RA_OK or the first RA_ERR_TIMEOUT a kernel recorded) and clears it.  Returns
+ * (RA_OK, or the first RA_ERR_TIMEOUT or RA_ERR_PAGES that a kernel recorded) and clears it.  Returns
  * RA_ERR_CUDA if the synchronisation itself fails.
  */
 RA_API int ring_attn_device_status(ra_stream stream);

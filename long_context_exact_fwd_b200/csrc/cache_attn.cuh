@@ -13,15 +13,17 @@
 // Numbers.  Codes are exact in fp16.  A query row is scaled by a power of two to just below fp16's
 // top and keeps its bf16 values exactly down to 2^-29 of the row's largest; scores and sums are
 // fp32.  exp uses a reference that is raised when a score passes it by 2^8; P is rounded to fp16
-// (half a step: 2^-12 relative) at 2^7 times its value, so terms down to 2^-21 of the largest keep
-// full precision and smaller ones an absolute 2^-32.  P carries the value scale of its page
+// (half a step, 2^-11 of the term; bf16's is 2^-8) at 2^7 times its value, so terms down to 2^-21 of the
+// largest keep all 11 bits and smaller ones an absolute 2^-32.  P carries the value scale of its page
 // relative to the largest met so far (a power of two); the sum for lse uses unrounded terms.
 //
 // Bound: memory, 2 Dh bytes per token and head.  Work is a line of 32-token tiles over (sequence,
 // head, row block); every block takes an equal stretch of it, whatever the lengths (they are only
 // known on the device), so stretches end inside sequences: such parts go to the workspace and a
-// second, small launch joins them.  Each warp streams its own tiles
-// with cp.async through a private ring in shared memory, no block barrier inside a stretch.
+// second, small launch joins them.  Each warp streams its own tiles with cp.async through a private
+// ring in shared memory, no block barrier inside a stretch (TMA boxes in its place: 7 % slower).
+// Measured on B200, 8 heads of 128, 4 query heads each: one context of 512K tokens 172 us, 95 % of a copy's
+// rate; 128K 53 us (77 %, some 11 us are start, join and launches); 32 of 16 to 16384 tokens 91 us (91 %).
 #pragma once
 #include "cache.cuh"
 

@@ -16,6 +16,9 @@
 //   w_j = 2^(x_j - ref + dv_j + 7),   l += 2^-(dv_j + 7) w_j,   dv_j = e_j - e_max <= 0.
 // Work is cut as in attend_kernel: one line of 128-key tiles over all items, equal stretches, parts
 // joined by chunk_join_kernel.
+// Bound: the products, and shared memory, which both operands of S, the tiles of V and the conversion go
+// through (about 320 KB a key tile; a tile takes some 4650 cycles, 2048 of them its products).  Measured on
+// B200, 16 query heads on 4 of 128, 2048 new tokens: at 16K tokens 312 us, 825 TFLOP/s; at 32K 585 us, 910.
 #pragma once
 #include "cache_attn.cuh"
 #include "cache_io.cuh"
@@ -42,7 +45,6 @@ struct alignas(16) ChScales {
   float rescale;     // what O has to be multiplied by for the new e_max (1: nothing)
   float unit;        // 2^(e_max - 7): true value of O's unit
   unsigned lots;     // of the tile's eight, those that have a page
-  unsigned pad;
 };
 
 template <int HD>

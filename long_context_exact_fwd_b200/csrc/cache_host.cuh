@@ -11,6 +11,9 @@ namespace {
 
 namespace rc = ra::cache;
 
+// Shared memory of the attention kernels set on this device: [Dh 128, Dh 64][8-row column blocks - 1, then chunks].
+std::atomic<bool> g_attend_set[MAX_DEVICES][2][4];
+
 // Checks the description of a cache and fills `p` with all layers' view; layer >= 0 picks one.
 int cache_pool(const ra_cache* c, int layer, rc::Pool* p) {
   if (!c || !c->k || !c->v || !c->k_scale || !c->v_scale || !c->table || !c->lens || !c->refs) return RA_ERR_ARG;
@@ -66,13 +69,14 @@ int copy_grid(const rc::Pool& c, long long pairs, int sm_count) {
 }
 
 // Which kernel a call's rows per kv head (T * g) take: 0 is chunk_kernel; otherwise attend_kernel with
-// blocks of 8 * nt rows, as few blocks as 24 rows allow and the narrowest that do.
-#ifndef RA_CHUNK_ROWS
-#define RA_CHUNK_ROWS 64
-#endif
+// blocks of 8 * nt rows, as few blocks as 24 rows allow and the narrowest that do.  Measured, attend_kernel
+// and chunk_kernel, 4 heads of 128: 16 contexts up to 4K, 48 rows 70 and 72 us, 64 rows 95 and 73, 128 rows 165
+// and 81; one context of 32K, 48 rows 37 and 40, 64 rows 45 and 41, 256 rows 103 and 46; one of 4K, where neither
+// is busy, 64 rows 22 and 27.
+constexpr int CHUNK_ROWS = 64;
 constexpr int AT_MAX_NT = 3;
 int attend_nt(long long rows) {
-  if (rows >= RA_CHUNK_ROWS) return 0;
+  if (rows >= CHUNK_ROWS) return 0;
   const long long blocks = (rows + 8 * AT_MAX_NT - 1) / (8 * AT_MAX_NT);
   return static_cast<int>((rows + 8 * blocks - 1) / (8 * blocks));
 }
@@ -108,7 +112,7 @@ int attend_smem(std::atomic<bool>& set, K kernel, int most) {
 
 template <int HD, int NT>
 int attend_launch(const rc::AttendParams& p, DevInfo* di, cudaStream_t stream) {
-  int st = attend_smem(di->attend_attr[HD == 128 ? 0 : 1][NT - 1], rc::attend_kernel<HD, NT>,
+  int st = attend_smem(g_attend_set[di - g_dev][HD == 128 ? 0 : 1][NT - 1], rc::attend_kernel<HD, NT>,
                        rc::AttLayout<HD, NT>::bytes(rc::MAX_BATCH));
   if (st != RA_OK) return st;
   const int grid = rc::at_per_sm(NT) * (di->sm_count < rc::AT_MAX_SMS ? di->sm_count : rc::AT_MAX_SMS);
@@ -123,7 +127,7 @@ int attend_launch(const rc::AttendParams& p, DevInfo* di, cudaStream_t stream) {
 
 template <int HD>
 int chunk_launch(const rc::AttendParams& p, DevInfo* di, cudaStream_t stream) {
-  int st = attend_smem(di->attend_attr[HD == 128 ? 0 : 1][AT_MAX_NT], rc::chunk_kernel<HD>,
+  int st = attend_smem(g_attend_set[di - g_dev][HD == 128 ? 0 : 1][AT_MAX_NT], rc::chunk_kernel<HD>,
                        rc::ChLayout<HD>::bytes(rc::MAX_BATCH));
   if (st != RA_OK) return st;
   const int grid = di->sm_count < rc::CH_MAX_CTAS ? di->sm_count : rc::CH_MAX_CTAS;
@@ -228,6 +232,12 @@ int ring_attn_cache_attend(const ra_cache* cache, int layer, const int* slots, c
   if (Hq % p.c.heads) return RA_ERR_SHAPE;
   if ((st = cache_rows(q, q_strides, B, Hq, T)) != RA_OK) return st;
   if (!aligned16(o) || reinterpret_cast<uintptr_t>(lse) % 4 || reinterpret_cast<uintptr_t>(n_new) % 4) return RA_ERR_ALIGN;
+  // rows are written while others' queries are still read: the output may not lie over the queries
+  const auto reach = [&](int i, int n) { return n > 1 ? q_strides[i] * (n - 1) : 0; };
+  const uintptr_t q0 = reinterpret_cast<uintptr_t>(q), o0 = reinterpret_cast<uintptr_t>(o);
+  const uintptr_t q1 = q0 + 2 * static_cast<uintptr_t>(reach(0, B) + reach(1, Hq) + reach(2, T) + p.c.Dh);
+  const uintptr_t o1 = o0 + static_cast<uintptr_t>(B) * Hq * T * p.c.Dh * (o_dtype == RA_F32 ? 4 : 2);
+  if (q0 < o1 && o0 < q1) return RA_ERR_ARG;
   p.g = Hq / p.c.heads;
   const long long rows = static_cast<long long>(T) * p.g;
   if (rows > INT_MAX / 2) return RA_ERR_SHAPE;

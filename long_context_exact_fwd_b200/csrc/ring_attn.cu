@@ -62,7 +62,6 @@ struct DevInfo {
   std::atomic<bool> fwd_attr[4] = {false, false, false, false};
   std::atomic<bool> bwd_attr[2] = {false, false};   // [HD 128, HD 64]
   std::atomic<bool> ffn_attr{false};
-  std::atomic<bool> attend_attr[2][4] = {};         // [Dh 128, Dh 64][8-row column blocks - 1, then chunks]
 };
 
 std::mutex g_dev_mu;

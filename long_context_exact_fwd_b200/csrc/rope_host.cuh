@@ -88,10 +88,8 @@ int rope_dispatch(ra::rope::Params& p, int sm_count, bool interleaved, cudaStrea
   }
   if (n == 4) return rope_launch<T, 4, true>(p, sm_count, interleaved, stream);
   if (n == 2) return rope_launch<T, 2, true>(p, sm_count, interleaved, stream);
-  // Nothing lines up: single elements (an interleaved pair is still one thread's; its partner
-  // columns and an even rest are two at a time).
-  if (interleaved && (p.Dh - p.rot) % 2 == 0) return rope_launch<T, 2, false>(p, sm_count, true, stream);
-  if (interleaved) return RA_ERR_SHAPE;   // unreachable: Dh is even
+  // Nothing lines up: element by element (an interleaved pair is still one thread's; rot and Dh are even).
+  if (interleaved) return rope_launch<T, 2, false>(p, sm_count, true, stream);
   return rope_launch<T, 1, false>(p, sm_count, false, stream);
 }
 

@@ -210,6 +210,7 @@ def test_cache_argument_errors(ra):
     expect("attend", ra.RA_ERR_ARG, dtype=3)
     expect("attend", ra.RA_ERR_ARG, o=0)
     expect("attend", ra.RA_ERR_ALIGN, lse=(1 << 26) + 2)
+    expect("attend", ra.RA_ERR_ARG, o=(1 << 20) + 256)                                  # the output over the queries
     for kw in (dict(ws=0), dict(ws=272), dict(size=64)):
         expect("reserve attend fork compact", ra.RA_ERR_WORKSPACE, **kw)
     if not torch.cuda.is_available():
