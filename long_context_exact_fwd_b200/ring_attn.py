@@ -1,6 +1,6 @@
 """ctypes binding of libringattn.so (include/ring_attn.h): argument marshalling only.
 
-Every step of the forward, backward and merge runs in the library's CUDA kernels; this
+Every step of the operations runs in the library's CUDA kernels; this
 module only checks tensor properties, allocates outputs with torch (device memory
 plumbing) and passes raw pointers plus the current CUDA stream.  There is no fallback:
 importing this module fails loudly when the library has not been built.
