@@ -69,8 +69,8 @@ struct AttLayout {
   static constexpr int SCALES = AT_WARPS * RING;       // [warp][stage][4] floats
   static constexpr int ML = SCALES + AT_WARPS * STAGES * 16;   // [warp][rows][2] floats, rows <= 32
   static constexpr int NANS = ML + AT_WARPS * 32 * 8;  // [HD] ints
-  static constexpr int PREFIX = NANS + HD * 4;         // [B + 1] ints, then slots [B], lengths [B]
-  static int bytes(int B) { return PREFIX + (3 * B + 1) * 4; }
+  static constexpr int PREFIX = NANS + HD * 4;         // [B + 1] ints, then slots, lengths, new tokens [B]
+  static int bytes(int B) { return PREFIX + (4 * B + 1) * 4; }
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool fill) {
@@ -84,17 +84,13 @@ template <int N>
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
-  return v;
+  return *reinterpret_cast<const uint4*>(__cvta_shared_to_generic(a));
 }
 __device__ __forceinline__ uint2 lds64(uint32_t a) {
-  uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
-  return v;
+  return *reinterpret_cast<const uint2*>(__cvta_shared_to_generic(a));
 }
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -157,7 +153,7 @@ __global__ void __launch_bounds__(AT_THREADS, at_per_sm(NT)) attend_kernel(const
   float* s_ml = reinterpret_cast<float*>(smem + L::ML);
   int* s_nan = reinterpret_cast<int*>(smem + L::NANS);
   int* s_prefix = reinterpret_cast<int*>(smem + L::PREFIX);
-  int *s_slot = s_prefix + p.B + 1, *s_len = s_slot + p.B;
+  int *s_slot = s_prefix + p.B + 1, *s_len = s_slot + p.B, *s_n = s_len + p.B;
   __shared__ int s_warp[AT_WARPS];
 
   asm volatile("griddepcontrol.wait;" ::: "memory");   // what ran before on the stream is complete
@@ -175,6 +171,7 @@ __global__ void __launch_bounds__(AT_THREADS, at_per_sm(NT)) attend_kernel(const
         if (ok && n > 0) w = (max(1, (len + AT_TILE - 1) / AT_TILE) + AT_START) * c.heads * p.n_blocks;
         s_slot[b] = slot;
         s_len[b] = len;
+        s_n[b] = n;
       } else if (slot != -1 && blockIdx.x == 0) {
         record_status(RA_ERR_PAGES);
       }
@@ -225,13 +222,31 @@ __global__ void __launch_bounds__(AT_THREADS, at_per_sm(NT)) attend_kernel(const
     const int t0 = max(0, x - seg0), t1 = min(nt, line1 - seg0);
     x = seg0 + nt;
     if (t0 >= t1) continue;                   // its tiles are the next block's
-    const int slot = s_slot[b], len = s_len[b], n = p.n_new ? p.n_new[b] : p.T;
+    const int slot = s_slot[b], len = s_len[b], n = s_n[b];
     const int row0 = rb * ROWS, rows = min(ROWS, n * p.g - row0);
     // keys that a row sees: its token's position + 1 (causal), or all
     auto limit_of = [&](int r) { return p.causal ? max(0, min(len, len - n + (row0 + r) / p.g + 1)) : len; };
     const int lim_min = rows > 0 ? limit_of(0) : 0;
     const int lim_max = rows > 0 ? limit_of(rows - 1) : 0;
     const int* table = c.table + static_cast<long long>(slot) * c.max_pages;
+
+    // ---- queries: column gr of block j is row j * 8 + gr, head columns gc * HD / 4 ..; loaded ahead of the
+    // page numbers, made fragments behind them
+    uint32_t raw[NT][KS * 2];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const int r = j * 8 + gr;
+      const int tt = (row0 + r) / p.g, hq = h * p.g + (row0 + r) - tt * p.g;
+      const uint4* src = reinterpret_cast<const uint4*>(p.q + b * p.qb + hq * p.qh + tt * p.qt + gc * (HD / 4));
+#pragma unroll
+      for (int i = 0; i < KS / 2; ++i) {
+        const uint4 v = r < rows ? src[i] : make_uint4(0, 0, 0, 0);
+        raw[j][4 * i] = v.x;
+        raw[j][4 * i + 1] = v.y;
+        raw[j][4 * i + 2] = v.z;
+        raw[j][4 * i + 3] = v.w;
+      }
+    }
 
     // ---- this warp's tiles: t0 + warp, + AT_WARPS, ...; those behind every row's limit are empty
     const int t_end = min(t1, (lim_max + AT_TILE - 1) / AT_TILE);
@@ -295,28 +310,12 @@ __global__ void __launch_bounds__(AT_THREADS, at_per_sm(NT)) attend_kernel(const
 #pragma unroll
     for (int i = 0; i < STAGES - 1; ++i) fetch(i);
 
-    // ---- queries as B fragments: column gr of block j is row j * 8 + gr, head columns gc * HD / 4 ..
-    uint32_t qf[NT][KS][2];
+    uint32_t qf[NT][KS][2];                   // B fragments
     float row_scale[NT][2];                   // of the accumulator's columns 2 gc, 2 gc + 1
     int limit[NT][2];
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-      const int r = j * 8 + gr;
-      uint32_t w[KS * 2];
-#pragma unroll
-      for (int i = 0; i < KS * 2; ++i) w[i] = 0;
-      if (r < rows) {
-        const int tt = (row0 + r) / p.g, hq = h * p.g + (row0 + r) % p.g;
-        const uint4* src = reinterpret_cast<const uint4*>(p.q + b * p.qb + hq * p.qh + tt * p.qt + gc * (HD / 4));
-#pragma unroll
-        for (int i = 0; i < KS / 2; ++i) {
-          const uint4 v = src[i];
-          w[4 * i] = v.x;
-          w[4 * i + 1] = v.y;
-          w[4 * i + 2] = v.z;
-          w[4 * i + 3] = v.w;
-        }
-      }
+      const uint32_t (&w)[KS * 2] = raw[j];
       float amax = 0.f;
 #pragma unroll
       for (int i = 0; i < KS * 2; ++i) {
@@ -599,31 +598,32 @@ __global__ void __launch_bounds__(LOT * WARPS * 32) join_kernel(const AttendPara
   const int n = c1 - c0 + 1;
   float m = -INFINITY, z = 0.f;
   float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int k0 = w; k0 < n; k0 += 32 * WARPS) {   // 32 parts of this warp at a time, one per lane
-    const int k = k0 + lane * WARPS;
-    const float2 ml = k < n ? *reinterpret_cast<const float2*>(part(k) + HD) : make_float2(-INFINITY, 0.f);
-    float mk = ml.x;
+  constexpr int AT_ONCE = WARPS >= 16 ? 16 : 8;   // parts read together, statistics and all
+  for (int k0 = w; k0 < n; k0 += AT_ONCE * WARPS) {
+    float2 ml[AT_ONCE];
+    float4 y[AT_ONCE];
 #pragma unroll
-    for (int i = 16; i; i >>= 1) mk = fmaxf(mk, __shfl_xor_sync(0xffffffffu, mk, i));
-    mk = fmaxf(mk, m);
-    const float old = m == mk ? 1.f : ex2_approx(m - mk);   // nothing yet: 0, or both -inf
-    m = mk;
+    for (int i = 0; i < AT_ONCE; ++i) {
+      const int k = k0 + i * WARPS;
+      ml[i] = make_float2(-INFINITY, 0.f);
+      if (k < n) {
+        ml[i] = *reinterpret_cast<const float2*>(part(k) + HD);
+        if (lane < GROUPS) y[i] = *reinterpret_cast<const float4*>(part(k) + 4 * lane);
+      }
+    }
+    float top = m;
+#pragma unroll
+    for (int i = 0; i < AT_ONCE; ++i) top = fmaxf(top, ml[i].x);
+    const float old = m == top ? 1.f : ex2_approx(m - top);   // nothing yet: 0, or both -inf
+    m = top;
     z *= old;
     a = make_float4(a.x * old, a.y * old, a.z * old, a.w * old);
-    const float f = ml.y == 0.f ? 0.f : (ml.x == m ? 1.f : ex2_approx(ml.x - m));
-    const unsigned seen = __ballot_sync(0xffffffffu, ml.y != 0.f);
-    float zs = ml.y == 0.f ? 0.f : ml.y * f;
 #pragma unroll
-    for (int i = 16; i; i >>= 1) zs += __shfl_xor_sync(0xffffffffu, zs, i);
-    z += zs;
-    const int here = min(32, (n - k0 + WARPS - 1) / WARPS);
-#pragma unroll 8
-    for (int j = 0; j < here; ++j) {
-      const float fj = __shfl_sync(0xffffffffu, f, j);
-      if (lane < GROUPS && (seen >> j & 1u)) {
-        const float4 y = *reinterpret_cast<const float4*>(part(k0 + j * WARPS) + 4 * lane);
-        a = make_float4(fmaf(y.x, fj, a.x), fmaf(y.y, fj, a.y), fmaf(y.z, fj, a.z), fmaf(y.w, fj, a.w));
-      }
+    for (int i = 0; i < AT_ONCE; ++i) {
+      if (ml[i].y == 0.f) continue;           // saw nothing, or no part
+      const float f = ml[i].x == m ? 1.f : ex2_approx(ml[i].x - m);
+      z += ml[i].y * f;
+      a = make_float4(fmaf(y[i].x, f, a.x), fmaf(y[i].y, f, a.y), fmaf(y[i].z, f, a.z), fmaf(y[i].w, f, a.w));
     }
   }
   if (lane < GROUPS) s_o[rr][w][lane] = a;
