@@ -54,7 +54,10 @@ struct AttendParams {
   void* o;                     // [B][Hq][T][Dh] bf16 (or fp32)
   float* lse;                  // [B][Hq][T]
   float* part;                 // [2 * CTAs][8 NT rows][Dh + 4]: O, then m and l
-  int4* split;                 // [CTAs] the segment that starts in a block and ends in another
+  // What is to be joined: a segment's last and first block, and b, h * n_blocks + row block; last < 0: nothing.
+  // By segment ([B * heads * n_blocks]) if there are few, else by the block it starts in ([CTAs]).
+  int4* split;
+  int by_segment;
   int B, T, g, n_blocks;       // row blocks per (sequence, head)
   int page_shift, causal, o_f32;
   float scale_log2;
@@ -176,6 +179,8 @@ __global__ void __launch_bounds__(AT_THREADS, at_per_sm(NT)) attend_kernel(const
         record_status(RA_ERR_PAGES);
       }
     }
+    if (p.by_segment && blockIdx.x == 0 && b < p.B && w == 0)   // nobody comes by these
+      for (int i = 0; i < c.heads * p.n_blocks; ++i) p.split[b * c.heads * p.n_blocks + i] = make_int4(-1, 0, 0, 0);
     // block prefix sum
     int s = w;
 #pragma unroll
@@ -562,18 +567,22 @@ __global__ void __launch_bounds__(AT_THREADS, at_per_sm(NT)) attend_kernel(const
         if (d == 0) *reinterpret_cast<float2*>(row + HD) = make_float2(m, z);
       }
     }
-    if (!whole && static_cast<int>(blockIdx.x) == c0) mine_split = make_int4(c1, b, h, rb);
+    if (static_cast<int>(blockIdx.x) == c0) {
+      const int4 joined = make_int4(whole ? -1 : c1, c0, b, seg);
+      if (!p.by_segment) mine_split = joined;   // a segment that ends here does not hide one that does not: it comes first
+      else if (threadIdx.x == 0) p.split[b * c.heads * p.n_blocks + seg] = joined;
+    }
     __syncthreads();                          // rings and s_nan are free again
     if (lim_max > lim_min) {
       for (int i = threadIdx.x; i < HD; i += AT_THREADS) s_nan[i] = INT_MAX;
       __syncthreads();
     }
   }
-  if (threadIdx.x == 0) p.split[blockIdx.x] = mine_split;
+  if (!p.by_segment && threadIdx.x == 0) p.split[blockIdx.x] = mine_split;
 }
 
-// Joins the parts of the segments that the kernel before left split: block (c, j) has rows LOT j .. of the
-// segment that starts in its block c, WARPS warps a row, each lane 4 columns of every WARPS-th part.  Parts
+// Joins the parts of the segments that the kernel before left split: block (i, j) has rows LOT j .. of the
+// i-th entry's segment, WARPS warps a row, each lane 4 columns of every WARPS-th part.  Parts
 // are added in an order that only the lengths fix.  Bound: latency of three dependent reads; one block
 // alone doing this at the end of its stretch cost 0.6 us per part.
 template <int HD, int ROWS, int LOT, int WARPS>
@@ -583,11 +592,11 @@ __global__ void __launch_bounds__(LOT * WARPS * 32) join_kernel(const AttendPara
   __shared__ float2 s_ml[LOT][WARPS];
   asm volatile("griddepcontrol.wait;" ::: "memory");   // the parts are complete
   asm volatile("griddepcontrol.launch_dependents;");
-  const int c0 = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int4 d = p.split[c0];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int4 d = p.split[blockIdx.x];
   if (d.x < 0) return;
-  const int c1 = d.x, b = d.y, h = d.z;
-  const int row0 = d.w * ROWS, rows = min(ROWS, (p.n_new ? p.n_new[b] : p.T) * p.g - row0);
+  const int c1 = d.x, c0 = d.y, b = d.z, h = d.w / p.n_blocks;
+  const int row0 = (d.w - h * p.n_blocks) * ROWS, rows = min(ROWS, (p.n_new ? p.n_new[b] : p.T) * p.g - row0);
   const int rr = warp / WARPS, w = warp % WARPS;
   const int r = blockIdx.y * LOT + rr;
   const long long step = 2ll * ROWS * (HD + 4);

@@ -573,7 +573,7 @@ __device__ void ch_softmax(int t, const AttendParams& p, ChWalk w, int per, uint
     // ---- epilogue
     const bool whole = w.t0 == 0 && w.t1 == w.nt;
     const int c0 = w.first / per, c1 = (w.first + w.nt - 1) / per;
-    if (!whole && static_cast<int>(blockIdx.x) == c0 && threadIdx.x == 0) p.split[blockIdx.x] = make_int4(c1, w.b, w.h, w.i);
+    if (!whole && static_cast<int>(blockIdx.x) == c0 && threadIdx.x == 0) p.split[blockIdx.x] = make_int4(c1, c0, w.b, w.h * p.n_blocks + w.i);
     int* nans = reinterpret_cast<int*>(smem + L::NAN_OFF) + (piece * 8 + (threadIdx.x >> 5)) * (HD + 4);
     const bool any_nan = *reinterpret_cast<volatile int*>(nans + HD) != 0;
     const int gr = row0 + r, tt = gr / p.g, hq = w.h * p.g + gr - tt * p.g;
@@ -788,10 +788,9 @@ template <int HD>
 __global__ void __launch_bounds__(CHJ_WARPS * 32) chunk_join_kernel(const AttendParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");   // the parts are complete
   asm volatile("griddepcontrol.launch_dependents;");
-  const int c0 = blockIdx.x;
-  const int4 d = p.split[c0];
+  const int4 d = p.split[blockIdx.x];
   if (d.x < 0) return;
-  const int n = d.x - c0 + 1, b = d.y, h = d.z, row0 = d.w * CH_ROWS;
+  const int c0 = d.y, n = d.x - c0 + 1, b = d.z, h = d.w / p.n_blocks, row0 = (d.w - h * p.n_blocks) * CH_ROWS;
   const int r = blockIdx.y * 32 + (threadIdx.x & 31), group = blockIdx.z * CHJ_WARPS + (threadIdx.x >> 5);
   if (r >= min(CH_ROWS, (p.n_new ? p.n_new[b] : p.T) * p.g - row0)) return;
   constexpr long long PART = static_cast<long long>(CH_ROWS) * (HD / 4 + 1);

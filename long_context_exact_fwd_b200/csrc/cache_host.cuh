@@ -74,6 +74,10 @@ int copy_grid(const rc::Pool& c, long long pairs, int sm_count) {
 // and 81; one context of 32K, 48 rows 37 and 40, 64 rows 45 and 41, 256 rows 103 and 46; one of 4K, where neither
 // is busy, 64 rows 22 and 27.
 constexpr int CHUNK_ROWS = 64;
+// Calls of so few segments join them with a block per row and 16 warps (4 warps a row otherwise).  Measured, 16
+// warps and 4: one segment of 128K tokens (444 parts) 17.7 and 27.4 us, eight of them 49.9 and 51.5, eight of 8K
+// 12.4 and 12.1, 16 of 777 11.2 and 9.9.
+constexpr int FEW_SEGMENTS = 8;
 constexpr int AT_MAX_NT = 3;
 int attend_nt(long long rows) {
   if (rows >= CHUNK_ROWS) return 0;
@@ -118,10 +122,8 @@ int attend_launch(const rc::AttendParams& p, DevInfo* di, cudaStream_t stream) {
   const int grid = rc::at_per_sm(NT) * (di->sm_count < rc::AT_MAX_SMS ? di->sm_count : rc::AT_MAX_SMS);
   st = launch_behind(rc::attend_kernel<HD, NT>, p, dim3(grid), rc::AT_THREADS, rc::AttLayout<HD, NT>::bytes(p.B), stream);
   if (st != RA_OK) return st;
-  // Few segments have many parts each: 16 warps a row instead of 4.  The whole call, 4 against 16: one segment of
-  // 128K tokens (444 parts) 36.4 and 24.0 us; eight of them 53.7 and 54.5; 16 of 777 tokens 10.5 and 13.8.
-  if (static_cast<long long>(p.B) * p.c.heads * p.n_blocks <= 4)
-    return launch_behind(rc::join_kernel<HD, 8 * NT, 1, 16>, p, dim3(grid, 8 * NT), 512, 0, stream);
+  if (p.by_segment)   // few segments, many parts each: a block per row, 16 warps
+    return launch_behind(rc::join_kernel<HD, 8 * NT, 1, 16>, p, dim3(p.B * p.c.heads * p.n_blocks, 8 * NT), 512, 0, stream);
   return launch_behind(rc::join_kernel<HD, 8 * NT, 2, 4>, p, dim3(grid, 4 * NT), 256, 0, stream);
 }
 
@@ -245,6 +247,8 @@ int ring_attn_cache_attend(const ra_cache* cache, int layer, const int* slots, c
   // rows per block, and the line of places, which is numbered in int
   const int block = nt ? 8 * nt : rc::CH_ROWS, tile = nt ? rc::AT_TILE : rc::CH_BN, start = nt ? rc::AT_START : rc::CH_START;
   p.n_blocks = static_cast<int>((rows + block - 1) / block);
+  // up to so many segments, each is likely split: one entry per segment, and the wide join
+  p.by_segment = static_cast<long long>(B) * p.c.heads * p.n_blocks <= FEW_SEGMENTS;
   const double places = std::ceil(static_cast<double>(p.c.max_pages) * p.c.page / tile) + start;
   if (places * p.c.heads * p.n_blocks * B > INT_MAX / 2) return RA_ERR_SHAPE;
   if ((st = pages_check_ws(workspace, workspace_bytes, ring_attn_cache_attend_workspace_size(T, Hq, p.c.heads, p.c.Dh))) != RA_OK)
