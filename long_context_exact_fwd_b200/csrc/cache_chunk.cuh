@@ -238,11 +238,12 @@ __device__ void ch_convert(const AttendParams& p, ChWalk w, uint8_t* smem, uint3
 
     // ---- K and V tiles: HD / 16 lanes a token, 16 codes a lane, AT_ONCE tokens a warp step
     constexpr int LANES = HD / 16, AT_ONCE = 32 / LANES, STEPS = CH_BN / (AT_ONCE * CH_CONV_WARPS);
-    const int col = lane % LANES, tok = cw * AT_ONCE + lane / LANES, sub = col >> 2, c4 = col & 3;
-    // Token t's row of a 64-column block lies at t * 128, its 16-byte chunks exchanged by t & 7.  The
-    // lanes of the second block write their two chunks in the other order, so that eight lanes of one
-    // token meet all banks.
-    const int at0 = ((2 * c4 + sub) ^ (tok & 7)) << 4, at1 = ((2 * c4 + 1 - sub) ^ (tok & 7)) << 4;
+    // HD 128: half a warp has the tokens' first 64 columns, the other half their second
+    const int sub = HD == 128 ? lane >> 4 : 0, tok = cw * AT_ONCE + ((lane >> 2) & (AT_ONCE - 1)), c4 = lane & 3;
+    const int col = sub * 4 + c4;
+    // Token t's row of a 64-column block lies at t * 128, its 16-byte chunks exchanged by t & 7: the eight
+    // threads of a phase (two tokens, four lanes each) meet all banks.
+    const int at0 = ((2 * c4) ^ (tok & 7)) << 4, at1 = ((2 * c4 + 1) ^ (tok & 7)) << 4;
     static_assert(AT_ONCE * CH_CONV_WARPS % 8 == 0, "a lane's tokens share their place in the swizzle");
     for (int tile = w.t0; tile < w.t1; ++tile) {
       const int tok0 = tile * CH_BN;
@@ -291,8 +292,8 @@ __device__ void ch_convert(const AttendParams& p, ChWalk w, uint8_t* smem, uint3
                 codes_to_half2(static_cast<uint16_t>(x[k].z)), codes_to_half2(static_cast<uint16_t>(x[k].z >> 16)),
                 codes_to_half2(static_cast<uint16_t>(x[k].w)), codes_to_half2(static_cast<uint16_t>(x[k].w >> 16)));
             uint8_t* row = dst + (k0 + k) * (AT_ONCE * CH_CONV_WARPS) * 128;
-            *reinterpret_cast<uint4*>(row + at0) = HD == 128 && sub ? hi : lo;
-            *reinterpret_cast<uint4*>(row + at1) = HD == 128 && sub ? lo : hi;
+            *reinterpret_cast<uint4*>(row + at0) = lo;
+            *reinterpret_cast<uint4*>(row + at1) = hi;
           }
         }
         // A NaN among values that some rows of the item do not see must not reach them through 0 * NaN:
