@@ -32,9 +32,11 @@ namespace cache {
 
 constexpr int AT_WARPS = 4;
 // Blocks per SM (one joins its warps while the others stream) and stages of a warp's ring, by the
-// registers that NT takes.  Measured (32 contexts up to 16K, NT 1 / 16 contexts, 16 rows, NT 2): 2 blocks
-// of 3 stages 98.9 / 51.7 us, 3 of 2 94.8 / 57.8 (spills).
-__host__ __device__ constexpr int at_per_sm(int nt) { return nt == 1 ? 3 : 2; }
+// registers that NT and the head take.  Measured, heads of 128 (32 contexts up to 16K, NT 1 / 16 contexts,
+// 16 rows, NT 2): 2 blocks of 3 stages 98.9 / 51.7 us, 3 of 2 94.8 / 57.8 (spills).  Heads of 64 take fewer
+// registers, and one block more beats the widest register split (16 contexts up to 64K, NT 1 / 2 / 3):
+// 58.9 / 87.5 / 103.8 us -> 57.6 / 76.5 / 94.9; short contexts (5K) as they were, within 3 %.
+__host__ __device__ constexpr int at_per_sm(int hd, int nt) { return (nt == 1 ? 3 : 2) + (hd == 64 ? 1 : 0); }
 __host__ __device__ constexpr int at_stages(int nt) { return nt == 1 ? 2 : 3; }
 constexpr int AT_THREADS = AT_WARPS * 32;
 constexpr int AT_TILE = 32;          // tokens of a warp's tile
@@ -42,7 +44,9 @@ constexpr int AT_MAX_SMS = 160;      // SMs that the workspace has room for
 // What starting and joining a stretch costs, in tiles: it counts in a block's share.  Measured for 32
 // contexts of 16 to 16384 tokens, 8 heads: 0 115.8 us, 8 102.2, 16 98.7, 24 100.4.
 constexpr int AT_START = 16;
-constexpr int AT_LEAST = 8;          // tiles of a stretch, at least
+// Tiles of a stretch, at least: one a warp.  Measured (one context of 777 / 8192 tokens): 4 9.1 / 12.0 us,
+// 8 10.0 / 12.4, 16 12.1 / 13.7.
+constexpr int AT_LEAST = 4;
 constexpr float AT_RAISE = 8.f;      // log2: P <= 2^8, times 2^7 still an fp16 number
 constexpr float AT_P_UNIT = 128.f;
 
@@ -142,7 +146,7 @@ __device__ __forceinline__ void store_row(const AttendParams& p, int b, int h, i
 }
 
 template <int HD, int NT>
-__global__ void __launch_bounds__(AT_THREADS, at_per_sm(NT)) attend_kernel(const AttendParams p) {
+__global__ void __launch_bounds__(AT_THREADS, at_per_sm(HD, NT)) attend_kernel(const AttendParams p) {
   using L = AttLayout<HD, NT>;
   constexpr int ROWS = 8 * NT, STAGES = L::STAGES;
   constexpr int KS = HD / 16;          // k steps of a score, and 16-column blocks of a head

@@ -119,7 +119,7 @@ int attend_launch(const rc::AttendParams& p, DevInfo* di, cudaStream_t stream) {
   int st = attend_smem(g_attend_set[di - g_dev][HD == 128 ? 0 : 1][NT - 1], rc::attend_kernel<HD, NT>,
                        rc::AttLayout<HD, NT>::bytes(rc::MAX_BATCH));
   if (st != RA_OK) return st;
-  const int grid = rc::at_per_sm(NT) * (di->sm_count < rc::AT_MAX_SMS ? di->sm_count : rc::AT_MAX_SMS);
+  const int grid = rc::at_per_sm(HD, NT) * (di->sm_count < rc::AT_MAX_SMS ? di->sm_count : rc::AT_MAX_SMS);
   st = launch_behind(rc::attend_kernel<HD, NT>, p, dim3(grid), rc::AT_THREADS, rc::AttLayout<HD, NT>::bytes(p.B), stream);
   if (st != RA_OK) return st;
   if (p.by_segment)   // few segments, many parts each: a block per row, 16 warps
@@ -148,7 +148,7 @@ int attend_dispatch(int nt, const rc::AttendParams& p, DevInfo* di, cudaStream_t
 }
 
 size_t attend_part_bytes(int nt, int Dh) {
-  const size_t parts = nt ? 2ull * rc::at_per_sm(nt) * rc::AT_MAX_SMS * 8 * nt : 2ull * rc::CH_MAX_CTAS * rc::CH_ROWS;
+  const size_t parts = nt ? 2ull * rc::at_per_sm(Dh, nt) * rc::AT_MAX_SMS * 8 * nt : 2ull * rc::CH_MAX_CTAS * rc::CH_ROWS;
   return align256(parts * (Dh + 4) * sizeof(float));
 }
 
@@ -219,7 +219,7 @@ int ring_attn_cache_read(const ra_cache* cache, int layer, const int* slots, con
 size_t ring_attn_cache_attend_workspace_size(int T, int Hq, int Hkv, int Dh) {
   if (T <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || (Dh != 64 && Dh != 128)) return 0;
   const int nt = attend_nt(static_cast<long long>(T) * (Hq / Hkv));
-  return attend_part_bytes(nt, Dh) + align256(3 * rc::AT_MAX_SMS * sizeof(int4))   /* blocks: at_per_sm per SM, at most 3 */;
+  return attend_part_bytes(nt, Dh) + align256(4 * rc::AT_MAX_SMS * sizeof(int4))   /* blocks: at_per_sm per SM, at most 4 */;
 }
 
 int ring_attn_cache_attend(const ra_cache* cache, int layer, const int* slots, const int* n_new, int B, int T, int Hq,
