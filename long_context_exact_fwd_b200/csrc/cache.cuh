@@ -61,6 +61,13 @@ __device__ __forceinline__ uint32_t floats_to_codes(float lo, float hi) {
   return r;
 }
 
+// What ran before on the stream is complete; the next launch may be set up from here on.  First in every kernel, on
+// every path: a block that ended without waiting would let a later launch pass an unfinished one.
+__device__ __forceinline__ void behind_last() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
+}
+
 // Whether an earlier entry of the batch names the same slot (the whole block asks; barrier inside).
 __device__ __forceinline__ bool named_before(const int* slots, int b, int slot) {
   bool dup = false;

@@ -85,10 +85,10 @@ int attend_nt(long long rows) {
   return static_cast<int>((rows + 8 * blocks - 1) / (8 * blocks));
 }
 
-// A launch that may be set up while the kernel before it on the stream still runs; the kernel waits for that
-// one's end (griddepcontrol.wait) before it touches memory.
-int launch_behind(void (*kernel)(rc::AttendParams), const rc::AttendParams& p, dim3 grid, int threads, int smem,
-                  cudaStream_t stream) {
+// A launch that may be set up while the kernel before it on the stream still runs; every kernel of the cache
+// waits for that one's end (behind_last) before it touches memory.
+template <typename... P, typename... A>
+int launch_behind(void (*kernel)(P...), dim3 grid, int threads, int smem, cudaStream_t stream, A... args) {
   cudaLaunchAttribute early;
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   early.val.programmaticStreamSerializationAllowed = 1;
@@ -99,8 +99,8 @@ int launch_behind(void (*kernel)(rc::AttendParams), const rc::AttendParams& p, d
   cfg.stream = stream;
   cfg.attrs = &early;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
-  if (e != cudaSuccess) return cuda_fail(static_cast<int>(e), "cudaLaunchKernelEx(cache attention)");
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+  if (e != cudaSuccess) return cuda_fail(static_cast<int>(e), "cudaLaunchKernelEx(cache)");
   return launch_status();
 }
 
@@ -120,11 +120,11 @@ int attend_launch(const rc::AttendParams& p, DevInfo* di, cudaStream_t stream) {
                        rc::AttLayout<HD, NT>::bytes(rc::MAX_BATCH));
   if (st != RA_OK) return st;
   const int grid = rc::at_per_sm(HD, NT) * (di->sm_count < rc::AT_MAX_SMS ? di->sm_count : rc::AT_MAX_SMS);
-  st = launch_behind(rc::attend_kernel<HD, NT>, p, dim3(grid), rc::AT_THREADS, rc::AttLayout<HD, NT>::bytes(p.B), stream);
+  st = launch_behind(rc::attend_kernel<HD, NT>, dim3(grid), rc::AT_THREADS, rc::AttLayout<HD, NT>::bytes(p.B), stream, p);
   if (st != RA_OK) return st;
   if (p.by_segment)   // few segments, many parts each: a block per row, 16 warps
-    return launch_behind(rc::join_kernel<HD, 8 * NT, 1, 16>, p, dim3(p.B * p.c.heads * p.n_blocks, 8 * NT), 512, 0, stream);
-  return launch_behind(rc::join_kernel<HD, 8 * NT, 2, 4>, p, dim3(grid, 4 * NT), 256, 0, stream);
+    return launch_behind(rc::join_kernel<HD, 8 * NT, 1, 16>, dim3(p.B * p.c.heads * p.n_blocks, 8 * NT), 512, 0, stream, p);
+  return launch_behind(rc::join_kernel<HD, 8 * NT, 2, 4>, dim3(grid, 4 * NT), 256, 0, stream, p);
 }
 
 template <int HD>
@@ -133,10 +133,10 @@ int chunk_launch(const rc::AttendParams& p, DevInfo* di, cudaStream_t stream) {
                        rc::ChLayout<HD>::bytes(rc::MAX_BATCH));
   if (st != RA_OK) return st;
   const int grid = di->sm_count < rc::CH_MAX_CTAS ? di->sm_count : rc::CH_MAX_CTAS;
-  st = launch_behind(rc::chunk_kernel<HD>, p, dim3(grid), rc::CH_THREADS, rc::ChLayout<HD>::bytes(p.B), stream);
+  st = launch_behind(rc::chunk_kernel<HD>, dim3(grid), rc::CH_THREADS, rc::ChLayout<HD>::bytes(p.B), stream, p);
   if (st != RA_OK) return st;
-  return launch_behind(rc::chunk_join_kernel<HD>, p, dim3(grid, rc::CH_ROWS / 32, HD / 4 / rc::CHJ_WARPS), rc::CHJ_WARPS * 32, 0,
-                       stream);
+  return launch_behind(rc::chunk_join_kernel<HD>, dim3(grid, rc::CH_ROWS / 32, HD / 4 / rc::CHJ_WARPS), rc::CHJ_WARPS * 32, 0,
+                       stream, p);
 }
 
 template <int HD>
@@ -187,8 +187,7 @@ int ring_attn_cache_append(const ra_cache* cache, int layer, const int* slots, c
                                      : units <= 4 * rc::AP_THREADS ? rc::append_kernel<4>
                                      : units <= 8 * rc::AP_THREADS ? rc::append_kernel<8>
                                                                    : rc::append_kernel<16>;
-  kernel<<<grid, rc::AP_THREADS, 0, s>>>(p);
-  return launch_status();
+  return launch_behind(kernel, grid, rc::AP_THREADS, 0, s, p);
 }
 
 int ring_attn_cache_read(const ra_cache* cache, int layer, const int* slots, const int* start, int B, int length,
@@ -209,11 +208,7 @@ int ring_attn_cache_read(const ra_cache* cache, int layer, const int* slots, con
   const int per_block = rc::READ_UNITS * rc::IO_THREADS * rc::UNIT / p.c.Dh;   // tokens
   const dim3 grid((length + static_cast<long long>(per_block) - 1) / per_block, p.c.heads, 2 * B);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (p.c.Dh == 128)
-    rc::read_kernel<128><<<grid, rc::IO_THREADS, 0, s>>>(p);
-  else
-    rc::read_kernel<64><<<grid, rc::IO_THREADS, 0, s>>>(p);
-  return launch_status();
+  return launch_behind(p.c.Dh == 128 ? rc::read_kernel<128> : rc::read_kernel<64>, grid, rc::IO_THREADS, 0, s, p);
 }
 
 size_t ring_attn_cache_attend_workspace_size(int T, int Hq, int Hkv, int Dh) {
@@ -294,10 +289,10 @@ int ring_attn_cache_reserve(const ra_cache* cache, const int* slots, const int* 
   rc::Plan* plan = static_cast<rc::Plan*>(workspace);
   int* pairs = reinterpret_cast<int*>(static_cast<char*>(workspace) + align256(sizeof(rc::Plan)));
   int* free_list = pairs + 2 * B;
-  rc::reserve_plan_kernel<<<1, rc::PLAN_THREADS, 0, s>>>(c, slots, n_new, B, plan, pairs, free_list);
-  if ((st = launch_status()) != RA_OK) return st;
-  rc::copy_pages_kernel<<<copy_grid(c, B, di->sm_count), rc::COPY_THREADS, 0, s>>>(c, plan, pairs, pairs + 1, 2, nullptr);
-  return launch_status();
+  st = launch_behind(rc::reserve_plan_kernel, dim3(1), rc::PLAN_THREADS, 0, s, c, slots, n_new, B, plan, pairs, free_list);
+  if (st != RA_OK) return st;
+  return launch_behind(rc::copy_pages_kernel, dim3(copy_grid(c, B, di->sm_count)), rc::COPY_THREADS, 0, s, c, plan, pairs,
+                       pairs + 1, 2, nullptr);
 }
 
 int ring_attn_cache_fork(const ra_cache* cache, const int* src, const int* dst, int B, void* workspace,
@@ -312,13 +307,12 @@ int ring_attn_cache_fork(const ra_cache* cache, const int* src, const int* dst, 
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   rc::Plan* plan = static_cast<rc::Plan*>(workspace);
   int* first = reinterpret_cast<int*>(static_cast<char*>(workspace) + align256(sizeof(rc::Plan)));
-  rc::fork_plan_kernel<<<1, rc::PLAN_THREADS, 0, s>>>(c, src, dst, B, plan, first);
-  if ((st = launch_status()) != RA_OK) return st;
+  st = launch_behind(rc::fork_plan_kernel, dim3(1), rc::PLAN_THREADS, 0, s, c, src, dst, B, plan, first);
+  if (st != RA_OK) return st;
   const long long items = static_cast<long long>(B) * c.max_pages;
   const long long blocks = (items + rc::COPY_THREADS - 1) / rc::COPY_THREADS;
   const int grid = static_cast<int>(blocks < 2ll * di->sm_count ? blocks : 2ll * di->sm_count);
-  rc::fork_apply_kernel<<<grid, rc::COPY_THREADS, 0, s>>>(c, src, dst, plan, first);
-  return launch_status();
+  return launch_behind(rc::fork_apply_kernel, dim3(grid), rc::COPY_THREADS, 0, s, c, src, dst, plan, first);
 }
 
 int ring_attn_cache_trim(const ra_cache* cache, const int* slots, const int* keep, int B, ra_stream stream) {
@@ -328,8 +322,7 @@ int ring_attn_cache_trim(const ra_cache* cache, const int* slots, const int* kee
   if ((st = cache_batch(slots, B)) != RA_OK) return st;
   if (reinterpret_cast<uintptr_t>(keep) % 4) return RA_ERR_ALIGN;
   if (!dev_info(&st)) return st;
-  rc::trim_kernel<<<B, rc::COPY_THREADS, 0, static_cast<cudaStream_t>(stream)>>>(c, slots, keep, B);
-  return launch_status();
+  return launch_behind(rc::trim_kernel, dim3(B), rc::COPY_THREADS, 0, static_cast<cudaStream_t>(stream), c, slots, keep, B);
 }
 
 int ring_attn_cache_compact(const ra_cache* cache, void* workspace, size_t workspace_bytes, ra_stream stream) {
@@ -343,11 +336,10 @@ int ring_attn_cache_compact(const ra_cache* cache, void* workspace, size_t works
   rc::Plan* plan = static_cast<rc::Plan*>(workspace);
   int* holes = reinterpret_cast<int*>(static_cast<char*>(workspace) + align256(sizeof(rc::Plan)));
   int *movers = holes + c.pages, *moved_to = movers + c.pages;
-  rc::compact_plan_kernel<<<1, rc::PLAN_THREADS, 0, s>>>(c, plan, holes, movers, moved_to);
-  if ((st = launch_status()) != RA_OK) return st;
+  st = launch_behind(rc::compact_plan_kernel, dim3(1), rc::PLAN_THREADS, 0, s, c, plan, holes, movers, moved_to);
+  if (st != RA_OK) return st;
   const int grid = copy_grid(c, c.pages / 2 + 1, di->sm_count);
-  rc::copy_pages_kernel<<<grid, rc::COPY_THREADS, 0, s>>>(c, plan, movers, holes, 1, moved_to);
-  return launch_status();
+  return launch_behind(rc::copy_pages_kernel, dim3(grid), rc::COPY_THREADS, 0, s, c, plan, movers, holes, 1, moved_to);
 }
 
 }  // extern "C"

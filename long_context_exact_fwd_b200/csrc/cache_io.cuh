@@ -71,6 +71,7 @@ __device__ __forceinline__ uint32_t restate4(uint32_t codes, float f) {
 constexpr int AP_THREADS = 128;
 template <int NU>
 __global__ void __launch_bounds__(AP_THREADS) append_kernel(const AppendParams p) {
+  behind_last();
   const Pool& c = p.c;
   const int b = blockIdx.z >> 1, kv = blockIdx.z & 1, h = blockIdx.y;
   const int slot = p.slots[b];
@@ -195,6 +196,7 @@ struct ReadParams {
 constexpr int READ_UNITS = 4;
 template <int HD>
 __global__ void __launch_bounds__(IO_THREADS) read_kernel(const ReadParams p) {
+  behind_last();
   constexpr int PER_ROW = HD / UNIT;
   const Pool& c = p.c;
   const int b = blockIdx.z >> 1, kv = blockIdx.z & 1, h = blockIdx.y;

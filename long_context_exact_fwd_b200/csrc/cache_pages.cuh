@@ -79,6 +79,7 @@ __device__ __forceinline__ int list_pages(const int* refs, int from, int to, boo
 // too few free pages nothing changes.
 __global__ void __launch_bounds__(PLAN_THREADS)
     reserve_plan_kernel(Pool c, const int* slots, const int* n_new, int B, Plan* plan, int* pairs, int* free_list) {
+  behind_last();
   __shared__ int s_slot[MAX_BATCH], s_last[MAX_BATCH], s_first[MAX_BATCH], s_have[MAX_BATCH], warp_sum[33];
   const int b = threadIdx.x;
   const int slot = b < B ? slots[b] : -1;
@@ -154,6 +155,7 @@ __global__ void __launch_bounds__(PLAN_THREADS)
 // call; a destination has to be empty, and the first entry that names it has it.
 __global__ void __launch_bounds__(PLAN_THREADS)
     fork_plan_kernel(Pool c, const int* src, const int* dst, int B, Plan* plan, int* first) {
+  behind_last();
   __shared__ int s_dst[MAX_BATCH], warp_sum[33];
   const int b = threadIdx.x;
   const int s = b < B ? src[b] : -1, d = b < B ? dst[b] : -1;
@@ -184,6 +186,7 @@ __global__ void __launch_bounds__(PLAN_THREADS)
 
 __global__ void __launch_bounds__(COPY_THREADS)
     fork_apply_kernel(Pool c, const int* src, const int* dst, const Plan* plan, const int* first) {
+  behind_last();
   const int rows = plan->rows, items = plan->items;
   for (int i = blockIdx.x * COPY_THREADS + threadIdx.x; i < items; i += gridDim.x * COPY_THREADS) {
     const int r = find_row(first, rows, i);
@@ -200,6 +203,7 @@ __global__ void __launch_bounds__(COPY_THREADS)
 
 // Pages behind the first keep[b] tokens lose one reference (free at 0); len = min(len, keep).
 __global__ void __launch_bounds__(COPY_THREADS) trim_kernel(Pool c, const int* slots, const int* keep, int B) {
+  behind_last();
   const int b = blockIdx.x;
   const int slot = slots[b];
   if (slot == -1) return;
@@ -228,6 +232,7 @@ __global__ void __launch_bounds__(COPY_THREADS) trim_kernel(Pool c, const int* s
 // Live pages at or above n_live (the number of live pages), in order, go to the holes below it.
 __global__ void __launch_bounds__(PLAN_THREADS)
     compact_plan_kernel(Pool c, Plan* plan, int* holes, int* movers, int* moved_to) {
+  behind_last();
   __shared__ int warp_sum[33];
   int live = 0;
   for (int base = threadIdx.x * SWEEP; base < c.pages; base += PLAN_THREADS * SWEEP)
@@ -257,6 +262,7 @@ __global__ void __launch_bounds__(PLAN_THREADS)
 // page table is renumbered by it in the same launch.
 __global__ void __launch_bounds__(COPY_THREADS)
     copy_pages_kernel(Pool c, const Plan* plan, const int* src, const int* dst, int stride, const int* moved_to) {
+  behind_last();
   const int n_pairs = plan->pairs;
   if (moved_to && n_pairs > 0) {
     const long long n = static_cast<long long>(c.slots) * c.max_pages;
