@@ -31,13 +31,13 @@ namespace ra {
 namespace cache {
 
 constexpr int AT_WARPS = 4;
-// Blocks per SM (one joins its warps while the others stream) and stages of a warp's ring, by the
-// registers that NT and the head take.  Measured, heads of 128 (32 contexts up to 16K, NT 1 / 16 contexts,
-// 16 rows, NT 2): 2 blocks of 3 stages 98.9 / 51.7 us, 3 of 2 94.8 / 57.8 (spills).  Heads of 64 take fewer
-// registers, and one block more beats the widest register split (16 contexts up to 64K, NT 1 / 2 / 3):
-// 58.9 / 87.5 / 103.8 us -> 57.6 / 76.5 / 94.9; short contexts (5K) as they were, within 3 %.
-__host__ __device__ constexpr int at_per_sm(int hd, int nt) { return (nt == 1 ? 3 : 2) + (hd == 64 ? 1 : 0); }
-__host__ __device__ constexpr int at_stages(int nt) { return nt == 1 ? 2 : 3; }
+// Blocks per SM (one joins its warps while the others stream), by the registers that NT and the head take;
+// each warp's ring has two stages.  Measured, heads of 128: one context of 512K, 16 rows (NT 2), 2 blocks of 3
+// stages 185 us, 3 of 2 180; 24 rows, 3 stages and 2 234 and 232 us; 32 contexts up to 16K, NT 1, 2 blocks of 3
+// stages 98.9, 3 of 2 94.8.  Heads of 64, 16 contexts up to 64K: NT 1, 3 blocks
+// 58.9 and 4 57.6 us; NT 2, 2 87.5, 3 76.5 and 4 no better; NT 3, 2 103.8 and 3 94.9.
+__host__ __device__ constexpr int at_per_sm(int hd, int nt) { return hd == 64 ? (nt == 1 ? 4 : 3) : (nt == 3 ? 2 : 3); }
+constexpr int AT_STAGES = 2;
 constexpr int AT_THREADS = AT_WARPS * 32;
 constexpr int AT_TILE = 32;          // tokens of a warp's tile
 constexpr int AT_MAX_SMS = 160;      // SMs that the workspace has room for
@@ -69,14 +69,18 @@ struct AttendParams {
 
 template <int HD, int NT>
 struct AttLayout {
-  static constexpr int STAGES = at_stages(NT);
+  static constexpr int STAGES = AT_STAGES;
   static constexpr int KV = AT_TILE * HD;              // bytes of a tile's keys
   static constexpr int STAGE = 2 * KV;
   static constexpr int RING = STAGES * STAGE;          // per warp
   static constexpr int SCALES = AT_WARPS * RING;       // [warp][stage][4] floats
   static constexpr int ML = SCALES + AT_WARPS * STAGES * 16;   // [warp][rows][2] floats, rows <= 32
   static constexpr int NANS = ML + AT_WARPS * 32 * 8;  // [HD] ints
-  static constexpr int PREFIX = NANS + HD * 4;         // [B + 1] ints, then slots, lengths, new tokens [B]
+  // [NT][HD / 16][32] uint2, fragments of the queries: shared by the warps, read again for every tile (in
+  // registers: 16 rows on 512K tokens 197 us, so 185)
+  static constexpr int Q = NANS + HD * 4;
+  static constexpr int QS = Q + NT * (HD / 16) * 256;  // [rows] floats, their scales
+  static constexpr int PREFIX = QS + 8 * NT * 4;         // [B + 1] ints, then slots, lengths, new tokens [B]
   static int bytes(int B) { return PREFIX + (4 * B + 1) * 4; }
 };
 
@@ -159,6 +163,8 @@ __global__ void __launch_bounds__(AT_THREADS, at_per_sm(HD, NT)) attend_kernel(c
   const uint32_t scales_u = smem_u32(scales);
   float* s_ml = reinterpret_cast<float*>(smem + L::ML);
   int* s_nan = reinterpret_cast<int*>(smem + L::NANS);
+  uint2* s_q = reinterpret_cast<uint2*>(smem + L::Q);
+  float* s_qs = reinterpret_cast<float*>(smem + L::QS);
   int* s_prefix = reinterpret_cast<int*>(smem + L::PREFIX);
   int *s_slot = s_prefix + p.B + 1, *s_len = s_slot + p.B, *s_n = s_len + p.B;
   __shared__ int s_warp[AT_WARPS];
@@ -239,22 +245,15 @@ __global__ void __launch_bounds__(AT_THREADS, at_per_sm(HD, NT)) attend_kernel(c
     const int lim_max = rows > 0 ? limit_of(rows - 1) : 0;
     const int* table = c.table + static_cast<long long>(slot) * c.max_pages;
 
-    // ---- queries: column gr of block j is row j * 8 + gr, head columns gc * HD / 4 ..; loaded ahead of the
-    // page numbers, made fragments behind them
-    uint32_t raw[NT][KS * 2];
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      const int r = j * 8 + gr;
+    // ---- queries: warp j < NT has rows j * 8 .., lane (gr, gc) row gr's head columns gc * HD / 4 ..; loaded
+    // ahead of the page numbers, made fragments behind them
+    uint4 raw[KS / 2];
+    if (warp < NT) {
+      const int r = warp * 8 + gr;
       const int tt = (row0 + r) / p.g, hq = h * p.g + (row0 + r) - tt * p.g;
       const uint4* src = reinterpret_cast<const uint4*>(p.q + b * p.qb + hq * p.qh + tt * p.qt + gc * (HD / 4));
 #pragma unroll
-      for (int i = 0; i < KS / 2; ++i) {
-        const uint4 v = r < rows ? src[i] : make_uint4(0, 0, 0, 0);
-        raw[j][4 * i] = v.x;
-        raw[j][4 * i + 1] = v.y;
-        raw[j][4 * i + 2] = v.z;
-        raw[j][4 * i + 3] = v.w;
-      }
+      for (int i = 0; i < KS / 2; ++i) raw[i] = r < rows ? src[i] : make_uint4(0, 0, 0, 0);
     }
 
     // ---- this warp's tiles: t0 + warp, + AT_WARPS, ...; those behind every row's limit are empty
@@ -319,36 +318,39 @@ __global__ void __launch_bounds__(AT_THREADS, at_per_sm(HD, NT)) attend_kernel(c
 #pragma unroll
     for (int i = 0; i < STAGES - 1; ++i) fetch(i);
 
-    uint32_t qf[NT][KS][2];                   // B fragments
-    float row_scale[NT][2];                   // of the accumulator's columns 2 gc, 2 gc + 1
-    int limit[NT][2];
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      const uint32_t (&w)[KS * 2] = raw[j];
+    if (warp < NT) {
       float amax = 0.f;
 #pragma unroll
-      for (int i = 0; i < KS * 2; ++i) {
-        const float lo = fabsf(__uint_as_float(w[i] << 16)), hi = fabsf(__uint_as_float(w[i] & 0xffff0000u));
-        amax = fmaxf(amax, fmaxf(lo <= 3.4028234663852886e38f ? lo : 0.f, hi <= 3.4028234663852886e38f ? hi : 0.f));
-      }
+      for (int i = 0; i < KS / 2; ++i)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const uint32_t w = (&raw[i].x)[x];
+          const float lo = fabsf(__uint_as_float(w << 16)), hi = fabsf(__uint_as_float(w & 0xffff0000u));
+          amax = fmaxf(amax, fmaxf(lo <= 3.4028234663852886e38f ? lo : 0.f, hi <= 3.4028234663852886e38f ? hi : 0.f));
+        }
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
       const int up = amax > 0.f ? min(max(14 - exponent_of(amax), -113), 126) : 0;   // amax -> [2^14, 2^15)
       const float f = two_to(up);
+      auto half2 = [&](uint32_t v) { return pack_half2(__uint_as_float(v << 16) * f, __uint_as_float(v & 0xffff0000u) * f); };
 #pragma unroll
-      for (int s = 0; s < KS; ++s)
+      for (int i = 0; i < KS / 2; ++i) {
+        s_q[(warp * KS + 2 * i) * 32 + lane] = make_uint2(half2(raw[i].x), half2(raw[i].y));
+        s_q[(warp * KS + 2 * i + 1) * 32 + lane] = make_uint2(half2(raw[i].z), half2(raw[i].w));
+      }
+      if (gc == 0) s_qs[warp * 8 + gr] = p.scale_log2 * two_to(-up);
+    }
+    __syncthreads();
+    float row_scale[NT][2];                   // of the accumulator's columns 2 gc, 2 gc + 1
+    int limit[NT][2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint32_t v = w[2 * s + i];
-          qf[j][s][i] = pack_half2(__uint_as_float(v << 16) * f, __uint_as_float(v & 0xffff0000u) * f);
-        }
+    for (int j = 0; j < NT; ++j)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int rr = j * 8 + 2 * gc + e;
-        row_scale[j][e] = p.scale_log2 * two_to(-__shfl_sync(0xffffffffu, up, (2 * gc + e) * 4));
+        row_scale[j][e] = s_qs[rr];
         limit[j][e] = rr < rows ? limit_of(rr) : len;
       }
-    }
 
     float o[KS][NT][4];
     float m_ref[NT][2], l[NT][2];
@@ -374,26 +376,30 @@ __global__ void __launch_bounds__(AT_THREADS, at_per_sm(HD, NT)) attend_kernel(c
       // scores: S^T, rows tokens gr and gr + 8 of each half, columns queries 2 gc, 2 gc + 1
       float s[2][NT][4];
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
+      for (int half = 0; half < 2; ++half)
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
           for (int e = 0; e < 4; ++e) s[half][j][e] = 0.f;
-        uint32_t ka[KS], kb[KS];              // codes of tokens gr, gr + 8: head columns gc * HD / 4 ..
 #pragma unroll
-        for (int w = 0; w < KS / 4; ++w) {
-          const uint4 a = lds128(kst + key_offset<HD>(half * 16 + gr, gc * (KS / 4) + w));
-          const uint4 z = lds128(kst + key_offset<HD>(half * 16 + gr + 8, gc * (KS / 4) + w));
-          ka[4 * w] = a.x; ka[4 * w + 1] = a.y; ka[4 * w + 2] = a.z; ka[4 * w + 3] = a.w;
-          kb[4 * w] = z.x; kb[4 * w + 1] = z.y; kb[4 * w + 2] = z.z; kb[4 * w + 3] = z.w;
-        }
+      for (int w = 0; w < KS / 4; ++w) {      // codes of tokens gr, gr + 8 of both halves: head columns gc * HD / 4 ..
+        uint4 k[4];
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-          const uint32_t a[4] = {codes_to_half2(static_cast<uint16_t>(ka[ks])), codes_to_half2(static_cast<uint16_t>(kb[ks])),
-                                 codes_to_half2(static_cast<uint16_t>(ka[ks] >> 16)),
-                                 codes_to_half2(static_cast<uint16_t>(kb[ks] >> 16))};
+        for (int i = 0; i < 4; ++i) k[i] = lds128(kst + key_offset<HD>(i * 8 + gr, gc * (KS / 4) + w));
 #pragma unroll
-          for (int j = 0; j < NT; ++j) mma_f16(s[half][j], a, qf[j][ks][0], qf[j][ks][1]);
+        for (int x = 0; x < 4; ++x) {
+          uint2 q[NT];
+#pragma unroll
+          for (int j = 0; j < NT; ++j) q[j] = s_q[(j * KS + 4 * w + x) * 32 + lane];
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const uint32_t lo = (&k[2 * half].x)[x], hi = (&k[2 * half + 1].x)[x];
+            const uint32_t a[4] = {codes_to_half2(static_cast<uint16_t>(lo)), codes_to_half2(static_cast<uint16_t>(hi)),
+                                   codes_to_half2(static_cast<uint16_t>(lo >> 16)),
+                                   codes_to_half2(static_cast<uint16_t>(hi >> 16))};
+#pragma unroll
+            for (int j = 0; j < NT; ++j) mma_f16(s[half][j], a, q[j].x, q[j].y);
+          }
         }
       }
 
@@ -465,7 +471,28 @@ __global__ void __launch_bounds__(AT_THREADS, at_per_sm(HD, NT)) attend_kernel(c
       }
 
       // O^T += V^T P^T: thread's tokens 2 gc, 2 gc + 1, 2 gc + 8, 2 gc + 9, head columns gr * HD / 8 ..
-      const bool diagonal = masked && lim_max > lim_min;   // rows of the block see different keys here
+      // A NaN that some rows of the block do not see must not reach them through 0 * NaN: it is taken out of
+      // the tile, where rows see different keys, and put back into the rows that see it at the end.
+      if (masked && lim_max > lim_min) {
+#pragma unroll 1
+        for (int i = lane; i < AT_TILE * (HD / 16); i += 32) {
+          const int t = i / (HD / 16), chunk = i % (HD / 16);
+          uint32_t* at = reinterpret_cast<uint32_t*>(ring_ptr + stage * L::STAGE + L::KV + value_offset<HD>(t, chunk));
+#pragma unroll 1
+          for (int w = 0; w < 4; ++w) {
+            uint32_t x = at[w];
+            if (!has_nan_code(x)) continue;
+#pragma unroll 1
+            for (int y = 0; y < 4; ++y)
+              if (((x >> (8 * y)) & 0x7fu) == 0x7fu) {
+                atomicMin(s_nan + chunk * 16 + 4 * w + y, tok0 + t);
+                x &= ~(0xffu << (8 * y));
+              }
+            at[w] = x;
+          }
+        }
+        __syncwarp();
+      }
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         uint32_t v[4][HD / 32];
@@ -478,20 +505,6 @@ __global__ void __launch_bounds__(AT_THREADS, at_per_sm(HD, NT)) attend_kernel(c
           } else {
             const uint2 a = lds64(vst + value_offset<HD>(t, gr >> 1) + (gr & 1) * 8);
             v[k][0] = a.x; v[k][1] = a.y;
-          }
-          // A NaN that some rows of the block do not see must not reach them through 0 * NaN: it is
-          // taken out here and put back into the rows that see it at the end.
-          if (diagonal) {
-#pragma unroll
-            for (int w = 0; w < HD / 32; ++w)
-              if (has_nan_code(v[k][w])) {
-#pragma unroll
-                for (int y = 0; y < 4; ++y)
-                  if (((v[k][w] >> (8 * y)) & 0x7fu) == 0x7fu) {
-                    atomicMin(s_nan + gr * (HD / 8) + 4 * w + y, tok0 + t);
-                    v[k][w] &= ~(0xffu << (8 * y));
-                  }
-              }
           }
         }
 #pragma unroll
