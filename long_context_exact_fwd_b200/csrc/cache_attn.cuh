@@ -243,6 +243,7 @@ __global__ void __launch_bounds__(AT_THREADS, at_per_sm(HD, NT)) attend_kernel(c
     auto limit_of = [&](int r) { return p.causal ? max(0, min(len, len - n + (row0 + r) / p.g + 1)) : len; };
     const int lim_min = rows > 0 ? limit_of(0) : 0;
     const int lim_max = rows > 0 ? limit_of(rows - 1) : 0;
+    const bool unseen = lim_min < len && t1 * AT_TILE > lim_min;   // tokens here that some row does not see
     const int* table = c.table + static_cast<long long>(slot) * c.max_pages;
 
     // ---- queries: warp j < NT has rows j * 8 .., lane (gr, gc) row gr's head columns gc * HD / 4 ..; loaded
@@ -472,8 +473,8 @@ __global__ void __launch_bounds__(AT_THREADS, at_per_sm(HD, NT)) attend_kernel(c
 
       // O^T += V^T P^T: thread's tokens 2 gc, 2 gc + 1, 2 gc + 8, 2 gc + 9, head columns gr * HD / 8 ..
       // A NaN that some rows of the block do not see must not reach them through 0 * NaN: it is taken out of
-      // the tile, where rows see different keys, and put back into the rows that see it at the end.
-      if (masked && lim_max > lim_min) {
+      // such tiles, and put back into the rows that see it at the end.
+      if (masked && unseen) {
 #pragma unroll 1
         for (int i = lane; i < AT_TILE * (HD / 16); i += 32) {
           const int t = i / (HD / 16), chunk = i % (HD / 16);
@@ -568,7 +569,7 @@ __global__ void __launch_bounds__(AT_THREADS, at_per_sm(HD, NT)) attend_kernel(c
         z += zw * f;
         a = make_float4(fmaf(y.x, f, a.x), fmaf(y.y, f, a.y), fmaf(y.z, f, a.z), fmaf(y.w, f, a.w));
       }
-      if (lim_max > lim_min) {
+      if (unseen) {
         const int lim = limit_of(r);
         const float nan = __uint_as_float(0x7fffffffu);
         if (s_nan[d] < lim) a.x = nan;
@@ -590,7 +591,7 @@ __global__ void __launch_bounds__(AT_THREADS, at_per_sm(HD, NT)) attend_kernel(c
       else if (threadIdx.x == 0) p.split[b * c.heads * p.n_blocks + seg] = joined;
     }
     __syncthreads();                          // rings and s_nan are free again
-    if (lim_max > lim_min) {
+    if (unseen) {
       for (int i = threadIdx.x; i < HD; i += AT_THREADS) s_nan[i] = INT_MAX;
       __syncthreads();
     }

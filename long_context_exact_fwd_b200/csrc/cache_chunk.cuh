@@ -232,9 +232,9 @@ __device__ void ch_convert(const AttendParams& p, ChWalk w, uint8_t* smem, uint3
   uint32_t phase = 0;
   for (bool go = w.next(true); go; go = w.next(false), piece = piece == 2 ? 0 : piece + 1) {
     const int len = w.len(), h = w.h;
-    const int row0 = w.i * CH_ROWS, rows = min(CH_ROWS, w.n() * p.g - row0);
+    const int row0 = w.i * CH_ROWS;
     const int* table = c.table + static_cast<long long>(w.slot()) * c.max_pages;
-    const int lim_min = w.limit(row0), lim_max = w.limit(row0 + rows - 1);
+    const int lim_min = w.limit(row0);
 
     // ---- K and V tiles: HD / 16 lanes a token, 16 codes a lane, AT_ONCE tokens a warp step
     constexpr int LANES = HD / 16, AT_ONCE = 32 / LANES, STEPS = CH_BN / (AT_ONCE * CH_CONV_WARPS);
@@ -247,7 +247,7 @@ __device__ void ch_convert(const AttendParams& p, ChWalk w, uint8_t* smem, uint3
     static_assert(AT_ONCE * CH_CONV_WARPS % 8 == 0, "a lane's tokens share their place in the swizzle");
     for (int tile = w.t0; tile < w.t1; ++tile) {
       const int tok0 = tile * CH_BN;
-      const bool diagonal = lim_max > lim_min && tok0 + CH_BN > lim_min;
+      const bool diagonal = lim_min < len && tok0 + CH_BN > lim_min;   // some row does not see all
       unsigned lots = 0;
 #pragma unroll 1
       for (int kv = 0; kv < 2; ++kv) {

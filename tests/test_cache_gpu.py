@@ -493,3 +493,21 @@ def test_refusals(ra):
     with pytest.raises(ra.RingAttnError):
         ra.cache_attend(c, 0, s, None, _randn((1, 2, 1, 68), 3).cuda()[..., 4:])     # rows off 16 bytes
     assert ra.device_status() == 0
+
+
+@pytest.mark.parametrize("Hq,Dh", [(24, 128), (31, 64), (256, 128), (300, 64)])
+def test_a_value_that_no_row_of_a_block_sees(ra, Hq, Dh):
+    """So many query heads on one key/value head that a block of rows holds one token only: a NaN behind that
+    token, in the same tile, does not reach it."""
+    two = Both(ra, 8, 1, 32, Dh, 1, 4)
+    n = 100
+    assert two.reserve([0], [n])
+    k, v = _randn((1, 1, n, Dh), 1), _randn((1, 1, n, Dh), 2)
+    v[0, 0, n - 1, 7] = float("nan")
+    two.append([0], [n], kv=(k, v))
+    q = _randn((1, Hq, 2, Dh), 3).cuda()
+    o, lse = ra.cache_attend(two.gpu, 0, _i32([0]), None, q)
+    bad = torch.isnan(o[0]).cpu()
+    want = torch.zeros((Hq, 2, Dh), dtype=torch.bool)
+    want[:, 1, 7] = True
+    assert torch.equal(bad, want) and torch.isfinite(lse).all() and ra.device_status() == 0
