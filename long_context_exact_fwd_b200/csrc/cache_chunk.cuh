@@ -17,8 +17,8 @@
 // Work is cut as in attend_kernel: one line of 128-key tiles over all items, equal stretches, parts
 // joined by chunk_join_kernel.
 // Bound: the products, and shared memory, which both operands of S, the tiles of V and the conversion go
-// through (about 320 KB a key tile; a tile takes some 4500 cycles, 2048 of them its products).  Measured on
-// B200, 16 query heads on 4 of 128, 2048 new tokens: at 16K tokens 305 us, 845 TFLOP/s; at 32K 573 us, 929.
+// through (about 320 KB a key tile; a tile takes some 4200 cycles, 2048 of them its products).  Measured on
+// B200, 16 query heads on 4 of 128, 2048 new tokens: at 16K tokens 285 us, 904 TFLOP/s; at 32K 538 us, 990.
 #pragma once
 #include "cache_attn.cuh"
 #include "cache_io.cuh"
@@ -29,7 +29,7 @@ namespace cache {
 constexpr int CH_BM = 128, CH_BN = 128, CH_ROWS = 256, CH_STAGES = 4;
 constexpr int CH_THREADS = 384;
 constexpr int CH_WARP_MMA = 8, CH_WARP_FETCH = 9, CH_WARP_CONV = 10, CH_CONV_WARPS = 2;
-constexpr uint32_t CH_REGS_LAUNCH = 168, CH_REGS_SOFTMAX = 200, CH_REGS_OTHER = 104;
+constexpr uint32_t CH_REGS_LAUNCH = 168, CH_REGS_SOFTMAX = 208, CH_REGS_OTHER = 88;
 static_assert(2 * (CH_REGS_SOFTMAX - CH_REGS_LAUNCH) <= CH_REGS_LAUNCH - CH_REGS_OTHER, "register split exceeds the pool");
 constexpr int CH_MAX_CTAS = 160;      // blocks that the workspace has room for (one per SM)
 constexpr int CH_START = 3;          // what starting and ending an item costs, in tiles
@@ -257,25 +257,18 @@ __device__ void ch_convert(const AttendParams& p, ChWalk w, uint8_t* smem, uint3
         const uint8_t* raw = smem + L::raw(stage) + tok * HD + col * 16;
         uint8_t* dst = smem + L::KV_OFF + stage * L::TILE_BYTES + sub * L::SUB_BYTES + tok * 128;
         bool odd = false;
-        uint4 next[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) next[k] = *reinterpret_cast<const uint4*>(raw + k * (AT_ONCE * CH_CONV_WARPS) * HD);
-        // Rolled up: unrolled over the tile, this loop and the softmax's did not fit the instruction
-        // cache together, and every role ran at less than half its speed.
+        // Short: this loop and the softmax's share the instruction cache.  Unrolled over the tile, every role
+        // ran at less than half its speed; 2048 queries on 16K tokens, 1, 2, 4 and 8 loads together: 332, 285,
+        // 293 and 309 us.
 #pragma unroll 1
-        for (int k0 = 0; k0 < STEPS; k0 += 4) {
-          uint4 x[4];
+        for (int k0 = 0; k0 < STEPS; k0 += 2) {
+          uint4 x[2];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) x[k] = next[k];
-          if (k0 + 4 < STEPS) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              next[k] = *reinterpret_cast<const uint4*>(raw + (k0 + 4 + k) * (AT_ONCE * CH_CONV_WARPS) * HD);
-          }
+          for (int k = 0; k < 2; ++k) x[k] = *reinterpret_cast<const uint4*>(raw + (k0 + k) * (AT_ONCE * CH_CONV_WARPS) * HD);
           __syncwarp();   // HD 128: a token's second block is written where its codes were
           if (!plain) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
+            for (int k = 0; k < 2; ++k) {
               const int t = tok + (k0 + k) * (AT_ONCE * CH_CONV_WARPS);
               // what lies behind the end, or was not fetched, is 0
               if (!(lots >> (t >> 4) & 1u) || tok0 + t >= len) x[k] = make_uint4(0, 0, 0, 0);
@@ -284,7 +277,7 @@ __device__ void ch_convert(const AttendParams& p, ChWalk w, uint8_t* smem, uint3
             }
           }
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
+          for (int k = 0; k < 2; ++k) {
             const uint4 lo = make_uint4(
                 codes_to_half2(static_cast<uint16_t>(x[k].x)), codes_to_half2(static_cast<uint16_t>(x[k].x >> 16)),
                 codes_to_half2(static_cast<uint16_t>(x[k].y)), codes_to_half2(static_cast<uint16_t>(x[k].y >> 16)));
