@@ -49,6 +49,7 @@ constexpr int AT_START = 16;
 constexpr int AT_LEAST = 4;
 constexpr float AT_RAISE = 8.f;      // log2: P <= 2^8, times 2^7 still an fp16 number
 constexpr float AT_P_UNIT = 128.f;
+constexpr float NOTHING = 3.4028234663852886e38f;   // minus the reference of a row that has seen nothing: any score raises it
 
 struct AttendParams {
   Pool c;                      // one layer
@@ -100,10 +101,11 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
 __device__ __forceinline__ uint2 lds64(uint32_t a) {
   return *reinterpret_cast<const uint2*>(__cvta_shared_to_generic(a));
 }
-__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma_f16(float& c0, float& c1, float& c2, float& c3, const uint32_t (&a)[4], uint32_t b0,
+                                        uint32_t b1) {
   asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "+f"(c0), "+f"(c1), "+f"(c2), "+f"(c3)
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
@@ -342,28 +344,29 @@ __global__ void __launch_bounds__(AT_THREADS, at_per_sm(HD, NT)) attend_kernel(c
       if (gc == 0) s_qs[warp * 8 + gr] = p.scale_log2 * two_to(-up);
     }
     __syncthreads();
-    float row_scale[NT][2];                   // of the accumulator's columns 2 gc, 2 gc + 1
+    float2 row_scale[NT];                     // of the accumulator's columns 2 gc, 2 gc + 1
     int limit[NT][2];
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int rr = j * 8 + 2 * gc + e;
-        row_scale[j][e] = s_qs[rr];
+        (e ? row_scale[j].y : row_scale[j].x) = s_qs[rr];
         limit[j][e] = rr < rows ? limit_of(rr) : len;
       }
 
     float o[KS][NT][4];
-    float m_ref[NT][2], l[NT][2];
+    float2 neg_ref[NT], l[NT];                // minus the reference, and the sum, of columns 2 gc, 2 gc + 1
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-      m_ref[j][0] = m_ref[j][1] = -INFINITY;
-      l[j][0] = l[j][1] = 0.f;
+      neg_ref[j] = make_float2(NOTHING, NOTHING);
+      l[j] = make_float2(0.f, 0.f);
 #pragma unroll
       for (int m = 0; m < KS; ++m)
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[m][j][i] = 0.f;
     }
+    float p_unit = 0.f;                       // AT_P_UNIT / v_ref
     float v_ref = 0.f;                        // largest value scale so far; O is in units of it
 
     for (int i = 0; i < count; ++i) {
@@ -375,13 +378,11 @@ __global__ void __launch_bounds__(AT_THREADS, at_per_sm(HD, NT)) attend_kernel(c
       const float4 sc = *reinterpret_cast<const float4*>(scales + stage * 4);
 
       // scores: S^T, rows tokens gr and gr + 8 of each half, columns queries 2 gc, 2 gc + 1
-      float s[2][NT][4];
+      float2 s[2][NT][2];                     // [half][..][token gr or gr + 8]
 #pragma unroll
       for (int half = 0; half < 2; ++half)
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) s[half][j][e] = 0.f;
+        for (int j = 0; j < NT; ++j) s[half][j][0] = s[half][j][1] = make_float2(0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < KS / 4; ++w) {      // codes of tokens gr, gr + 8 of both halves: head columns gc * HD / 4 ..
         uint4 k[4];
@@ -399,75 +400,85 @@ __global__ void __launch_bounds__(AT_THREADS, at_per_sm(HD, NT)) attend_kernel(c
                                    codes_to_half2(static_cast<uint16_t>(lo >> 16)),
                                    codes_to_half2(static_cast<uint16_t>(hi >> 16))};
 #pragma unroll
-            for (int j = 0; j < NT; ++j) mma_f16(s[half][j], a, q[j].x, q[j].y);
+            for (int j = 0; j < NT; ++j)
+              mma_f16(s[half][j][0].x, s[half][j][0].y, s[half][j][1].x, s[half][j][1].y, a, q[j].x, q[j].y);
           }
         }
       }
 
       // log2 units, mask, and the largest of each column
       const bool masked = tok0 + AT_TILE > lim_min;
-      bool raise = false;
-      float mx[NT][2];
+      float top = -INFINITY;                  // over the reference
+      float2 mx[NT];
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float f0 = row_scale[j][e] * sc.x, f1 = row_scale[j][e] * sc.y;
-          s[0][j][e] *= f0;
-          s[0][j][e + 2] *= f0;
-          s[1][j][e] *= f1;
-          s[1][j][e + 2] *= f1;
-          if (masked) {
-            const int left = limit[j][e] - tok0 - gr;   // tokens of the tile, from this thread's first, that are seen
-            if (left <= 0) s[0][j][e] = -INFINITY;
-            if (left <= 8) s[0][j][e + 2] = -INFINITY;
-            if (left <= 16) s[1][j][e] = -INFINITY;
-            if (left <= 24) s[1][j][e + 2] = -INFINITY;
-          }
-          mx[j][e] = fmaxf(fmaxf(s[0][j][e], s[0][j][e + 2]), fmaxf(s[1][j][e], s[1][j][e + 2]));
-          raise |= mx[j][e] > m_ref[j][e] + AT_RAISE;
+        for (int half = 0; half < 2; ++half) {
+          const float k = half ? sc.y : sc.x;
+          const float2 f = __fmul2_rn(row_scale[j], make_float2(k, k));
+#pragma unroll
+          for (int y = 0; y < 2; ++y) s[half][j][y] = __fmul2_rn(s[half][j][y], f);
         }
+        if (masked) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {       // tokens of the tile, from this thread's first, that are seen
+            if (limit[j][0] - tok0 - gr <= 8 * i) s[i >> 1][j][i & 1].x = -INFINITY;
+            if (limit[j][1] - tok0 - gr <= 8 * i) s[i >> 1][j][i & 1].y = -INFINITY;
+          }
+        }
+        mx[j] = make_float2(fmaxf(fmaxf(s[0][j][0].x, s[0][j][1].x), fmaxf(s[1][j][0].x, s[1][j][1].x)),
+                            fmaxf(fmaxf(s[0][j][0].y, s[0][j][1].y), fmaxf(s[1][j][0].y, s[1][j][1].y)));
+        const float2 over = __fadd2_rn(mx[j], neg_ref[j]);
+        top = fmaxf(top, fmaxf(over.x, over.y));
       }
       const float v_max = fmaxf(sc.z, sc.w);
       const bool raise_v = v_max > v_ref;               // the same in the whole warp
-      if (__any_sync(0xffffffffu, raise) || raise_v) {
-        const float fv = raise_v ? v_ref / v_max : 1.f; // powers of two: exact
-        if (raise_v) v_ref = v_max;
+      if (__any_sync(0xffffffffu, top > AT_RAISE) || raise_v) {
+        float fv = 1.f;                                 // powers of two: exact
+        if (raise_v) {
+          fv = v_ref / v_max;
+          v_ref = v_max;
+          p_unit = AT_P_UNIT / v_max;
+        }
+        auto raised = [&](float& ref, float& sum, float m) {   // returns what O has to be multiplied by
+          m = fmaxf(-ref, m);
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+          const float a = -ref == m ? 1.f : ex2_approx(-ref - m);
+          ref = -m;
+          sum *= a;
+          return a * fv;
+        };
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
+        for (int j = 0; j < NT; ++j) {
+          const float f0 = raised(neg_ref[j].x, l[j].x, mx[j].x), f1 = raised(neg_ref[j].y, l[j].y, mx[j].y);
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float m = fmaxf(m_ref[j][e], mx[j][e]);
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-            const float a = m_ref[j][e] == m ? 1.f : ex2_approx(m_ref[j][e] - m);   // from -inf: 0
-            m_ref[j][e] = m;
-            l[j][e] *= a;
-#pragma unroll
-            for (int k = 0; k < KS; ++k) {
-              o[k][j][e] *= a * fv;
-              o[k][j][e + 2] *= a * fv;
-            }
+          for (int k = 0; k < KS; ++k) {
+            o[k][j][0] *= f0;
+            o[k][j][1] *= f1;
+            o[k][j][2] *= f0;
+            o[k][j][3] *= f1;
           }
+        }
       }
-      const float inv_v = v_ref > 0.f ? 1.f / v_ref : 0.f;
-      const float w0 = sc.z * inv_v * AT_P_UNIT, w1 = sc.w * inv_v * AT_P_UNIT;
 
       // P^T as B fragments
       uint32_t pf[2][NT][2];
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        const float r0 = m_ref[j][0] == -INFINITY ? 0.f : m_ref[j][0], r1 = m_ref[j][1] == -INFINITY ? 0.f : m_ref[j][1];
+      for (int half = 0; half < 2; ++half) {
+        const float w = (half ? sc.w : sc.z) * p_unit;
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const float w = half ? w1 : w0;
-          const float a0 = ex2_approx(s[half][j][0] - r0), a1 = ex2_approx(s[half][j][1] - r1);
-          const float b0 = ex2_approx(s[half][j][2] - r0), b1 = ex2_approx(s[half][j][3] - r1);
-          l[j][0] += a0 + b0;
-          l[j][1] += a1 + b1;
-          pf[half][j][0] = transpose8(pack_half2(a0 * w, a1 * w));
-          pf[half][j][1] = transpose8(pack_half2(b0 * w, b1 * w));
+        for (int j = 0; j < NT; ++j) {
+          float2 e[2];
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const float2 x = __fadd2_rn(s[half][j][y], neg_ref[j]);
+            e[y] = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+            const float2 wide = __fmul2_rn(e[y], make_float2(w, w));
+            pf[half][j][y] = transpose8(pack_half2(wide.x, wide.y));
+          }
+          l[j] = __fadd2_rn(l[j], __fadd2_rn(e[0], e[1]));
         }
       }
 
@@ -517,7 +528,10 @@ __global__ void __launch_bounds__(AT_THREADS, at_per_sm(HD, NT)) attend_kernel(c
             const uint32_t a[4] = {codes_to_half2(static_cast<uint16_t>(lo)), codes_to_half2(static_cast<uint16_t>(lo >> 16)),
                                    codes_to_half2(static_cast<uint16_t>(hi)), codes_to_half2(static_cast<uint16_t>(hi >> 16))};
 #pragma unroll
-            for (int j = 0; j < NT; ++j) mma_f16(o[2 * w + y][j], a, pf[half][j][0], pf[half][j][1]);
+            for (int j = 0; j < NT; ++j) {
+              float (&c)[4] = o[2 * w + y][j];
+              mma_f16(c[0], c[1], c[2], c[3], a, pf[half][j][0], pf[half][j][1]);
+            }
           }
         }
       }
@@ -532,13 +546,13 @@ __global__ void __launch_bounds__(AT_THREADS, at_per_sm(HD, NT)) attend_kernel(c
     for (int j = 0; j < NT; ++j)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        float z = l[j][e];
+        float z = e ? l[j].y : l[j].x;
         z += __shfl_xor_sync(0xffffffffu, z, 4);
         z += __shfl_xor_sync(0xffffffffu, z, 8);
         z += __shfl_xor_sync(0xffffffffu, z, 16);
         const int r = j * 8 + 2 * gc + e;
         if (gr == 0) {
-          s_ml[(warp * 32 + r) * 2] = m_ref[j][e];
+          s_ml[(warp * 32 + r) * 2] = z == 0.f ? -INFINITY : -(e ? neg_ref[j].y : neg_ref[j].x);
           s_ml[(warp * 32 + r) * 2 + 1] = z;
         }
 #pragma unroll
