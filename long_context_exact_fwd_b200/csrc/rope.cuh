@@ -16,6 +16,7 @@
 // 8198 tokens, 8 + 2 heads, 96 of 128 columns, float32: 15.0 us.
 #pragma once
 #include <cstdint>
+#include <type_traits>
 #include <cuda_bf16.h>
 
 namespace ra {
@@ -37,6 +38,7 @@ struct Params {
   const long long* pos;       // or null: position = offset + s
   long long pos_b, pos_s, offset;
   long long tokens;           // B * S
+  int wide_ids;               // tokens * units passes 32 bits
   int S, Dh, rot;
   int units;                  // groups of columns per token
   int rot_units;              // of them, groups that are rotated
@@ -197,6 +199,145 @@ __global__ void __launch_bounds__(THREADS) rope_kernel(const Params p) {
     narrow<N>(f, a);
     store<T, N, VECTOR>(y + col, a);
   }
+}
+
+// N elements from element `at` of a warp's rows in shared memory.
+template <int N>
+__device__ __forceinline__ void window(const Pack<float, N>* rows, int at, float (&f)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) f[i] = reinterpret_cast<const float*>(rows)[at + i];
+}
+template <int N>   // one that starts in the middle of a word is shifted
+__device__ __forceinline__ void window(const Pack<__nv_bfloat16, N>* rows, int at, float (&f)[N]) {
+  const uint32_t* words = reinterpret_cast<const uint32_t*>(rows) + (at >> 1);
+  const int shift = (at & 1) * 16;
+  uint32_t w[N / 2 + 1];
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) w[i] = words[i];
+  w[N / 2] = shift ? words[N / 2] : 0;
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) {
+    const uint32_t v = __funnelshift_r(w[i], w[i + 1], shift);
+    f[2 * i] = __uint_as_float(v << 16);
+    f[2 * i + 1] = __uint_as_float(v & 0xffff0000u);
+  }
+}
+
+// A thread's place: its token, and its unit of the row.
+struct Place {
+  long long token, b, s;
+  int unit;
+};
+__device__ __forceinline__ Place place(const Params& p) {
+  Place r;
+  const long long id = static_cast<long long>(blockIdx.x) * THREADS + threadIdx.x;
+  if (p.wide_ids) {
+    r.token = id / p.units;
+    r.b = r.token / p.S;
+  } else {
+    r.token = static_cast<unsigned>(id) / static_cast<unsigned>(p.units);
+    r.b = static_cast<unsigned>(r.token) / static_cast<unsigned>(p.S);
+  }
+  r.unit = static_cast<int>(id - r.token * p.units);
+  r.s = r.token - r.b * p.S;
+  return r;
+}
+// Calls body(x, y, x's and y's distance from head to head, heads) for the block's heads of Q, then of K; x, y at
+// column `col` of the first.
+template <typename T, typename F>
+__device__ __forceinline__ void each_tensor(const Params& p, const Place& at, int col, F body) {
+  const int h0 = blockIdx.y * p.heads_per_thread, h1 = h0 + p.heads_per_thread;
+#pragma unroll 1
+  for (int i = 0; i < 2; ++i) {
+    const Tensor& t = p.t[i];
+    const int before = i ? p.t[0].heads : 0;
+    const int a = max(h0 - before, 0), n = min(h1 - before, t.heads) - a;
+    if (n > 0)
+      body(static_cast<const T*>(t.x) + at.b * t.xb + at.s * t.xs + a * t.xh + col,
+           static_cast<T*>(t.y) + at.b * t.yb + at.s * t.ys + a * t.yh + col, t.xh, t.yh, n);
+  }
+}
+
+// The same for pairs that do not lie at a vector's distance, in rows that do start at vectors: a thread has one
+// vector of a row, and a half layout's partners, at any offset, come from the row's other threads through
+// shared memory (a row's threads are in one warp; outputs may be the inputs, so a row is read before it is
+// written).  Measured, float32 columns of a projection: half, 38 of 128, 19516 tokens, 16 + 8 heads: 79 us, 93 % of a
+// copy (rope_kernel, element by element, 164); bf16 is bound by its instructions: 30 of 64, 64 + 16 heads 51 %.
+template <typename T, int N, bool INTERLEAVED>
+__global__ void __launch_bounds__(THREADS) rope_rows_kernel(const Params p) {
+  // a warp's rows, with room for a window that begins before the first or ends behind the last
+  __shared__ Pack<T, N> rows[INTERLEAVED ? 1 : THREADS / 32][INTERLEAVED ? 1 : HEADS_AT_ONCE][34];
+  const Place at = place(p);
+  if (at.token >= p.tokens) return;
+  const int col = at.unit * N, half = p.rot / 2, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const bool rotated = col < p.rot;
+  float c[N], sn[N];                         // y = x c + partner sn
+  if (rotated) {
+    const long long pos = p.pos ? p.pos[at.b * p.pos_b + at.s * p.pos_s] : p.offset + at.s;
+    const float amplitude = p.inverse ? -p.amplitude : p.amplitude;
+#pragma unroll
+    for (int i = 0; i < N; i += INTERLEAVED ? 2 : 1) {
+      const int j = min(col + i, p.rot - 1);
+      const bool first = INTERLEAVED || j < half;
+      turn(static_cast<unsigned long long>(pos) * p.steps[INTERLEAVED ? j / 2 : first ? j : j - half], c[i], sn[i]);
+      c[i] *= p.amplitude;
+      sn[i] *= first ? -amplitude : amplitude;
+      if (INTERLEAVED) {
+        c[i + 1] = c[i];
+        sn[i + 1] = -sn[i];
+      }
+    }
+  }
+  each_tensor<T>(p, at, col, [&](const T* x, T* y, long long xh, long long yh, int n) {
+    for (int h = 0; h < n; h += HEADS_AT_ONCE, x += HEADS_AT_ONCE * xh, y += HEADS_AT_ONCE * yh) {
+      Pack<T, N> a[HEADS_AT_ONCE];
+#pragma unroll
+      for (int k = 0; k < HEADS_AT_ONCE; ++k)
+        if (h + k < n) a[k] = *reinterpret_cast<const Pack<T, N>*>(x + k * xh);
+      if constexpr (!INTERLEAVED) {
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < HEADS_AT_ONCE; ++k)
+          if (h + k < n) rows[warp][k][1 + lane] = a[k];
+        __syncwarp();
+      }
+#pragma unroll
+      for (int k = 0; k < HEADS_AT_ONCE; ++k) {
+        if (h + k >= n) break;
+        if (rotated) {
+          float f[N], z[N];
+          widen<N>(a[k].v, f);
+          if constexpr (INTERLEAVED) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) z[i] = f[i ^ 1];
+          } else {
+            const int own = (1 + lane) * N;    // this thread's first element
+            if (col + N <= half) {
+              window<N>(rows[warp][k], own + half, z);
+            } else if (col >= half) {
+              window<N>(rows[warp][k], own - half, z);
+            } else {                           // the halves meet in this vector
+              float low[N];
+              window<N>(rows[warp][k], own + half, z);
+              window<N>(rows[warp][k], own - half, low);
+#pragma unroll
+              for (int i = 0; i < N; ++i) z[i] = col + i < half ? z[i] : low[i];
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < N; ++i) f[i] = fmaf(f[i], c[i], z[i] * sn[i]);
+          Pack<T, N> r;
+          narrow<N>(f, r.v);
+          // rot is even, and so is col: pairs of columns are rotated together
+          using Two = std::conditional_t<sizeof(T) == 2, uint32_t, uint2>;
+#pragma unroll
+          for (int i = 0; i < N; i += 2)
+            if (col + i < p.rot) reinterpret_cast<Two*>(a[k].v)[i / 2] = reinterpret_cast<const Two*>(r.v)[i / 2];
+        }
+        if (rotated || x != y) *reinterpret_cast<Pack<T, N>*>(y + k * yh) = a[k];
+      }
+    }
+  });
 }
 
 }  // namespace rope

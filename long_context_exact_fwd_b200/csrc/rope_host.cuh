@@ -42,37 +42,46 @@ int rope_tensor(ra::rope::Tensor* t, const void* x, void* y, int H, const long l
   return RA_OK;
 }
 
+// As many heads per thread (one sine and cosine for all of them) as leave 8 blocks per SM.  Measured
+// (16K prompt / float32 gradient): 4 blocks 53.6 / 15.2 us, 8 49.5 / 15.0, 16 50.9 / 16.3, 32 58.9 / 19.2.
+int rope_heads(const ra::rope::Params& p, int units, int sm_count) {
+  const long long blocks = (p.tokens * units + ra::rope::THREADS - 1) / ra::rope::THREADS;
+  const int heads = p.t[0].heads + p.t[1].heads;
+  int hpt = 1;
+  while (hpt < heads && hpt < 16 && blocks * ((heads + 2 * hpt - 1) / (2 * hpt)) >= 8ll * sm_count) hpt *= 2;
+  return hpt;
+}
+
+// One thread a unit of a token, p.units of them a row.
+int rope_launch(void (*kernel)(ra::rope::Params), ra::rope::Params& p, int sm_count, cudaStream_t stream) {
+  using namespace ra::rope;
+  const long long threads = p.tokens * p.units;
+  p.wide_ids = threads > UINT_MAX - THREADS;
+  const long long blocks = (threads + THREADS - 1) / THREADS;
+  p.heads_per_thread = rope_heads(p, p.units, sm_count);
+  const int gy = (p.t[0].heads + p.t[1].heads + p.heads_per_thread - 1) / p.heads_per_thread;
+  if (blocks > INT_MAX || gy > 65535) return RA_ERR_SHAPE;
+  kernel<<<dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(gy)), THREADS, 0, stream>>>(p);
+  return launch_status();
+}
+
 template <typename T, int N, bool VECTOR>
-int rope_launch(ra::rope::Params& p, int sm_count, bool interleaved, cudaStream_t stream) {
+int rope_units(ra::rope::Params& p, int sm_count, bool interleaved, cudaStream_t stream) {
   using namespace ra::rope;
   p.rot_units = interleaved ? p.rot / N : p.rot / 2 / N;
   p.units = p.rot_units + (p.Dh - p.rot) / N;
-  const long long threads = p.tokens * p.units;
-  const long long blocks = (threads + THREADS - 1) / THREADS;
-  const int heads = p.t[0].heads + p.t[1].heads;
-  // As many heads per thread (one sine and cosine for all of them) as leave 8 blocks per SM.  Measured
-  // (16K prompt / float32 gradient): 4 blocks 53.6 / 15.2 us, 8 49.5 / 15.0, 16 50.9 / 16.3, 32 58.9 / 19.2.
-  int hpt = 1;
-  while (hpt < heads && hpt < 16 && blocks * ((heads + 2 * hpt - 1) / (2 * hpt)) >= 8ll * sm_count) hpt *= 2;
-  p.heads_per_thread = hpt;
-  const int gy = (heads + hpt - 1) / hpt;
-  if (blocks > INT_MAX || gy > 65535) return RA_ERR_SHAPE;
-  const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(gy));
-  if (interleaved) {
-    if constexpr (N >= 2) rope_kernel<T, N, true, VECTOR><<<grid, THREADS, 0, stream>>>(p);
-  } else {
-    rope_kernel<T, N, false, VECTOR><<<grid, THREADS, 0, stream>>>(p);
+  if constexpr (N >= 2) {
+    if (interleaved) return rope_launch(rope_kernel<T, N, true, VECTOR>, p, sm_count, stream);
   }
-  return launch_status();
+  return rope_launch(rope_kernel<T, N, false, VECTOR>, p, sm_count, stream);
 }
 
 template <typename T>
 int rope_dispatch(ra::rope::Params& p, int sm_count, bool interleaved, cudaStream_t stream) {
   constexpr int WIDE = 16 / static_cast<int>(sizeof(T));
-  // The widest access that every row start, the pairs' distance and the untouched rest allow.
-  int n = WIDE;
-  auto fits = [&](int m) {
-    if ((interleaved ? p.rot : p.rot / 2) % m || (p.Dh - p.rot) % m) return false;
+  // The widest access that every row start allows,
+  auto rows_fit = [&](int m) {
+    if (p.Dh % m) return false;
     for (const ra::rope::Tensor& t : p.t) {
       if (!t.heads) continue;
       if (reinterpret_cast<uintptr_t>(t.x) % (m * sizeof(T)) || reinterpret_cast<uintptr_t>(t.y) % (m * sizeof(T)))
@@ -82,15 +91,33 @@ int rope_dispatch(ra::rope::Params& p, int sm_count, bool interleaved, cudaStrea
     }
     return true;
   };
-  while (n > 1 && !fits(n)) n /= 2;
+  // and the pairs' distance and the untouched rest.
+  auto fits = [&](int m) { return (interleaved ? p.rot : p.rot / 2) % m == 0 && (p.Dh - p.rot) % m == 0 && rows_fit(m); };
   if constexpr (WIDE == 8) {
-    if (n == 8) return rope_launch<T, 8, true>(p, sm_count, interleaved, stream);
+    if (fits(8)) return rope_units<T, 8, true>(p, sm_count, interleaved, stream);
+  } else {
+    if (fits(4)) return rope_units<T, 4, true>(p, sm_count, interleaved, stream);
   }
-  if (n == 4) return rope_launch<T, 4, true>(p, sm_count, interleaved, stream);
-  if (n == 2) return rope_launch<T, 2, true>(p, sm_count, interleaved, stream);
+  if constexpr (WIDE == 8) {
+    if (fits(4)) return rope_units<T, 4, true>(p, sm_count, interleaved, stream);
+  }
+  // Rows of vectors with pairs at an odd distance: rope_rows_kernel, which takes every angle twice in the half
+  // layout and so needs heads to share it among where pairs of elements would fit.  Measured, that and
+  // rope_kernel: half, bf16, rot 30 of 64, 64 + 16 heads 72 and 147 us; 102 of 128, 2 + 2 heads 72 and 94; two
+  // elements fit, 76 of 128, 64 + 16 heads 68 and 92, 60 of 64, 2 + 2 heads 40 and 30; interleaved, float32, 106 of
+  // 128, 8 + 4 heads 34 and 47.  Vectors of 4 bf16 (8: 90 us in the first).
+  constexpr int ROWS_N = 4;
+  const int units = p.Dh / ROWS_N;
+  if (rows_fit(ROWS_N)) {
+    p.units = units;
+    if (interleaved) return rope_launch(ra::rope::rope_rows_kernel<T, ROWS_N, true>, p, sm_count, stream);
+    if (units <= 32 && 32 % units == 0 && (!fits(2) || rope_heads(p, units, sm_count) >= 8))
+      return rope_launch(ra::rope::rope_rows_kernel<T, ROWS_N, false>, p, sm_count, stream);
+  }
+  if (fits(2)) return rope_units<T, 2, true>(p, sm_count, interleaved, stream);
   // Nothing lines up: element by element (an interleaved pair is still one thread's; rot and Dh are even).
-  if (interleaved) return rope_launch<T, 2, false>(p, sm_count, true, stream);
-  return rope_launch<T, 1, false>(p, sm_count, false, stream);
+  if (interleaved) return rope_units<T, 2, false>(p, sm_count, true, stream);
+  return rope_units<T, 1, false>(p, sm_count, false, stream);
 }
 
 }  // namespace

@@ -191,3 +191,34 @@ def test_refusals(ra):
     with pytest.raises(ra.RingAttnError):
         ra.rope(big[:q.numel()].view(q.shape), plan, out=big[64:64 + q.numel()].view(q.shape))
     assert ra.device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("Dh,rot", [(64, 2), (64, 10), (64, 30), (64, 60), (128, 26), (128, 102), (128, 126), (256, 58), (32, 14),
+                                    (8, 6), (1024, 778)])
+def test_rotated_widths_that_no_vector_divides(ra, Dh, rot, inter, dtype):
+    """Rows start at vectors, the pairs' distance does not: apart and in place, rows of several tokens in one
+    warp, more heads than a thread has at once, what a row's neighbours hold not finite."""
+    B, S, H, Hk = 2, 5, 5, 2
+    w, amp = ra.rope_inv_freq(rot, scaling="ramp", factor=2.0, original_length=50)
+    plan = ra.rope_plan(w, "interleaved" if inter else "half", amp)
+    rows = _x((B, S, H + 2 * Hk, Dh), dtype, 21)
+    rows[:, :, H + Hk:] = float("nan")
+    rows[:, 3, 2] = float("inf")
+    q, k = (rows[:, :, :H].permute(0, 2, 1, 3), rows[:, :, H:H + Hk].permute(0, 2, 1, 3))
+    pos = torch.arange(7, 7 + S).cuda()
+    p2 = np.broadcast_to(pos.cpu().numpy(), (B, S))
+    for inverse in (False, True):
+        a, b = ra.rope(q, plan, k=k, pos=pos, inverse=inverse)
+        for got, x in ((a, q), (b, k)):
+            ok = [s for s in range(S) if s != 3]
+            _check(got[:, :, ok], x[:, :, ok], p2[:, ok], w.numpy(), inter, amp, inverse)
+        assert torch.isfinite(a[:, [h for h in range(H) if h != 2], 3]).all()
+        assert torch.equal(a[:, 2, 3, rot:], q[:, 2, 3, rot:])
+        keep = rows.clone()
+        ra.rope(q, plan, k=k, pos=pos, inverse=inverse, out=q, k_out=k)
+        for x, want in ((q, a), (k, b)):
+            assert torch.equal(x.nan_to_num(nan=5.0), want.nan_to_num(nan=5.0))
+        assert torch.equal(rows[:, :, H + Hk:].isnan(), keep[:, :, H + Hk:].isnan())
+        rows.copy_(keep)
