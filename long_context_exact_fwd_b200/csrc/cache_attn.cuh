@@ -22,8 +22,8 @@
 // known on the device), so stretches end inside sequences: such parts go to the workspace and a
 // second, small launch joins them.  Each warp streams its own tiles with cp.async through a private
 // ring in shared memory, no block barrier inside a stretch (TMA boxes in its place: 7 % slower).
-// Measured on B200, 8 heads of 128, 4 query heads each: one context of 512K tokens 167 us, 98 % of a copy's
-// rate; 128K 50 us (82 %, some 9 us are start, join and launches); 32 of 16 to 16384 tokens 92 us (90 %).
+// Measured on B200, 8 heads of 128, 4 query heads each: one context of 512K tokens 168 us, 98 % of a copy's
+// rate; 128K 50 us (83 %, some 9 us are start, join and launches); 32 of 16 to 16384 tokens 91 us (91 %).
 #pragma once
 #include "cache.cuh"
 
@@ -33,9 +33,9 @@ namespace cache {
 constexpr int AT_WARPS = 4;
 // Blocks per SM (one joins its warps while the others stream), by the registers that NT and the head take;
 // each warp's ring has two stages.  Measured, heads of 128: one context of 512K, 16 rows (NT 2), 2 blocks of 3
-// stages 185 us, 3 of 2 180; 24 rows, 3 stages and 2 234 and 232 us; 32 contexts up to 16K, NT 1, 2 blocks of 3
-// stages 98.9, 3 of 2 94.8.  Heads of 64, 16 contexts up to 64K: NT 1, 3 blocks
-// 58.9 and 4 57.6 us; NT 2, 2 87.5, 3 76.5 and 4 no better; NT 3, 2 103.8 and 3 94.9.
+// stages 185 us, 3 of 2 180; 24 rows, 3 stages and 2 234 and 232; 32 contexts up to 16K, NT 1, 2 blocks of 3
+// stages 98.9, 3 of 2 94.8.  Heads of 64, 16 contexts up to 64K: NT 1, 3 blocks 58.9 and 4 57.6 us; NT 2, 2 87.5,
+// 3 76.5 and 4 no better; NT 3, 2 103.8 and 3 94.9.
 __host__ __device__ constexpr int at_per_sm(int hd, int nt) { return hd == 64 ? (nt == 1 ? 4 : 3) : (nt == 3 ? 2 : 3); }
 constexpr int AT_STAGES = 2;
 constexpr int AT_THREADS = AT_WARPS * 32;
