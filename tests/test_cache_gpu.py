@@ -511,3 +511,86 @@ def test_a_value_that_no_row_of_a_block_sees(ra, Hq, Dh):
     want = torch.zeros((Hq, 2, Dh), dtype=torch.bool)
     want[:, 1, 7] = True
     assert torch.equal(bad, want) and torch.isfinite(lse).all() and ra.device_status() == 0
+
+
+@pytest.mark.parametrize("T,captured", [(1, False), (1, True), (40, False), (40, True)])
+def test_launches_set_up_early_wait_for_both_streams(ra, T, captured):
+    """Inputs that another stream writes late, behind an event, between calls whose launches are set up behind
+    one another."""
+    H, Dh, n = 2, 128, 300
+    k, v, q = _randn((1, H, n, Dh), 1).cuda(), _randn((1, H, n, Dh), 2).cuda(), _randn((1, 4, T, Dh), 3).cuda()
+    k2, v2 = _randn((1, H, T, Dh), 4).cuda(), _randn((1, H, T, Dh), 5).cuda()
+    slots, first, more = _i32([0]), _i32([n]), _i32([T])
+    busy = torch.randn((4096, 4096), device="cuda")
+    side, at = torch.cuda.Stream(), {}
+
+    def run(cache, kk, vv, qq, late):
+        ra.cache_reserve(cache, slots, first)
+        ra.cache_append(cache, 0, slots, None, k, v)
+        ra.cache_reserve(cache, slots, more)
+        if late:
+            side.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(side):
+                for _ in range(4):
+                    at["busy"] = busy @ busy
+                kk.copy_(k2)
+                vv.copy_(v2)
+            torch.cuda.current_stream().wait_stream(side)
+        ra.cache_append(cache, 0, slots, None, kk, vv)
+        if late:
+            side.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(side):
+                for _ in range(4):
+                    at["busy"] = busy @ busy
+                qq.copy_(q)
+            torch.cuda.current_stream().wait_stream(side)
+        return ra.cache_attend(cache, 0, slots, None, qq)
+
+    new = lambda: ra.kv_cache(1, 16, H, 32, Dh, 1, 16)  # noqa: E731
+    want = run(new(), k2, v2, q, False)
+    cache, late = new(), [torch.zeros_like(x) for x in (k2, v2, q)]
+    if captured:
+        busy @ busy
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got = run(cache, *late, True)
+        g.replay()
+    else:
+        got = run(cache, *late, True)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and ra.device_status() == 0
+
+
+def test_many_calls_back_to_back(ra):
+    """A hundred rounds of all calls without a pause give what the same rounds with pauses give."""
+    B, H, Dh, page = 6, 2, 64, 16
+    xs = [_randn((B, H, 7, Dh), 10 + i).cuda() for i in range(5)]
+    qs = [_randn((B, 4, 7, Dh), 20 + i).cuda() for i in range(5)]
+    slots, a, b = _i32([0, 1, 2, 3, 4, 5]), _i32([0, 1, 2]), _i32([3, 4, 5])
+    counts = [_i32([(3 * i + j) % 7 + 1 for j in range(B)]) for i in range(5)]
+    keep = _i32([20, 33, 47])
+
+    def rounds(pause):
+        cache, outs = ra.kv_cache(1, 400, H, page, Dh, B, 64), []
+        for i in range(100):
+            n = counts[i % 5]
+            ra.cache_reserve(cache, slots, n)
+            ra.cache_append(cache, 0, slots, n, xs[i % 5], xs[(i + 1) % 5])
+            o = torch.zeros_like(qs[0])
+            lse = torch.zeros(qs[0].shape[:3], device="cuda")
+            outs.append(ra.cache_attend(cache, 0, slots, n, qs[i % 5], out=o, lse=lse)[0])
+            if i % 10 == 9:
+                ra.cache_trim(cache, a, keep)
+                ra.cache_free(cache, b)
+                ra.cache_fork(cache, a, b)
+                ra.cache_compact(cache)
+            if pause:
+                torch.cuda.synchronize()
+        return torch.stack(outs), cache
+
+    (o1, c1), (o2, c2) = rounds(True), rounds(False)
+    assert ra.device_status() == 0
+    assert torch.equal(o1, o2)
+    for name in ("table", "lens", "refs"):
+        assert torch.equal(getattr(c1, name), getattr(c2, name))
+    assert torch.equal(ra.cache_read(c1, 0, slots, 100)[0], ra.cache_read(c2, 0, slots, 100)[0])
