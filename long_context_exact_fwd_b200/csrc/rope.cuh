@@ -13,7 +13,7 @@
 // Bound: memory (each element read and written once).  A thread owns one group of pairs of one
 // token and walks over heads, so one sine and cosine serve `heads_per_thread` heads of Q and K.
 // Measured on B200: 16384 tokens, 16 + 16 heads of 128, bf16: 49.1 us, 5.5 TB/s (84 % of a copy);
-// 8198 tokens, 8 + 2 heads, 96 of 128 columns, float32: 15.0 us.
+// 8198 tokens, 8 + 2 heads, 96 of 128 columns, interleaved float32: 13.2 us, 97 %.
 #pragma once
 #include <cstdint>
 #include <type_traits>
@@ -201,28 +201,6 @@ __global__ void __launch_bounds__(THREADS) rope_kernel(const Params p) {
   }
 }
 
-// N elements from element `at` of a warp's rows in shared memory.
-template <int N>
-__device__ __forceinline__ void window(const Pack<float, N>* rows, int at, float (&f)[N]) {
-#pragma unroll
-  for (int i = 0; i < N; ++i) f[i] = reinterpret_cast<const float*>(rows)[at + i];
-}
-template <int N>   // one that starts in the middle of a word is shifted
-__device__ __forceinline__ void window(const Pack<__nv_bfloat16, N>* rows, int at, float (&f)[N]) {
-  const uint32_t* words = reinterpret_cast<const uint32_t*>(rows) + (at >> 1);
-  const int shift = (at & 1) * 16;
-  uint32_t w[N / 2 + 1];
-#pragma unroll
-  for (int i = 0; i < N / 2; ++i) w[i] = words[i];
-  w[N / 2] = shift ? words[N / 2] : 0;
-#pragma unroll
-  for (int i = 0; i < N / 2; ++i) {
-    const uint32_t v = __funnelshift_r(w[i], w[i + 1], shift);
-    f[2 * i] = __uint_as_float(v << 16);
-    f[2 * i + 1] = __uint_as_float(v & 0xffff0000u);
-  }
-}
-
 // A thread's place: its token, and its unit of the row.
 struct Place {
   long long token, b, s;
@@ -258,33 +236,53 @@ __device__ __forceinline__ void each_tensor(const Params& p, const Place& at, in
   }
 }
 
-// The same for pairs that do not lie at a vector's distance, in rows that do start at vectors: a thread has one
-// vector of a row, and a half layout's partners, at any offset, come from the row's other threads through
-// shared memory (a row's threads are in one warp; outputs may be the inputs, so a row is read before it is
-// written).  Measured, float32 columns of a projection: half, 38 of 128, 19516 tokens, 16 + 8 heads: 79 us, 93 % of a
-// copy (rope_kernel, element by element, 164); bf16 is bound by its instructions: 30 of 64, 64 + 16 heads 51 %.
+// The same by whole rows, where a row starts at a vector: for pairs at any distance, and for interleaved ones.  A
+// thread has one vector of a row; a half layout's partners, and its angles, come from the row's other threads
+// through shared memory (they are in one warp; outputs may be the inputs, so a row is read before it is written).
+// Measured, columns of a projection: half, float32, 38 of 128, 19516 tokens, 16 + 8 heads 74 us, 99 % of a copy
+// (rope_kernel, element by element, 164); bf16, 30 of 64, 11710 tokens, 64 + 16 heads 48 us, 76 % (147).  Bound
+// there by instructions: partners read as shifted words, with a branch for each half, took 72 us.
 template <typename T, int N, bool INTERLEAVED>
 __global__ void __launch_bounds__(THREADS) rope_rows_kernel(const Params p) {
-  // a warp's rows, with room for a window that begins before the first or ends behind the last
-  __shared__ Pack<T, N> rows[INTERLEAVED ? 1 : THREADS / 32][INTERLEAVED ? 1 : HEADS_AT_ONCE][34];
+  __shared__ Pack<T, N> rows[INTERLEAVED ? 1 : THREADS / 32][INTERLEAVED ? 1 : HEADS_AT_ONCE][32];
   const Place at = place(p);
   if (at.token >= p.tokens) return;
   const int col = at.unit * N, half = p.rot / 2, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const bool rotated = col < p.rot;
   float c[N], sn[N];                         // y = x c + partner sn
-  if (rotated) {
-    const long long pos = p.pos ? p.pos[at.b * p.pos_b + at.s * p.pos_s] : p.offset + at.s;
-    const float amplitude = p.inverse ? -p.amplitude : p.amplitude;
+  int partner[N];                            // half: its place in the warp's rows
 #pragma unroll
-    for (int i = 0; i < N; i += INTERLEAVED ? 2 : 1) {
-      const int j = min(col + i, p.rot - 1);
-      const bool first = INTERLEAVED || j < half;
-      turn(static_cast<unsigned long long>(pos) * p.steps[INTERLEAVED ? j / 2 : first ? j : j - half], c[i], sn[i]);
-      c[i] *= p.amplitude;
-      sn[i] *= first ? -amplitude : amplitude;
-      if (INTERLEAVED) {
+  for (int i = 0; i < N; ++i) {
+    const int j = col + i;
+    partner[i] = lane * N + i + (j < half ? half : j < p.rot ? -half : 0);
+  }
+  const long long pos = p.pos ? p.pos[at.b * p.pos_b + at.s * p.pos_s] : p.offset + at.s;
+  auto angle = [&](int i, float& co, float& si) {
+    turn(static_cast<unsigned long long>(pos) * p.steps[i], co, si);
+    co *= p.amplitude;
+    si *= p.inverse ? -p.amplitude : p.amplitude;
+  };
+  if constexpr (INTERLEAVED) {
+    if (rotated) {
+#pragma unroll
+      for (int i = 0; i < N; i += 2) {
+        angle(min(col + i, p.rot - 1) / 2, c[i], sn[i + 1]);
         c[i + 1] = c[i];
-        sn[i + 1] = -sn[i];
+        sn[i] = -sn[i + 1];
+      }
+    }
+  } else {                                   // a row's threads share its angles out
+    __shared__ float2 angles[THREADS / 32][16 * N];
+    float2* mine = angles[warp] + (lane - at.unit) * (N / 2);
+    for (int i = at.unit; i < half; i += p.units) angle(i, mine[i].x, mine[i].y);
+    __syncwarp();
+    if (rotated) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int j = min(col + i, p.rot - 1);
+        const float2 cs = mine[j < half ? j : j - half];
+        c[i] = cs.x;
+        sn[i] = j < half ? -cs.y : cs.y;
       }
     }
   }
@@ -298,7 +296,7 @@ __global__ void __launch_bounds__(THREADS) rope_rows_kernel(const Params p) {
         __syncwarp();
 #pragma unroll
         for (int k = 0; k < HEADS_AT_ONCE; ++k)
-          if (h + k < n) rows[warp][k][1 + lane] = a[k];
+          if (h + k < n) rows[warp][k][lane] = a[k];
         __syncwarp();
       }
 #pragma unroll
@@ -311,18 +309,10 @@ __global__ void __launch_bounds__(THREADS) rope_rows_kernel(const Params p) {
 #pragma unroll
             for (int i = 0; i < N; ++i) z[i] = f[i ^ 1];
           } else {
-            const int own = (1 + lane) * N;    // this thread's first element
-            if (col + N <= half) {
-              window<N>(rows[warp][k], own + half, z);
-            } else if (col >= half) {
-              window<N>(rows[warp][k], own - half, z);
-            } else {                           // the halves meet in this vector
-              float low[N];
-              window<N>(rows[warp][k], own + half, z);
-              window<N>(rows[warp][k], own - half, low);
+            T other[N];
 #pragma unroll
-              for (int i = 0; i < N; ++i) z[i] = col + i < half ? z[i] : low[i];
-            }
+            for (int i = 0; i < N; ++i) other[i] = reinterpret_cast<const T*>(rows[warp][k])[partner[i]];
+            widen<N>(other, z);
           }
 #pragma unroll
           for (int i = 0; i < N; ++i) f[i] = fmaf(f[i], c[i], z[i] * sn[i]);

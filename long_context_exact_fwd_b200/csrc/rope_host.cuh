@@ -42,24 +42,19 @@ int rope_tensor(ra::rope::Tensor* t, const void* x, void* y, int H, const long l
   return RA_OK;
 }
 
-// As many heads per thread (one sine and cosine for all of them) as leave 8 blocks per SM.  Measured
-// (16K prompt / float32 gradient): 4 blocks 53.6 / 15.2 us, 8 49.5 / 15.0, 16 50.9 / 16.3, 32 58.9 / 19.2.
-int rope_heads(const ra::rope::Params& p, int units, int sm_count) {
-  const long long blocks = (p.tokens * units + ra::rope::THREADS - 1) / ra::rope::THREADS;
-  const int heads = p.t[0].heads + p.t[1].heads;
-  int hpt = 1;
-  while (hpt < heads && hpt < 16 && blocks * ((heads + 2 * hpt - 1) / (2 * hpt)) >= 8ll * sm_count) hpt *= 2;
-  return hpt;
-}
-
 // One thread a unit of a token, p.units of them a row.
 int rope_launch(void (*kernel)(ra::rope::Params), ra::rope::Params& p, int sm_count, cudaStream_t stream) {
   using namespace ra::rope;
   const long long threads = p.tokens * p.units;
   p.wide_ids = threads > UINT_MAX - THREADS;
   const long long blocks = (threads + THREADS - 1) / THREADS;
-  p.heads_per_thread = rope_heads(p, p.units, sm_count);
-  const int gy = (p.t[0].heads + p.t[1].heads + p.heads_per_thread - 1) / p.heads_per_thread;
+  const int heads = p.t[0].heads + p.t[1].heads;
+  // As many heads per thread (one sine and cosine for all of them) as leave 8 blocks per SM.  Measured
+  // (16K prompt / float32 gradient): 4 blocks 53.6 / 15.2 us, 8 49.5 / 15.0, 16 50.9 / 16.3, 32 58.9 / 19.2.
+  int hpt = 1;
+  while (hpt < heads && hpt < 16 && blocks * ((heads + 2 * hpt - 1) / (2 * hpt)) >= 8ll * sm_count) hpt *= 2;
+  p.heads_per_thread = hpt;
+  const int gy = (heads + hpt - 1) / hpt;
   if (blocks > INT_MAX || gy > 65535) return RA_ERR_SHAPE;
   kernel<<<dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(gy)), THREADS, 0, stream>>>(p);
   return launch_status();
@@ -70,10 +65,16 @@ int rope_units(ra::rope::Params& p, int sm_count, bool interleaved, cudaStream_t
   using namespace ra::rope;
   p.rot_units = interleaved ? p.rot / N : p.rot / 2 / N;
   p.units = p.rot_units + (p.Dh - p.rot) / N;
-  if constexpr (N >= 2) {
+  if constexpr (N == 2) {
     if (interleaved) return rope_launch(rope_kernel<T, N, true, VECTOR>, p, sm_count, stream);
   }
   return rope_launch(rope_kernel<T, N, false, VECTOR>, p, sm_count, stream);
+}
+
+template <typename T, int N, bool INTERLEAVED>
+int rope_rows(ra::rope::Params& p, int sm_count, cudaStream_t stream) {
+  p.units = p.Dh / N;
+  return rope_launch(ra::rope::rope_rows_kernel<T, N, INTERLEAVED>, p, sm_count, stream);
 }
 
 template <typename T>
@@ -93,30 +94,25 @@ int rope_dispatch(ra::rope::Params& p, int sm_count, bool interleaved, cudaStrea
   };
   // and the pairs' distance and the untouched rest.
   auto fits = [&](int m) { return (interleaved ? p.rot : p.rot / 2) % m == 0 && (p.Dh - p.rot) % m == 0 && rows_fit(m); };
+  if (interleaved) {
+    // rope_rows_kernel (float32 gradient 13.2 us, rope_kernel 14.9; bf16, 40 of 64, 64 + 16 heads 43 and 53)
+    if constexpr (WIDE == 8) {
+      if (rows_fit(8)) return rope_rows<T, 8, true>(p, sm_count, stream);
+    }
+    if (rows_fit(4)) return rope_rows<T, 4, true>(p, sm_count, stream);
+    if (fits(2)) return rope_units<T, 2, true>(p, sm_count, true, stream);
+    return rope_units<T, 2, false>(p, sm_count, true, stream);   // a pair is still one thread's: rot and Dh are even
+  }
+  // Half: rope_kernel where the pairs lie at a vector's distance (the 16K prompt 49 us, rope_rows_kernel 53), else
+  // rope_rows_kernel (bf16, 30 of 64, 64 + 16 heads 48 us, rope_kernel 147; 102 of 128, 2 + 2 heads 54 and 94).
+  // Vectors of 4 bf16 there: of 8, 52 and 43 us.
   if constexpr (WIDE == 8) {
-    if (fits(8)) return rope_units<T, 8, true>(p, sm_count, interleaved, stream);
-  } else {
-    if (fits(4)) return rope_units<T, 4, true>(p, sm_count, interleaved, stream);
+    if (fits(8)) return rope_units<T, 8, true>(p, sm_count, false, stream);
   }
-  if constexpr (WIDE == 8) {
-    if (fits(4)) return rope_units<T, 4, true>(p, sm_count, interleaved, stream);
-  }
-  // Rows of vectors with pairs at an odd distance: rope_rows_kernel, which takes every angle twice in the half
-  // layout and so needs heads to share it among where pairs of elements would fit.  Measured, that and
-  // rope_kernel: half, bf16, rot 30 of 64, 64 + 16 heads 72 and 147 us; 102 of 128, 2 + 2 heads 72 and 94; two
-  // elements fit, 76 of 128, 64 + 16 heads 68 and 92, 60 of 64, 2 + 2 heads 40 and 30; interleaved, float32, 106 of
-  // 128, 8 + 4 heads 34 and 47.  Vectors of 4 bf16 (8: 90 us in the first).
-  constexpr int ROWS_N = 4;
-  const int units = p.Dh / ROWS_N;
-  if (rows_fit(ROWS_N)) {
-    p.units = units;
-    if (interleaved) return rope_launch(ra::rope::rope_rows_kernel<T, ROWS_N, true>, p, sm_count, stream);
-    if (units <= 32 && 32 % units == 0 && (!fits(2) || rope_heads(p, units, sm_count) >= 8))
-      return rope_launch(ra::rope::rope_rows_kernel<T, ROWS_N, false>, p, sm_count, stream);
-  }
-  if (fits(2)) return rope_units<T, 2, true>(p, sm_count, interleaved, stream);
-  // Nothing lines up: element by element (an interleaved pair is still one thread's; rot and Dh are even).
-  if (interleaved) return rope_units<T, 2, false>(p, sm_count, true, stream);
+  if (fits(4)) return rope_units<T, 4, true>(p, sm_count, false, stream);
+  const int units = p.Dh / 4;
+  if (rows_fit(4) && units <= 32 && 32 % units == 0) return rope_rows<T, 4, false>(p, sm_count, stream);
+  if (fits(2)) return rope_units<T, 2, true>(p, sm_count, false, stream);
   return rope_units<T, 1, false>(p, sm_count, false, stream);
 }
 

@@ -222,3 +222,17 @@ def test_rotated_widths_that_no_vector_divides(ra, Dh, rot, inter, dtype):
             assert torch.equal(x.nan_to_num(nan=5.0), want.nan_to_num(nan=5.0))
         assert torch.equal(rows[:, :, H + Hk:].isnan(), keep[:, :, H + Hk:].isnan())
         rows.copy_(keep)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("shift,rot", [(4, 128), (4, 30), (2, 64), (2, 30), (1, 64), (8, 90)])
+def test_rows_that_start_at_smaller_vectors(ra, shift, rot, inter, dtype):
+    B, S, H, Dh = 2, 6, 5, 128
+    w, _ = ra.rope_inv_freq(rot)
+    x = _x((B, H, S, Dh + shift), dtype, 31)[..., shift:]
+    p2 = np.broadcast_to(np.arange(50, 50 + S), (B, S))
+    y = ra.rope(x, ra.rope_plan(w, "interleaved" if inter else "half"), offset=50)
+    _check(y, x, p2, w.numpy(), inter, 1.0)
+    ra.rope(x, ra.rope_plan(w, "interleaved" if inter else "half"), offset=50, out=x)
+    assert torch.equal(x, y)
