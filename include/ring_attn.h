@@ -407,9 +407,9 @@ RA_API int ring_attn_cache_read(const ra_cache* cache, int layer, const int* slo
  *             are left as they were; a query that sees nothing has o = 0, lse = -inf.
  *   workspace ring_attn_cache_attend_workspace_size bytes, 256-byte aligned, of this call alone while
  *             it runs; contents on entry do not matter.
- * o must not overlap q (RA_ERR_ARG).  exp(s - lse) is rounded to fp16 (11 bits) before it multiplies v, value
- * scales are applied relative to the largest met (values below 2^-39 of a context's largest are lost to it);
- * sums are float32.  Calls with 64 rows and more per head (T * Hq / heads) run on tcgen05.  Two launches; a
+ * o must not overlap q (RA_ERR_ARG).  exp(s - lse) times the value scale of the token's page is rounded to fp16
+ * before it multiplies the code of v: 11 bits where it is above 2^-21 of the largest that the query itself has, an
+ * absolute 2^-32 of that below (tokens that it does not see have no part in this); sums are float32.  Calls with 64 rows and more per head (T * Hq / heads) run on tcgen05.  Two launches; a
  * bounded wait that gave up leaves RA_ERR_TIMEOUT in the device status word.
  */
 RA_API size_t ring_attn_cache_attend_workspace_size(int T, int Hq, int Hkv, int Dh);

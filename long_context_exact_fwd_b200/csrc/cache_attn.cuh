@@ -12,10 +12,14 @@
 //
 // Numbers.  Codes are exact in fp16.  A query row is scaled by a power of two to just below fp16's
 // top and keeps its bf16 values exactly down to 2^-29 of the row's largest; scores and sums are
-// fp32.  exp uses a reference that is raised when a score passes it by 2^8; P is rounded to fp16
-// (half a step, 2^-11 of the term; bf16's is 2^-8) at 2^7 times its value, so terms down to 2^-21 of the
-// largest keep all 11 bits and smaller ones an absolute 2^-32.  P carries the value scale of its page
-// relative to the largest met so far (a power of two); the sum for lse uses unrounded terms.
+// fp32.  P carries the value scale 2^e_j of its page, and is rounded to fp16 (half a step, 2^-11 of the term;
+// bf16's is 2^-8).  Each row has two references, raised when a term passes one by 2^8: R over its scores
+// x_j (log2 units) and R + K, K a whole number, over x_j + e_j:
+//   w_j = 2^(x_j + e_j - R - K + 7),   l = sum 2^(K - 7 - e_j) w_j,   o = 2^(K - 7) sum w_j code_j / l,
+// so that P's bits go by what a token adds to the row's own result: terms down to 2^-21 of the row's largest
+// softmax weight x value scale keep all 11 bits, smaller ones an absolute 2^-32 of it.  (One unit for a warp's rows,
+// from the largest scale read, lost rows whose weight lay on pages of small values.)  w_j is taken at no less
+// than 2^-93 of 2^(x_j - R), where it is 0 in fp16 and l still has it; the sums use unrounded terms.
 //
 // Bound: memory, 2 Dh bytes per token and head.  Work is a line of 32-token tiles over (sequence,
 // head, row block); every block takes an equal stretch of it, whatever the lengths (they are only
@@ -48,7 +52,9 @@ constexpr int AT_START = 16;
 // 8 10.0 / 12.4, 16 12.1 / 13.7.
 constexpr int AT_LEAST = 4;
 constexpr float AT_RAISE = 8.f;      // log2: P <= 2^8, times 2^7 still an fp16 number
-constexpr float AT_P_UNIT = 128.f;
+constexpr float AT_P_LOG2 = 7.f;     // P is held at 2^7 times its value
+constexpr float AT_W_LEAST = -93.f;  // log2 of w_j / 2^(x_j - R), at least
+constexpr float AT_L_MOST = 9.903520314283042e27f;   // 2^93
 constexpr float NOTHING = 3.4028234663852886e38f;   // minus the reference of a row that has seen nothing: any score raises it
 
 struct AttendParams {
@@ -150,6 +156,20 @@ __device__ __forceinline__ void store_row(const AttendParams& p, int b, int h, i
         make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
   if (d == 0) p.lse[at] = z == 0.f ? -INFINITY : (m + log2f(z)) * 0.69314718055994531f;
 }
+
+// Of parts that are joined: l and O of one whose reference lies d <= 0 above the common one, times 2^d.  In two
+// halves: a part of small weight and large values may be the result, and 2^d alone ends at 2^-126.
+struct Scaled {
+  float h;
+  __device__ __forceinline__ explicit Scaled(float d) : h(d == 0.f ? 1.f : ex2_approx(0.5f * d)) {}
+  __device__ __forceinline__ float operator()(float x) const { return x * h * h; }
+  __device__ __forceinline__ float4 operator()(const float4& x) const {
+    return make_float4((*this)(x.x), (*this)(x.y), (*this)(x.z), (*this)(x.w));
+  }
+  __device__ __forceinline__ void add(const float4& x, float4& a) const {
+    a = make_float4(fmaf(x.x * h, h, a.x), fmaf(x.y * h, h, a.y), fmaf(x.z * h, h, a.z), fmaf(x.w * h, h, a.w));
+  }
+};
 
 template <int HD, int NT>
 __global__ void __launch_bounds__(AT_THREADS, at_per_sm(HD, NT)) attend_kernel(const AttendParams p) {
@@ -356,18 +376,18 @@ __global__ void __launch_bounds__(AT_THREADS, at_per_sm(HD, NT)) attend_kernel(c
       }
 
     float o[KS][NT][4];
-    float2 neg_ref[NT], l[NT];                // minus the reference, and the sum, of columns 2 gc, 2 gc + 1
+    // of columns 2 gc, 2 gc + 1: minus R, minus (R + K), the sum, and 2^(K - 7), the unit of O
+    float2 neg_ref[NT], neg_top[NT], l[NT], unit[NT];
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-      neg_ref[j] = make_float2(NOTHING, NOTHING);
+      neg_ref[j] = neg_top[j] = make_float2(NOTHING, NOTHING);
+      unit[j] = make_float2(two_to(-7), two_to(-7));
       l[j] = make_float2(0.f, 0.f);
 #pragma unroll
       for (int m = 0; m < KS; ++m)
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[m][j][i] = 0.f;
     }
-    float p_unit = 0.f;                       // AT_P_UNIT / v_ref
-    float v_ref = 0.f;                        // largest value scale so far; O is in units of it
 
     for (int i = 0; i < count; ++i) {
       cp_async_wait<STAGES - 2>();
@@ -408,8 +428,10 @@ __global__ void __launch_bounds__(AT_THREADS, at_per_sm(HD, NT)) attend_kernel(c
 
       // log2 units, mask, and the largest of each column
       const bool masked = tok0 + AT_TILE > lim_min;
-      float top = -INFINITY;                  // over the reference
-      float2 mx[NT];
+      const int e0 = exponent_of(sc.z), e1 = exponent_of(sc.w);   // of the halves' value scales
+      const float2 up0 = make_float2(e0, e0), up1 = make_float2(e1, e1);
+      float top = -INFINITY;                  // over a reference
+      float2 mx[NT], my[NT];                  // largest score, and largest with its value scale
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
 #pragma unroll
@@ -426,33 +448,37 @@ __global__ void __launch_bounds__(AT_THREADS, at_per_sm(HD, NT)) attend_kernel(c
             if (limit[j][1] - tok0 - gr <= 8 * i) s[i >> 1][j][i & 1].y = -INFINITY;
           }
         }
-        mx[j] = make_float2(fmaxf(fmaxf(s[0][j][0].x, s[0][j][1].x), fmaxf(s[1][j][0].x, s[1][j][1].x)),
-                            fmaxf(fmaxf(s[0][j][0].y, s[0][j][1].y), fmaxf(s[1][j][0].y, s[1][j][1].y)));
-        const float2 over = __fadd2_rn(mx[j], neg_ref[j]);
-        top = fmaxf(top, fmaxf(over.x, over.y));
+        const float2 m0 = make_float2(fmaxf(s[0][j][0].x, s[0][j][1].x), fmaxf(s[0][j][0].y, s[0][j][1].y));
+        const float2 m1 = make_float2(fmaxf(s[1][j][0].x, s[1][j][1].x), fmaxf(s[1][j][0].y, s[1][j][1].y));
+        const float2 y0 = __fadd2_rn(m0, up0), y1 = __fadd2_rn(m1, up1);
+        mx[j] = make_float2(fmaxf(m0.x, m1.x), fmaxf(m0.y, m1.y));
+        my[j] = make_float2(fmaxf(y0.x, y1.x), fmaxf(y0.y, y1.y));
+        const float2 over = __fadd2_rn(mx[j], neg_ref[j]), over_y = __fadd2_rn(my[j], neg_top[j]);
+        top = fmaxf(fmaxf(top, fmaxf(over.x, over.y)), fmaxf(over_y.x, over_y.y));
       }
-      const float v_max = fmaxf(sc.z, sc.w);
-      const bool raise_v = v_max > v_ref;               // the same in the whole warp
-      if (__any_sync(0xffffffffu, top > AT_RAISE) || raise_v) {
-        float fv = 1.f;                                 // powers of two: exact
-        if (raise_v) {
-          fv = v_ref / v_max;
-          v_ref = v_max;
-          p_unit = AT_P_UNIT / v_max;
-        }
-        auto raised = [&](float& ref, float& sum, float m) {   // returns what O has to be multiplied by
-          m = fmaxf(-ref, m);
+      if (__any_sync(0xffffffffu, top > AT_RAISE)) {
+        auto largest = [](float m) {
           m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
           m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
-          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-          const float a = -ref == m ? 1.f : ex2_approx(-ref - m);
+          return fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+        };
+        // returns what O has to be multiplied by
+        auto raised = [&](float& ref, float& ref_top, float& sum, float& u, float m, float y) {
+          m = largest(fmaxf(-ref, m));
+          y = largest(fmaxf(-ref_top, y));
+          // never above the largest; both references still at NOTHING: 0
+          const float k = fminf(fmaxf(floorf(y - m), E_MIN), E_MAX);
+          const float a = -ref - m, f = -ref_top - (m + k);
+          sum *= a == 0.f ? 1.f : ex2_approx(a);
           ref = -m;
-          sum *= a;
-          return a * fv;
+          ref_top = -(m + k);
+          u = two_to(static_cast<int>(k) - 7);
+          return f == 0.f ? 1.f : ex2_approx(f);
         };
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-          const float f0 = raised(neg_ref[j].x, l[j].x, mx[j].x), f1 = raised(neg_ref[j].y, l[j].y, mx[j].y);
+          const float f0 = raised(neg_ref[j].x, neg_top[j].x, l[j].x, unit[j].x, mx[j].x, my[j].x);
+          const float f1 = raised(neg_ref[j].y, neg_top[j].y, l[j].y, unit[j].y, mx[j].y, my[j].y);
 #pragma unroll
           for (int k = 0; k < KS; ++k) {
             o[k][j][0] *= f0;
@@ -467,18 +493,23 @@ __global__ void __launch_bounds__(AT_THREADS, at_per_sm(HD, NT)) attend_kernel(c
       uint32_t pf[2][NT][2];
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        const float w = (half ? sc.w : sc.z) * p_unit;
+        const int e = half ? e1 : e0;
+        const float up = static_cast<float>(e) + AT_P_LOG2, inv = two_to(-e);
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-          float2 e[2];
+          const float2 least = __fadd2_rn(neg_ref[j], make_float2(AT_W_LEAST, AT_W_LEAST));
+          float2 at = __fadd2_rn(neg_top[j], make_float2(up, up));
+          at = make_float2(fmaxf(at.x, least.x), fmaxf(at.y, least.y));
+          float2 back = __fmul2_rn(unit[j], make_float2(inv, inv));
+          back = make_float2(fminf(back.x, AT_L_MOST), fminf(back.y, AT_L_MOST));
+          float2 w[2];
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
-            const float2 x = __fadd2_rn(s[half][j][y], neg_ref[j]);
-            e[y] = make_float2(ex2_approx(x.x), ex2_approx(x.y));
-            const float2 wide = __fmul2_rn(e[y], make_float2(w, w));
-            pf[half][j][y] = transpose8(pack_half2(wide.x, wide.y));
+            const float2 x = __fadd2_rn(s[half][j][y], at);
+            w[y] = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+            pf[half][j][y] = transpose8(pack_half2(w[y].x, w[y].y));
           }
-          l[j] = __fadd2_rn(l[j], __fadd2_rn(e[0], e[1]));
+          l[j] = __ffma2_rn(__fadd2_rn(w[0], w[1]), back, l[j]);
         }
       }
 
@@ -541,7 +572,6 @@ __global__ void __launch_bounds__(AT_THREADS, at_per_sm(HD, NT)) attend_kernel(c
     cp_async_wait<0>();
     __syncwarp();
     float* mine = reinterpret_cast<float*>(ring_ptr);   // [ROWS][HD]
-    const float unit = v_ref * (1.f / AT_P_UNIT);
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -551,6 +581,7 @@ __global__ void __launch_bounds__(AT_THREADS, at_per_sm(HD, NT)) attend_kernel(c
         z += __shfl_xor_sync(0xffffffffu, z, 8);
         z += __shfl_xor_sync(0xffffffffu, z, 16);
         const int r = j * 8 + 2 * gc + e;
+        const float u = e ? unit[j].y : unit[j].x;
         if (gr == 0) {
           s_ml[(warp * 32 + r) * 2] = z == 0.f ? -INFINITY : -(e ? neg_ref[j].y : neg_ref[j].x);
           s_ml[(warp * 32 + r) * 2 + 1] = z;
@@ -558,8 +589,7 @@ __global__ void __launch_bounds__(AT_THREADS, at_per_sm(HD, NT)) attend_kernel(c
 #pragma unroll
         for (int k = 0; k < KS / 2; ++k)
           *reinterpret_cast<float4*>(mine + r * HD + gr * (HD / 8) + 4 * k) =
-              make_float4(o[2 * k][j][e] * unit, o[2 * k][j][e + 2] * unit, o[2 * k + 1][j][e] * unit,
-                          o[2 * k + 1][j][e + 2] * unit);
+              make_float4(o[2 * k][j][e] * u, o[2 * k][j][e + 2] * u, o[2 * k + 1][j][e] * u, o[2 * k + 1][j][e + 2] * u);
       }
     __syncthreads();
     const bool whole = t0 == 0 && t1 == nt;
@@ -578,10 +608,9 @@ __global__ void __launch_bounds__(AT_THREADS, at_per_sm(HD, NT)) attend_kernel(c
       for (int w = 0; w < AT_WARPS; ++w) {
         const float mw = s_ml[(w * 32 + r) * 2], zw = s_ml[(w * 32 + r) * 2 + 1];
         if (zw == 0.f) continue;              // saw nothing
-        const float f = mw == m ? 1.f : ex2_approx(mw - m);
-        const float4 y = *reinterpret_cast<const float4*>(smem + w * L::RING + (r * HD + d) * 4);
-        z += zw * f;
-        a = make_float4(fmaf(y.x, f, a.x), fmaf(y.y, f, a.y), fmaf(y.z, f, a.z), fmaf(y.w, f, a.w));
+        const Scaled f(mw == m ? 0.f : mw - m);
+        z += f(zw);
+        f.add(*reinterpret_cast<const float4*>(smem + w * L::RING + (r * HD + d) * 4), a);
       }
       if (unseen) {
         const int lim = limit_of(r);
@@ -655,16 +684,16 @@ __global__ void __launch_bounds__(LOT * WARPS * 32) join_kernel(const AttendPara
     float top = m;
 #pragma unroll
     for (int i = 0; i < AT_ONCE; ++i) top = fmaxf(top, ml[i].x);
-    const float old = m == top ? 1.f : ex2_approx(m - top);   // nothing yet: 0, or both -inf
+    const Scaled old(m == top ? 0.f : m - top);               // nothing yet: 0, or both -inf
     m = top;
-    z *= old;
-    a = make_float4(a.x * old, a.y * old, a.z * old, a.w * old);
+    z = old(z);
+    a = old(a);
 #pragma unroll
     for (int i = 0; i < AT_ONCE; ++i) {
       if (ml[i].y == 0.f) continue;           // saw nothing, or no part
-      const float f = ml[i].x == m ? 1.f : ex2_approx(ml[i].x - m);
-      z += ml[i].y * f;
-      a = make_float4(fmaf(y[i].x, f, a.x), fmaf(y[i].y, f, a.y), fmaf(y[i].z, f, a.z), fmaf(y[i].w, f, a.w));
+      const Scaled f(ml[i].x == m ? 0.f : ml[i].x - m);
+      z += f(ml[i].y);
+      f.add(y[i], a);
     }
   }
   if (lane < GROUPS) s_o[rr][w][lane] = a;
@@ -680,10 +709,9 @@ __global__ void __launch_bounds__(LOT * WARPS * 32) join_kernel(const AttendPara
   for (int i = 0; i < WARPS; ++i) {
     const float2 ml = s_ml[rr][i];
     if (ml.y == 0.f) continue;
-    const float f = ml.x == m ? 1.f : ex2_approx(ml.x - m);
-    const float4 y = s_o[rr][i][lane];
-    z += ml.y * f;
-    a = make_float4(fmaf(y.x, f, a.x), fmaf(y.y, f, a.y), fmaf(y.z, f, a.z), fmaf(y.w, f, a.w));
+    const Scaled f(ml.x == m ? 0.f : ml.x - m);
+    z += f(ml.y);
+    f.add(s_o[rr][i][lane], a);
   }
   store_row<HD>(p, b, h, row0 + r, 4 * lane, m, z, a);
 }

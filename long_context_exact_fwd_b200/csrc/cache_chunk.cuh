@@ -12,8 +12,8 @@
 // The operands are fp16: codes are exact in it (one conversion instruction per two; as bf16 the
 // scale would have to be multiplied in), a query row is scaled to its range by a power of two.
 // The scales never touch the tiles: a page's key scale multiplies its 16-column groups of scores, and
-// its value scale, a power of two, is added to the exponent of P relative to the largest so far:
-//   w_j = 2^(x_j - ref + dv_j + 7),   l += 2^-(dv_j + 7) w_j,   dv_j = e_j - e_max <= 0.
+// its value scale 2^e_j goes into P with the row's two references, R and R + K, as in attend_kernel:
+//   w_j = 2^(x_j - R + max(e_j + 7 - K, -93)),   l += min(2^(K - 7 - e_j), 2^93) w_j,   o = 2^(K - 7) O / l.
 // Work is cut as in attend_kernel: one line of 128-key tiles over all items, equal stretches, parts
 // joined by chunk_join_kernel.
 // Bound: the products, and shared memory, which both operands of S, the tiles of V and the conversion go
@@ -34,16 +34,12 @@ static_assert(2 * (CH_REGS_SOFTMAX - CH_REGS_LAUNCH) <= CH_REGS_LAUNCH - CH_REGS
 constexpr int CH_MAX_CTAS = 160;      // blocks that the workspace has room for (one per SM)
 constexpr int CH_START = 3;          // what starting and ending an item costs, in tiles
 constexpr int CH_LEAST = 4;          // tiles of a stretch, at least
-constexpr int CH_P_LOG2 = 7;         // P is held at 2^7 times its value
-constexpr float CH_DV_MIN = -100.f;  // below, P's fp16 is 0 whatever follows
 
 // Scale constants of one key tile: groups of 16 keys.
 struct alignas(16) ChScales {
   float k[8];        // key scale
-  float add[8];      // dv + 7
-  float fac[8];      // 2^-(dv + 7)
-  float rescale;     // what O has to be multiplied by for the new e_max (1: nothing)
-  float unit;        // 2^(e_max - 7): true value of O's unit
+  float up[8];       // e + 7, 2^e the value scale
+  float inv[8];      // 2^-e
   unsigned lots;     // of the tile's eight, those that have a page
 };
 
@@ -161,12 +157,12 @@ __device__ void ch_fetch(const AttendParams& p, ChWalk w, uint8_t* smem, uint32_
     const int len = w.len(), h = w.h;
     const int* table = c.table + static_cast<long long>(w.slot()) * c.max_pages;
     int pid = ch_pages(p, table, len, w.t0);
-    float v_max = 0.f;                                   // largest value scale so far
     for (int tile = w.t0; tile < w.t1 && ok; ++tile) {
-      float sk = 1.f, sv = 0.f;                          // none: no key of the lot is seen
+      float sk = 1.f;                                    // no page: its codes will be 0
+      int e = E_MIN;
       if (pid >= 0) {
         sk = c.k_scale[static_cast<long long>(pid) * c.heads + h];
-        sv = c.v_scale[static_cast<long long>(pid) * c.heads + h];
+        e = exponent_of(c.v_scale[static_cast<long long>(pid) * c.heads + h]);
       }
       const int pid_next = tile + 1 < w.t1 ? ch_pages(p, table, len, tile + 1) : -1;
       const unsigned lots = __ballot_sync(0xffffffffu, pid >= 0) & 0xffu;
@@ -178,24 +174,13 @@ __device__ void ch_fetch(const AttendParams& p, ChWalk w, uint8_t* smem, uint32_
         ok = ok && __all_sync(0xffffffffu, mbar_wait(bar(L::B_KV_EMPTY + stage), phase ^ 1u, abort_flag));
         if (!ok) break;
         if (kv == 0) {                                   // before this tile's keys can be multiplied
-          float top = sv;
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
-          const float all = fmaxf(v_max, top);
           ChScales* s = scales + scale_slot;
           if (lane < 8) {
-            const float dv = sv > 0.f ? fmaxf(static_cast<float>(exponent_of(sv) - exponent_of(all)), CH_DV_MIN) : CH_DV_MIN;
             s->k[lane] = sk;
-            s->add[lane] = dv + CH_P_LOG2;
-            s->fac[lane] = two_to(-static_cast<int>(dv) - CH_P_LOG2);
+            s->up[lane] = static_cast<float>(e) + AT_P_LOG2;
+            s->inv[lane] = two_to(-e);
           }
-          if (lane == 0) {
-            s->rescale = all > v_max ? (v_max > 0.f ? v_max / all : 0.f) : 1.f;
-            s->unit = all > 0.f ? two_to(max(exponent_of(all) - CH_P_LOG2, -126)) : 0.f;
-            s->lots = lots;
-          }
-          v_max = all;
+          if (lane == 0) s->lots = lots;
           scale_slot = (scale_slot + 1) & 3;
           __syncwarp();
         }
@@ -474,7 +459,7 @@ __device__ void ch_softmax(int t, const AttendParams& p, ChWalk w, int per, uint
     const bool row_ok = r < rows;
     const int lim = row_ok ? w.limit(row0 + r) : w.len();
     const int lim_first = w.limit(row0 + min(t * CH_BM, rows - 1));
-    float m_ref = -INFINITY, l = 0.f, unit = 0.f;
+    float m_ref = -INFINITY, top = -INFINITY, K = 0.f, l = 0.f, unit = two_to(-7);   // R, R + K, 2^(K - 7)
     int n = 0;
     for (int tile = w.t0; tile < w.t1; ++tile, ++n) {
       if (!__all_sync(0xffffffffu, mbar_wait(bar(L::B_S_FULL + t), s_phase, abort_flag))) return;
@@ -493,7 +478,7 @@ __device__ void ch_softmax(int t, const AttendParams& p, ChWalk w, int per, uint
         for (int c = 0; c < CH_BN; ++c)
           if (c >= left) s[c] = __float_as_uint(-INFINITY);
       }
-      float m_tile = -INFINITY;
+      float m_tile = -INFINITY, y_tile = -INFINITY;   // largest score, and largest with its value scale 2^(e + 7)
 #pragma unroll
       for (int g1 = 0; g1 < 8; ++g1) {
         float a = -INFINITY, b = -INFINITY;
@@ -502,14 +487,22 @@ __device__ void ch_softmax(int t, const AttendParams& p, ChWalk w, int per, uint
           a = fmax3(a, __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
           b = fmax3(b, __uint_as_float(s[c + 2]), __uint_as_float(s[c + 3]));
         }
-        m_tile = fmaxf(m_tile, fmaxf(a, b) * ch_factor(row_scale, sc->k[g1]));
+        const float m = fmaxf(a, b) * ch_factor(row_scale, sc->k[g1]);
+        m_tile = fmaxf(m_tile, m);
+        y_tile = fmaxf(y_tile, m + sc->up[g1]);
       }
-      const float m_new = fmaxf(m_ref, m_tile);
-      const float fv = sc->rescale;
-      const bool raise = m_new > m_ref + AT_RAISE;
-      const float alpha = raise ? (m_ref == -INFINITY ? 0.f : ex2_approx(m_ref - m_new)) : 1.f;
-      if (n > 0 && (fv != 1.f || __any_sync(0xffffffffu, raise))) {
-        const float f = alpha * fv;
+      const bool raise = m_tile > m_ref + AT_RAISE || y_tile - AT_P_LOG2 > top + AT_RAISE;
+      float f = 1.f;                               // what O has to be multiplied by
+      if (raise) {
+        const float m_new = fmaxf(m_ref, m_tile), y_new = fmaxf(top, y_tile - AT_P_LOG2);
+        K = fminf(fmaxf(floorf(y_new - m_new), E_MIN), E_MAX);
+        f = ex2_approx(top - (m_new + K));         // nothing seen yet: 0
+        l *= ex2_approx(m_ref - m_new);
+        m_ref = m_new;
+        top = m_new + K;
+        unit = two_to(static_cast<int>(K) - 7);
+      }
+      if (n > 0 && __any_sync(0xffffffffu, raise)) {
 #pragma unroll 1
         for (int c = 0; c < HD / 16; ++c) {
           uint32_t o[16];
@@ -521,17 +514,14 @@ __device__ void ch_softmax(int t, const AttendParams& p, ChWalk w, int per, uint
         }
         tmem_st_wait();
       }
-      if (raise) {
-        l *= alpha;
-        m_ref = m_new;
-      }
       const float neg_ref = (m_ref == -INFINITY) ? 0.f : -m_ref;
 #pragma unroll
       for (int hh = 0; hh < 4; ++hh) {             // 32 keys -> 16 packed columns
         uint32_t pk[16];
 #pragma unroll
         for (int g1 = 0; g1 < 2; ++g1) {
-          const float k1 = ch_factor(row_scale, sc->k[2 * hh + g1]), a1 = neg_ref + sc->add[2 * hh + g1];
+          const float k1 = ch_factor(row_scale, sc->k[2 * hh + g1]);
+          const float a1 = neg_ref + fmaxf(sc->up[2 * hh + g1] - K, AT_W_LEAST);
           const float2 k2 = make_float2(k1, k1), a2 = make_float2(a1, a1);
           float2 acc = make_float2(0.f, 0.f);
 #pragma unroll
@@ -544,11 +534,10 @@ __device__ void ch_softmax(int t, const AttendParams& p, ChWalk w, int per, uint
             acc = __fadd2_rn(acc, e);
             pk[8 * g1 + c] = pack_half2(e.x, e.y);
           }
-          l = fmaf(acc.x + acc.y, sc->fac[2 * hh + g1], l);
+          l = fmaf(acc.x + acc.y, fminf(unit * sc->inv[2 * hh + g1], AT_L_MOST), l);
         }
         tmem_st16(tS + 16 * hh, pk);
       }
-      if (tile + 1 == w.t1) unit = sc->unit;
       tmem_st_wait();
       tc_fence_before();
       mbar_arrive(bar(L::B_P_READY + t));
@@ -808,16 +797,16 @@ __global__ void __launch_bounds__(CHJ_WARPS * 32) chunk_join_kernel(const Attend
     float top = m;
 #pragma unroll
     for (int k = 0; k < LOT; ++k) top = fmaxf(top, ml[k].x);
-    const float old = m == top ? 1.f : ex2_approx(m - top);   // nothing yet: 0, or both -inf
+    const Scaled old(m == top ? 0.f : m - top);          // nothing yet: 0, or both -inf
     m = top;
-    z *= old;
-    a = make_float4(a.x * old, a.y * old, a.z * old, a.w * old);
+    z = old(z);
+    a = old(a);
 #pragma unroll
     for (int k = 0; k < LOT; ++k) {
       if (ml[k].y == 0.f) continue;                    // saw nothing, or no part
-      const float f = ml[k].x == m ? 1.f : ex2_approx(ml[k].x - m);
-      z += ml[k].y * f;
-      a = make_float4(fmaf(y[k].x, f, a.x), fmaf(y[k].y, f, a.y), fmaf(y[k].z, f, a.z), fmaf(y[k].w, f, a.w));
+      const Scaled f(ml[k].x == m ? 0.f : ml[k].x - m);
+      z += f(ml[k].y);
+      f.add(y[k], a);
     }
   }
   store_row<HD>(p, b, h, row0 + r, 4 * group, m, z, a);
