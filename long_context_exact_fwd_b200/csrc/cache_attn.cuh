@@ -142,13 +142,11 @@ __device__ __forceinline__ uint32_t value_offset(int t, int chunk) {
   return line * 128 + ((at ^ (((t >> 1) & 3) << 1)) << 4);
 }
 
-// Four columns of one finished row (row = t * g + head) from its reference m, sum z and product a.
+// Four columns of one finished row (row = t * g + head) from its reference m, sum z and average a.
 template <int HD>
 __device__ __forceinline__ void store_row(const AttendParams& p, int b, int h, int row, int d, float m, float z, float4 a) {
   const int tt = row / p.g, hq = h * p.g + row % p.g;
   const long long at = (static_cast<long long>(b) * p.c.heads * p.g + hq) * p.T + tt;
-  const float inv = z > 0.f ? 1.f / z : z;   // nothing seen: 0; NaN stays
-  a = make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
   if (p.o_f32)
     *reinterpret_cast<float4*>(static_cast<float*>(p.o) + at * HD + d) = a;
   else
@@ -157,19 +155,35 @@ __device__ __forceinline__ void store_row(const AttendParams& p, int b, int h, i
   if (d == 0) p.lse[at] = z == 0.f ? -INFINITY : (m + log2f(z)) * 0.69314718055994531f;
 }
 
-// Of parts that are joined: l and O of one whose reference lies d <= 0 above the common one, times 2^d.  In two
-// halves: a part of small weight and large values may be the result, and 2^d alone ends at 2^-126.
-struct Scaled {
-  float h;
-  __device__ __forceinline__ explicit Scaled(float d) : h(d == 0.f ? 1.f : ex2_approx(0.5f * d)) {}
-  __device__ __forceinline__ float operator()(float x) const { return x * h * h; }
-  __device__ __forceinline__ float4 operator()(const float4& x) const {
-    return make_float4((*this)(x.x), (*this)(x.y), (*this)(x.z), (*this)(x.w));
+// Joins N parts to the average a of reference m and weight z.  Part i: an average y[i] of the values (sums could pass
+// float's range where the values are near its end) with its reference and weight ml[i]; weight 0 has seen nothing.  A
+// part whose reference lies d <= 0 above the common one counts 2^d, applied in two halves: one of small weight and
+// large values may be the result, and 2^d alone ends at 2^-126.  FIRST: a is none yet.
+template <bool FIRST, int N>
+__device__ __forceinline__ void join_parts(const float2 (&ml)[N], const float4 (&y)[N], float& m, float& z, float4& a) {
+  float top = FIRST ? ml[0].x : m;
+#pragma unroll
+  for (int i = 0; i < N; ++i) top = fmaxf(top, ml[i].x);
+  auto half_of = [&](float ref) { return ref == top ? 1.f : ex2_approx(0.5f * (ref - top)); };   // nothing yet: weight 0
+  const float old = FIRST ? 0.f : half_of(m);
+  float half[N], sum = FIRST ? 0.f : z * old * old;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    half[i] = half_of(ml[i].x);
+    sum += ml[i].y * half[i] * half[i];
   }
-  __device__ __forceinline__ void add(const float4& x, float4& a) const {
-    a = make_float4(fmaf(x.x * h, h, a.x), fmaf(x.y * h, h, a.y), fmaf(x.z * h, h, a.z), fmaf(x.w * h, h, a.w));
+  m = top;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  const float w = old * (z * inv);
+  a = FIRST ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(a.x * old * w, a.y * old * w, a.z * old * w, a.w * old * w);
+  z = sum;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    if (ml[i].y == 0.f) continue;
+    const float h = half[i], x = h * (ml[i].y * inv);
+    a = make_float4(fmaf(y[i].x * h, x, a.x), fmaf(y[i].y * h, x, a.y), fmaf(y[i].z * h, x, a.z), fmaf(y[i].w * h, x, a.w));
   }
-};
+}
 
 template <int HD, int NT>
 __global__ void __launch_bounds__(AT_THREADS, at_per_sm(HD, NT)) attend_kernel(const AttendParams p) {
@@ -568,7 +582,7 @@ __global__ void __launch_bounds__(AT_THREADS, at_per_sm(HD, NT)) attend_kernel(c
       }
     }
 
-    // ---- join the warps: each leaves m, l and O (true units) where its ring was
+    // ---- join the warps: each leaves m, l and its average of the values where its ring was
     cp_async_wait<0>();
     __syncwarp();
     float* mine = reinterpret_cast<float*>(ring_ptr);   // [ROWS][HD]
@@ -581,7 +595,7 @@ __global__ void __launch_bounds__(AT_THREADS, at_per_sm(HD, NT)) attend_kernel(c
         z += __shfl_xor_sync(0xffffffffu, z, 8);
         z += __shfl_xor_sync(0xffffffffu, z, 16);
         const int r = j * 8 + 2 * gc + e;
-        const float u = e ? unit[j].y : unit[j].x;
+        const float u = e ? unit[j].y : unit[j].x, inv = 1.f / z;   // a warp that saw nothing is passed over
         if (gr == 0) {
           s_ml[(warp * 32 + r) * 2] = z == 0.f ? -INFINITY : -(e ? neg_ref[j].y : neg_ref[j].x);
           s_ml[(warp * 32 + r) * 2 + 1] = z;
@@ -589,7 +603,8 @@ __global__ void __launch_bounds__(AT_THREADS, at_per_sm(HD, NT)) attend_kernel(c
 #pragma unroll
         for (int k = 0; k < KS / 2; ++k)
           *reinterpret_cast<float4*>(mine + r * HD + gr * (HD / 8) + 4 * k) =
-              make_float4(o[2 * k][j][e] * u, o[2 * k][j][e + 2] * u, o[2 * k + 1][j][e] * u, o[2 * k + 1][j][e + 2] * u);
+              make_float4(o[2 * k][j][e] * inv * u, o[2 * k][j][e + 2] * inv * u, o[2 * k + 1][j][e] * inv * u,
+                          o[2 * k + 1][j][e + 2] * inv * u);
       }
     __syncthreads();
     const bool whole = t0 == 0 && t1 == nt;
@@ -599,19 +614,16 @@ __global__ void __launch_bounds__(AT_THREADS, at_per_sm(HD, NT)) attend_kernel(c
     for (int i = threadIdx.x; i < ROWS * GROUPS; i += AT_THREADS) {
       const int r = i / GROUPS, d = (i % GROUPS) * 4;
       if (r >= rows) continue;
-      float m = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < AT_WARPS; ++w) m = fmaxf(m, s_ml[(w * 32 + r) * 2]);
-      float z = 0.f;
-      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+      float m, z;
+      float4 a;
+      float2 ml[AT_WARPS];
+      float4 y[AT_WARPS];
 #pragma unroll
       for (int w = 0; w < AT_WARPS; ++w) {
-        const float mw = s_ml[(w * 32 + r) * 2], zw = s_ml[(w * 32 + r) * 2 + 1];
-        if (zw == 0.f) continue;              // saw nothing
-        const Scaled f(mw == m ? 0.f : mw - m);
-        z += f(zw);
-        f.add(*reinterpret_cast<const float4*>(smem + w * L::RING + (r * HD + d) * 4), a);
+        ml[w] = *reinterpret_cast<const float2*>(s_ml + (w * 32 + r) * 2);
+        y[w] = *reinterpret_cast<const float4*>(smem + w * L::RING + (r * HD + d) * 4);
       }
+      join_parts<true>(ml, y, m, z, a);
       if (unseen) {
         const int lim = limit_of(r);
         const float nan = __uint_as_float(0x7fffffffu);
@@ -681,38 +693,20 @@ __global__ void __launch_bounds__(LOT * WARPS * 32) join_kernel(const AttendPara
         if (lane < GROUPS) y[i] = *reinterpret_cast<const float4*>(part(k) + 4 * lane);
       }
     }
-    float top = m;
-#pragma unroll
-    for (int i = 0; i < AT_ONCE; ++i) top = fmaxf(top, ml[i].x);
-    const Scaled old(m == top ? 0.f : m - top);               // nothing yet: 0, or both -inf
-    m = top;
-    z = old(z);
-    a = old(a);
-#pragma unroll
-    for (int i = 0; i < AT_ONCE; ++i) {
-      if (ml[i].y == 0.f) continue;           // saw nothing, or no part
-      const Scaled f(ml[i].x == m ? 0.f : ml[i].x - m);
-      z += f(ml[i].y);
-      f.add(y[i], a);
-    }
+    join_parts<false>(ml, y, m, z, a);
   }
   if (lane < GROUPS) s_o[rr][w][lane] = a;
   if (lane == 0) s_ml[rr][w] = make_float2(m, z);
   __syncthreads();
   if (w || lane >= GROUPS || r >= rows) return;
-  m = -INFINITY;
-#pragma unroll
-  for (int i = 0; i < WARPS; ++i) m = fmaxf(m, s_ml[rr][i].x);
-  z = 0.f;
-  a = make_float4(0.f, 0.f, 0.f, 0.f);
+  float2 ml[WARPS];
+  float4 y[WARPS];
 #pragma unroll
   for (int i = 0; i < WARPS; ++i) {
-    const float2 ml = s_ml[rr][i];
-    if (ml.y == 0.f) continue;
-    const Scaled f(ml.x == m ? 0.f : ml.x - m);
-    z += f(ml.y);
-    f.add(s_o[rr][i][lane], a);
+    ml[i] = s_ml[rr][i];
+    y[i] = s_o[rr][i][lane];
   }
+  join_parts<true>(ml, y, m, z, a);
   store_row<HD>(p, b, h, row0 + r, 4 * lane, m, z, a);
 }
 

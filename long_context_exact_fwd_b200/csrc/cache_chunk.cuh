@@ -565,7 +565,6 @@ __device__ void ch_softmax(int t, const AttendParams& p, ChWalk w, int per, uint
     float4* part = reinterpret_cast<float4*>(p.part) +
                    static_cast<long long>(2 * blockIdx.x + (static_cast<int>(blockIdx.x) == c0 ? 1 : 0)) * CH_ROWS * (HD / 4 + 1) + r;
     const float inv = l > 0.f ? 1.f / l : l;     // nothing seen: 0; NaN stays
-    const float f = whole ? inv * unit : unit;
 #pragma unroll 1
     for (int c = 0; c < HD / 16; ++c) {
       uint32_t o[16];
@@ -573,7 +572,7 @@ __device__ void ch_softmax(int t, const AttendParams& p, ChWalk w, int per, uint
       tmem_ld_wait();
       float y[16];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) y[i] = l == 0.f ? 0.f : __uint_as_float(o[i]) * f;
+      for (int i = 0; i < 16; ++i) y[i] = l == 0.f ? 0.f : __uint_as_float(o[i]) * inv * unit;
       if (any_nan) {
 #pragma unroll
         for (int i = 0; i < 16; ++i)
@@ -794,20 +793,7 @@ __global__ void __launch_bounds__(CHJ_WARPS * 32) chunk_join_kernel(const Attend
         y[k] = at(k0 + k)[group * CH_ROWS];
       }
     }
-    float top = m;
-#pragma unroll
-    for (int k = 0; k < LOT; ++k) top = fmaxf(top, ml[k].x);
-    const Scaled old(m == top ? 0.f : m - top);          // nothing yet: 0, or both -inf
-    m = top;
-    z = old(z);
-    a = old(a);
-#pragma unroll
-    for (int k = 0; k < LOT; ++k) {
-      if (ml[k].y == 0.f) continue;                    // saw nothing, or no part
-      const Scaled f(ml[k].x == m ? 0.f : ml[k].x - m);
-      z += f(ml[k].y);
-      f.add(y[k], a);
-    }
+    join_parts<false>(ml, y, m, z, a);
   }
   store_row<HD>(p, b, h, row0 + r, 4 * group, m, z, a);
 }

@@ -123,3 +123,19 @@ def test_many_parts_of_pages_far_apart(ra):  # noqa: F811
         q = 0.1 * _randn((1, g, T, 128), 4)
         q[..., 0] = 8.0
         _attend(two, [0], [T], q.to(torch.bfloat16), float(np.log(2.0)) * 0.9)
+
+
+@pytest.mark.parametrize("g,T", FORMS)
+@pytest.mark.parametrize("size", [3.3e38, 1e37, 1e-36])
+def test_values_at_the_ends_of_the_range(ra, g, T, size):  # noqa: F811
+    """Averages of values near the type's largest stay finite, of tiny ones keep their bits; in one part and in
+    many."""
+    for n in (T + 3, 3000):
+        two = Both(ra, 200, 1, 16, 64, 1, 190)
+        k, v = 0.05 * _randn((1, 1, n, 64), 1), torch.rand((1, 1, n, 64), generator=torch.Generator().manual_seed(2)) * 0.5 + 0.5
+        v[..., 1::2] *= -1
+        assert two.reserve([0], [n])
+        two.append([0], [n], kv=(k.to(torch.bfloat16), (v * size).to(torch.bfloat16)))
+        two.check()
+        _attend(two, [0], [T], _randn((1, g, T, 64), 3), 0.125)
+        _attend(two, [0], [T], _randn((1, g, T, 64), 3), 0.125, out_dtype=torch.bfloat16)
