@@ -404,7 +404,8 @@ RA_API int ring_attn_cache_read(const ra_cache* cache, int layer, const int* slo
  *   scale     > 0 overrides 1 / sqrt(head_dim).
  *   o         [B][Hq][T][head_dim] bf16 or (o_dtype RA_F32) float32, and lse [B][Hq][T] float32, as
  *             ring_attn_fwd's (float32 o and lse are one part of ring_attn_merge).  Rows t >= n_new[b]
- *             are left as they were; a query that sees nothing has o = 0, lse = -inf.
+ *             are left as they were; a query that sees nothing has o = 0, lse = -inf.  Tokens on a page whose
+ *             number is out of range are not seen.
  *   workspace ring_attn_cache_attend_workspace_size bytes, 256-byte aligned, of this call alone while
  *             it runs; contents on entry do not matter.
  * o must not overlap q (RA_ERR_ARG).  exp(s - lse) times the value scale of the token's page is rounded to fp16

@@ -441,7 +441,8 @@ __global__ void __launch_bounds__(AT_THREADS, at_per_sm(HD, NT)) attend_kernel(c
       }
 
       // log2 units, mask, and the largest of each column
-      const bool masked = tok0 + AT_TILE > lim_min;
+      const bool none0 = sc.x == 0.f, none1 = sc.y == 0.f;   // a half without a page (or behind the end) has no scale
+      const bool masked = tok0 + AT_TILE > lim_min || none0 || none1;
       const int e0 = exponent_of(sc.z), e1 = exponent_of(sc.w);   // of the halves' value scales
       const float2 up0 = make_float2(e0, e0), up1 = make_float2(e1, e1);
       float top = -INFINITY;                  // over a reference
@@ -458,8 +459,9 @@ __global__ void __launch_bounds__(AT_THREADS, at_per_sm(HD, NT)) attend_kernel(c
         if (masked) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {       // tokens of the tile, from this thread's first, that are seen
-            if (limit[j][0] - tok0 - gr <= 8 * i) s[i >> 1][j][i & 1].x = -INFINITY;
-            if (limit[j][1] - tok0 - gr <= 8 * i) s[i >> 1][j][i & 1].y = -INFINITY;
+            const bool none = i >> 1 ? none1 : none0;
+            if (none || limit[j][0] - tok0 - gr <= 8 * i) s[i >> 1][j][i & 1].x = -INFINITY;
+            if (none || limit[j][1] - tok0 - gr <= 8 * i) s[i >> 1][j][i & 1].y = -INFINITY;
           }
         }
         const float2 m0 = make_float2(fmaxf(s[0][j][0].x, s[0][j][1].x), fmaxf(s[0][j][0].y, s[0][j][1].y));

@@ -35,11 +35,11 @@ constexpr int CH_MAX_CTAS = 160;      // blocks that the workspace has room for 
 constexpr int CH_START = 3;          // what starting and ending an item costs, in tiles
 constexpr int CH_LEAST = 4;          // tiles of a stretch, at least
 
-// Scale constants of one key tile: groups of 16 keys.
+// Scale constants of one key tile: lots of 16 keys.
 struct alignas(16) ChScales {
-  float k[8];        // key scale
-  float up[8];       // e + 7, 2^e the value scale
-  float inv[8];      // 2^-e
+  // key scale; e + 7, 2^e the value scale; 2^-e; the least of e + 7 - K.  A lot without a page has no weight and no
+  // part in the largest: NaN, -inf, any, -inf.
+  float4 lot[8];
   unsigned lots;     // of the tile's eight, those that have a page
 };
 
@@ -158,8 +158,8 @@ __device__ void ch_fetch(const AttendParams& p, ChWalk w, uint8_t* smem, uint32_
     const int* table = c.table + static_cast<long long>(w.slot()) * c.max_pages;
     int pid = ch_pages(p, table, len, w.t0);
     for (int tile = w.t0; tile < w.t1 && ok; ++tile) {
-      float sk = 1.f;                                    // no page: its codes will be 0
-      int e = E_MIN;
+      float sk = 0.f;
+      int e = 0;
       if (pid >= 0) {
         sk = c.k_scale[static_cast<long long>(pid) * c.heads + h];
         e = exponent_of(c.v_scale[static_cast<long long>(pid) * c.heads + h]);
@@ -175,11 +175,9 @@ __device__ void ch_fetch(const AttendParams& p, ChWalk w, uint8_t* smem, uint32_
         if (!ok) break;
         if (kv == 0) {                                   // before this tile's keys can be multiplied
           ChScales* s = scales + scale_slot;
-          if (lane < 8) {
-            s->k[lane] = sk;
-            s->up[lane] = static_cast<float>(e) + AT_P_LOG2;
-            s->inv[lane] = two_to(-e);
-          }
+          if (lane < 8)
+            s->lot[lane] = pid >= 0 ? make_float4(sk, static_cast<float>(e) + AT_P_LOG2, two_to(-e), AT_W_LEAST)
+                                    : make_float4(__int_as_float(0x7fffffff), -INFINITY, 0.f, -INFINITY);
           if (lane == 0) s->lots = lots;
           scale_slot = (scale_slot + 1) & 3;
           __syncwarp();
@@ -402,6 +400,12 @@ __device__ void ch_issue(ChWalk w, uint32_t sbase, uint32_t tmem, volatile int* 
 __device__ __forceinline__ float ch_factor(float row_scale, float key_scale) {
   return fmaxf(row_scale * key_scale, 1.17549435e-38f);
 }
+// The same, but NaN for a key scale of NaN.
+__device__ __forceinline__ float ch_factor_nan(float row_scale, float key_scale) {
+  float f;
+  asm("max.NaN.f32 %0, %1, 0f00800000;" : "=f"(f) : "f"(row_scale * key_scale));
+  return f;
+}
 
 // This thread's query row of the piece that `w` stands on, as fp16 at the row's own power of two, into its
 // place in shared memory; returns the factor from its scores to log2 units (before the key scale).
@@ -487,9 +491,10 @@ __device__ void ch_softmax(int t, const AttendParams& p, ChWalk w, int per, uint
           a = fmax3(a, __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
           b = fmax3(b, __uint_as_float(s[c + 2]), __uint_as_float(s[c + 3]));
         }
-        const float m = fmaxf(a, b) * ch_factor(row_scale, sc->k[g1]);
+        const float4 lot = sc->lot[g1];
+        const float m = fmaxf(a, b) * ch_factor_nan(row_scale, lot.x);
         m_tile = fmaxf(m_tile, m);
-        y_tile = fmaxf(y_tile, m + sc->up[g1]);
+        y_tile = fmaxf(y_tile, m + lot.y);
       }
       const bool raise = m_tile > m_ref + AT_RAISE || y_tile - AT_P_LOG2 > top + AT_RAISE;
       float f = 1.f;                               // what O has to be multiplied by
@@ -520,8 +525,9 @@ __device__ void ch_softmax(int t, const AttendParams& p, ChWalk w, int per, uint
         uint32_t pk[16];
 #pragma unroll
         for (int g1 = 0; g1 < 2; ++g1) {
-          const float k1 = ch_factor(row_scale, sc->k[2 * hh + g1]);
-          const float a1 = neg_ref + fmaxf(sc->up[2 * hh + g1] - K, AT_W_LEAST);
+          const float4 lot = sc->lot[2 * hh + g1];
+          const float k1 = ch_factor(row_scale, lot.x);
+          const float a1 = neg_ref + fmaxf(lot.y - K, lot.w);
           const float2 k2 = make_float2(k1, k1), a2 = make_float2(a1, a1);
           float2 acc = make_float2(0.f, 0.f);
 #pragma unroll
@@ -534,7 +540,7 @@ __device__ void ch_softmax(int t, const AttendParams& p, ChWalk w, int per, uint
             acc = __fadd2_rn(acc, e);
             pk[8 * g1 + c] = pack_half2(e.x, e.y);
           }
-          l = fmaf(acc.x + acc.y, fminf(unit * sc->inv[2 * hh + g1], AT_L_MOST), l);
+          l = fmaf(acc.x + acc.y, fminf(unit * lot.z, AT_L_MOST), l);
         }
         tmem_st16(tS + 16 * hh, pk);
       }

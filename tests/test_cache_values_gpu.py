@@ -139,3 +139,30 @@ def test_values_at_the_ends_of_the_range(ra, g, T, size):  # noqa: F811
         two.check()
         _attend(two, [0], [T], _randn((1, g, T, 64), 3), 0.125)
         _attend(two, [0], [T], _randn((1, g, T, 64), 3), 0.125, out_dtype=torch.bfloat16)
+
+
+# ------------------------------------------------------------------------------------ pages out of range
+@pytest.mark.parametrize("Dh,page", [(128, 16), (64, 32), (128, 128)])
+@pytest.mark.parametrize("g,T", FORMS)
+def test_tokens_on_a_bad_page_are_left_out(ra, Dh, page, g, T):  # noqa: F811
+    """A table entry out of range is reported, and its tokens have no weight, whatever the others' scores."""
+    two = Both(ra, 80, 1, page, Dh, 2, 30)
+    n = [max(9 * page, T) + 5, 2 * page]
+    k, v = _randn((2, 1, n[0], Dh), 1), _randn((2, 1, n[0], Dh), 2)
+    k[..., 0] = 2.0
+    assert two.reserve([0, 1], n)
+    two.append([0, 1], n, kv=(k, v))
+    seen = [np.ones(m, dtype=bool) for m in n]
+    for j, bad in ((2, 87), (3, -3), (6, 80)):
+        two.gpu.table[0, j] = bad
+        seen[0][j * page:(j + 1) * page] = False
+    for shift in (0.0, -2000.0):                             # scores around 0, and all far below it
+        q = _randn((1, g, T, Dh), 3)
+        q[..., 0] = shift
+        for causal in (True, False):
+            _attend(two, [0], [T], q, Dh ** -0.5, causal, seen, status=ra.RA_ERR_PAGES)
+    # nothing left to see
+    two.gpu.table[1, :] = 99
+    m = min(T, n[1])
+    q = _randn((1, g, m, Dh), 4)
+    _attend(two, [1], [m], q, Dh ** -0.5, True, [np.zeros(n[1], dtype=bool)], status=ra.RA_ERR_PAGES)
