@@ -390,7 +390,8 @@ RA_API int ring_attn_cache_append(const ra_cache* cache, int layer, const int* s
 /*
  * ring_attn_cache_read -- one layer's keys and values as bf16 (exact): positions start[b] ..
  * start[b] + length - 1 of slots[b] (start NULL: 0) into k, v [B][heads][length][head_dim], zero
- * at positions that the sequence does not hold.  One launch.
+ * at positions that the sequence does not hold (a length out of range holds none) and of tokens whose page
+ * number is out of range.  One launch.
  */
 RA_API int ring_attn_cache_read(const ra_cache* cache, int layer, const int* slots, const int* start, int B,
                                 int length, void* k, void* v, ra_stream stream);

@@ -207,7 +207,11 @@ __global__ void __launch_bounds__(IO_THREADS) read_kernel(const ReadParams p) {
     return;
   }
   const int start = p.start ? p.start[b] : 0;
-  const int len = static_cast<int>(min(static_cast<long long>(c.lens[slot]), c.max_pages * static_cast<long long>(c.page)));
+  int len = c.lens[slot];
+  if (len < 0 || len > c.max_pages * static_cast<long long>(c.page)) {   // holds nothing that could be read
+    if (blockIdx.x == 0 && threadIdx.x == 0) record_status(RA_ERR_PAGES);
+    len = 0;
+  }
   const int* row = c.table + static_cast<long long>(slot) * c.max_pages;
   const int page_shift = 31 - __clz(c.page);
   const uint8_t* codes = kv ? c.v : c.k;

@@ -166,3 +166,14 @@ def test_tokens_on_a_bad_page_are_left_out(ra, Dh, page, g, T):  # noqa: F811
     m = min(T, n[1])
     q = _randn((1, g, m, Dh), 4)
     _attend(two, [1], [m], q, Dh ** -0.5, True, [np.zeros(n[1], dtype=bool)], status=ra.RA_ERR_PAGES)
+
+
+def test_reading_a_bad_length_is_reported(ra):  # noqa: F811
+    two = Both(ra, 8, 1, 16, 64, 2, 3)
+    two.add([0], [20])
+    for bad in (-1, 3 * 16 + 1, 2 ** 31 - 1):
+        two.gpu.lens[1] = bad
+        k, v = ra.cache_read(two.gpu, 0, _i32([1, 0]), 24)
+        assert ra.device_status() == ra.RA_ERR_PAGES
+        np.testing.assert_array_equal(k[1, :, :20].double().cpu().numpy(), two.cpu[0].values("k", 0))
+        assert torch.all(v[1, :, 20:] == 0) and torch.all(k[0] == 0) and torch.all(v[0] == 0)
