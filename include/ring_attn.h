@@ -392,9 +392,13 @@ RA_API int ring_attn_cache_append(const ra_cache* cache, int layer, const int* s
  * start[b] + length - 1 of slots[b] (start NULL: 0) into k, v [B][heads][length][head_dim], zero
  * at positions that the sequence does not hold (a length out of range holds none) and of tokens whose page
  * number is out of range.  One launch.
+ * _ex: fill_k, fill_v != 0 zero the rows of entries that are padding or left out in k, v (for outputs that hold
+ * nothing yet); 0 leaves them as they were, as the plain call does.
  */
 RA_API int ring_attn_cache_read(const ra_cache* cache, int layer, const int* slots, const int* start, int B,
                                 int length, void* k, void* v, ra_stream stream);
+RA_API int ring_attn_cache_read_ex(const ra_cache* cache, int layer, const int* slots, const int* start, int B,
+                                   int length, void* k, void* v, int fill_k, int fill_v, ra_stream stream);
 
 /*
  * ring_attn_cache_attend -- attention of each sequence's last n_new[b] tokens over one layer.
@@ -413,12 +417,18 @@ RA_API int ring_attn_cache_read(const ra_cache* cache, int layer, const int* slo
  * before it multiplies the code of v: 11 bits where it is above 2^-21 of the largest that the query itself has, an
  * absolute 2^-32 of that below (tokens that it does not see have no part in this); sums are float32.  Calls with 64 rows and more per head (T * Hq / heads) run on tcgen05.  Two launches; a
  * bounded wait that gave up leaves RA_ERR_TIMEOUT in the device status word.
+ * _ex: fill_o, fill_lse != 0 write o = 0, lse = -inf to the rows that the plain call leaves as they were (t >= n_new[b],
+ * and entries that are padding or left out), for outputs that hold nothing yet.
  */
 RA_API size_t ring_attn_cache_attend_workspace_size(int T, int Hq, int Hkv, int Dh);
 RA_API int ring_attn_cache_attend(const ra_cache* cache, int layer, const int* slots, const int* n_new, int B, int T,
                                   int Hq, const void* q, const long long* q_strides, float scale, int causal, void* o,
                                   ra_dtype o_dtype, float* lse, void* workspace, size_t workspace_bytes,
                                   ra_stream stream);
+RA_API int ring_attn_cache_attend_ex(const ra_cache* cache, int layer, const int* slots, const int* n_new, int B, int T,
+                                     int Hq, const void* q, const long long* q_strides, float scale, int causal,
+                                     void* o, ra_dtype o_dtype, float* lse, int fill_o, int fill_lse, void* workspace,
+                                     size_t workspace_bytes, ra_stream stream);
 
 /*
  * ring_attn_cache_fork -- slots dst[b] (empty) become copies of src[b]: the same pages, one more

@@ -71,6 +71,7 @@ struct AttendParams {
   int by_segment;
   int B, T, g, n_blocks;       // row blocks per (sequence, head)
   int page_shift, causal, o_f32;
+  int fill_o, fill_lse;        // rows of padding get o = 0, lse = -inf; otherwise they are left alone
   float scale_log2;
 };
 
@@ -185,6 +186,27 @@ __device__ __forceinline__ void join_parts(const float2 (&ml)[N], const float4 (
   }
 }
 
+// Rows t >= n[b] (shared memory; 0 for an entry that is left out), 32 tokens of a query head at a time over the grid.
+template <int HD>
+__device__ __forceinline__ void fill_padding(const AttendParams& p, const int* n) {
+  constexpr int AT_ONCE = 32;
+  const int heads = p.c.heads * p.g, per_head = (p.T + AT_ONCE - 1) / AT_ONCE;
+  const long long units = static_cast<long long>(p.B) * heads * per_head;
+  for (long long u = blockIdx.x; u < units; u += gridDim.x) {
+    const long long i = u / per_head;                // query head of the whole batch
+    const int t = static_cast<int>(u - i * per_head) * AT_ONCE;
+    const int t0 = max(t, n[i / heads]), t1 = min(t + AT_ONCE, p.T);
+    const long long row = i * p.T + t0;
+    if (p.fill_lse)
+      for (int k = threadIdx.x; k < t1 - t0; k += blockDim.x) p.lse[row + k] = -INFINITY;
+    if (p.fill_o) {
+      const int size = p.o_f32 ? 4 : 2;
+      uint4* o = reinterpret_cast<uint4*>(static_cast<char*>(p.o) + row * HD * size);
+      for (int k = threadIdx.x; k < (t1 - t0) * HD * size / 16; k += blockDim.x) o[k] = make_uint4(0, 0, 0, 0);
+    }
+  }
+}
+
 template <int HD, int NT>
 __global__ void __launch_bounds__(AT_THREADS, at_per_sm(HD, NT)) attend_kernel(const AttendParams p) {
   using L = AttLayout<HD, NT>;
@@ -208,10 +230,12 @@ __global__ void __launch_bounds__(AT_THREADS, at_per_sm(HD, NT)) attend_kernel(c
   asm volatile("griddepcontrol.wait;" ::: "memory");   // what ran before on the stream is complete
   // ---- the line: for each (head, row block) of a sequence AT_START places, then its tiles
   int total = 0;
+  bool padding = false;                       // some entry has rows that are none
   for (int b0 = 0; b0 < p.B; b0 += AT_THREADS) {
     const int b = b0 + threadIdx.x;
     int w = 0;
     if (b < p.B) {
+      s_n[b] = 0;
       const int slot = p.slots[b];
       if (slot >= 0 && slot < c.slots) {
         const int len = c.lens[slot], n = p.n_new ? p.n_new[b] : p.T;
@@ -220,10 +244,11 @@ __global__ void __launch_bounds__(AT_THREADS, at_per_sm(HD, NT)) attend_kernel(c
         if (ok && n > 0) w = (max(1, (len + AT_TILE - 1) / AT_TILE) + AT_START) * c.heads * p.n_blocks;
         s_slot[b] = slot;
         s_len[b] = len;
-        s_n[b] = n;
+        if (ok) s_n[b] = n;
       } else if (slot != -1 && blockIdx.x == 0) {
         record_status(RA_ERR_PAGES);
       }
+      padding |= s_n[b] < p.T;
     }
     if (p.by_segment && blockIdx.x == 0 && b < p.B && w == 0)   // nobody comes by these
       for (int i = 0; i < c.heads * p.n_blocks; ++i) p.split[b * c.heads * p.n_blocks + i] = make_int4(-1, 0, 0, 0);
@@ -248,7 +273,7 @@ __global__ void __launch_bounds__(AT_THREADS, at_per_sm(HD, NT)) attend_kernel(c
   }
   if (threadIdx.x == 0) s_prefix[p.B] = total;
   for (int i = threadIdx.x; i < HD; i += AT_THREADS) s_nan[i] = INT_MAX;
-  __syncthreads();
+  if (__syncthreads_or(padding && (p.fill_o || p.fill_lse))) fill_padding<HD>(p, s_n);
   const int per = max((total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x), AT_LEAST);
   const int line0 = min(static_cast<long long>(total), static_cast<long long>(blockIdx.x) * per);
   const int line1 = min(total, line0 + per);

@@ -730,8 +730,11 @@ __global__ void __launch_bounds__(CH_THREADS, 1) chunk_kernel(const AttendParams
       s_start[3] = prefix[b] + h * per_head + done + CH_START;
     }
   }
+  bool padding = false;
+  if (p.fill_o || p.fill_lse)
+    for (int b = threadIdx.x; b < p.B; b += CH_THREADS) padding |= s_n[b] < p.T;
   tc_fence_before();
-  __syncthreads();
+  if (__syncthreads_or(padding)) fill_padding<HD>(p, s_n);
   tc_fence_after();
   asm volatile("griddepcontrol.launch_dependents;");   // the join can be set up, and wait
   const uint32_t tmem = *tmem_holder;

@@ -192,6 +192,11 @@ int ring_attn_cache_append(const ra_cache* cache, int layer, const int* slots, c
 
 int ring_attn_cache_read(const ra_cache* cache, int layer, const int* slots, const int* start, int B, int length,
                          void* k, void* v, ra_stream stream) {
+  return ring_attn_cache_read_ex(cache, layer, slots, start, B, length, k, v, 0, 0, stream);
+}
+
+int ring_attn_cache_read_ex(const ra_cache* cache, int layer, const int* slots, const int* start, int B, int length,
+                            void* k, void* v, int fill_k, int fill_v, ra_stream stream) {
   rc::ReadParams p{};
   if (layer < 0 || length <= 0 || !k || !v || k == v) return RA_ERR_ARG;
   int st = cache_pool(cache, layer, &p.c);
@@ -205,6 +210,8 @@ int ring_attn_cache_read(const ra_cache* cache, int layer, const int* slots, con
   p.k = static_cast<__nv_bfloat16*>(k);
   p.v = static_cast<__nv_bfloat16*>(v);
   p.length = length;
+  p.fill_k = fill_k != 0;
+  p.fill_v = fill_v != 0;
   const int per_block = rc::READ_UNITS * rc::IO_THREADS * rc::UNIT / p.c.Dh;   // tokens
   const dim3 grid((length + static_cast<long long>(per_block) - 1) / per_block, p.c.heads, 2 * B);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -220,6 +227,14 @@ size_t ring_attn_cache_attend_workspace_size(int T, int Hq, int Hkv, int Dh) {
 int ring_attn_cache_attend(const ra_cache* cache, int layer, const int* slots, const int* n_new, int B, int T, int Hq,
                            const void* q, const long long* q_strides, float scale, int causal, void* o,
                            ra_dtype o_dtype, float* lse, void* workspace, size_t workspace_bytes, ra_stream stream) {
+  return ring_attn_cache_attend_ex(cache, layer, slots, n_new, B, T, Hq, q, q_strides, scale, causal, o, o_dtype, lse, 0, 0,
+                                   workspace, workspace_bytes, stream);
+}
+
+int ring_attn_cache_attend_ex(const ra_cache* cache, int layer, const int* slots, const int* n_new, int B, int T, int Hq,
+                              const void* q, const long long* q_strides, float scale, int causal, void* o,
+                              ra_dtype o_dtype, float* lse, int fill_o, int fill_lse, void* workspace,
+                              size_t workspace_bytes, ra_stream stream) {
   rc::AttendParams p{};
   if (layer < 0 || T <= 0 || Hq <= 0 || !o || !lse) return RA_ERR_ARG;
   if (o_dtype != RA_BF16 && o_dtype != RA_F32) return RA_ERR_ARG;
@@ -256,6 +271,8 @@ int ring_attn_cache_attend(const ra_cache* cache, int layer, const int* slots, c
   p.n_new = n_new;
   p.o = o;
   p.lse = lse;
+  p.fill_o = fill_o != 0;
+  p.fill_lse = fill_lse != 0;
   p.part = static_cast<float*>(workspace);
   p.split = reinterpret_cast<int4*>(static_cast<char*>(workspace) + attend_part_bytes(nt, p.c.Dh));
   p.B = B;

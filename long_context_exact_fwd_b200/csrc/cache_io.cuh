@@ -188,6 +188,7 @@ struct ReadParams {
   Pool c;                      // one layer
   const int *slots, *start;    // start null: 0
   __nv_bfloat16 *k, *v;        // [B][heads][length][Dh]
+  int fill_k, fill_v;          // rows of padding are zeroed; otherwise left alone
   int length;
 };
 
@@ -201,18 +202,18 @@ __global__ void __launch_bounds__(IO_THREADS) read_kernel(const ReadParams p) {
   const Pool& c = p.c;
   const int b = blockIdx.z >> 1, kv = blockIdx.z & 1, h = blockIdx.y;
   const int slot = p.slots[b];
-  if (slot == -1) return;
-  if (slot < 0 || slot >= c.slots) {
-    if (blockIdx.x == 0 && threadIdx.x == 0) record_status(RA_ERR_PAGES);
-    return;
+  const bool held = slot >= 0 && slot < c.slots;
+  if (!held) {
+    if (slot != -1 && blockIdx.x == 0 && threadIdx.x == 0) record_status(RA_ERR_PAGES);
+    if (!(kv ? p.fill_v : p.fill_k)) return;
   }
-  const int start = p.start ? p.start[b] : 0;
-  int len = c.lens[slot];
+  const int start = p.start && held ? p.start[b] : 0;
+  int len = held ? c.lens[slot] : 0;
   if (len < 0 || len > c.max_pages * static_cast<long long>(c.page)) {   // holds nothing that could be read
     if (blockIdx.x == 0 && threadIdx.x == 0) record_status(RA_ERR_PAGES);
     len = 0;
   }
-  const int* row = c.table + static_cast<long long>(slot) * c.max_pages;
+  const int* row = c.table + static_cast<long long>(held ? slot : 0) * c.max_pages;
   const int page_shift = 31 - __clz(c.page);
   const uint8_t* codes = kv ? c.v : c.k;
   const float* scales = kv ? c.v_scale : c.k_scale;

@@ -77,9 +77,12 @@ _cache_pages_ws = _sig("ring_attn_cache_pages_workspace_size", _sz, _i, _i)
 _cache_reserve = _sig("ring_attn_cache_reserve", _i, _cp, _vp, _vp, _i, _vp, _sz, _vp)
 _cache_append = _sig("ring_attn_cache_append", _i, _cp, _i, _vp, _vp, _i, _i, _vp, _llp, _vp, _llp, _vp)
 _cache_read = _sig("ring_attn_cache_read", _i, _cp, _i, _vp, _vp, _i, _i, _vp, _vp, _vp)
+_cache_read_ex = _sig("ring_attn_cache_read_ex", _i, _cp, _i, _vp, _vp, _i, _i, _vp, _vp, _i, _i, _vp)
 _cache_attend_ws = _sig("ring_attn_cache_attend_workspace_size", _sz, _i, _i, _i, _i)
 _cache_attend = _sig("ring_attn_cache_attend", _i, _cp, _i, _vp, _vp, _i, _i, _i, _vp, _llp, _f, _i, _vp, _i, _vp, _vp,
                      _sz, _vp)
+_cache_attend_ex = _sig("ring_attn_cache_attend_ex", _i, _cp, _i, _vp, _vp, _i, _i, _i, _vp, _llp, _f, _i, _vp, _i, _vp, _i,
+                        _i, _vp, _sz, _vp)
 _cache_fork = _sig("ring_attn_cache_fork", _i, _cp, _vp, _vp, _i, _vp, _sz, _vp)
 _cache_trim = _sig("ring_attn_cache_trim", _i, _cp, _vp, _vp, _i, _vp)
 _cache_compact = _sig("ring_attn_cache_compact", _i, _cp, _vp, _sz, _vp)
@@ -608,19 +611,21 @@ def cache_read(cache: KVCache, layer: int, slots: torch.Tensor, length: int, sta
                k: Optional[torch.Tensor] = None, v: Optional[torch.Tensor] = None,
                stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """One layer's keys and values, exact in bf16, [B, heads, length, Dh]: positions start[b] (None: 0) ..
-    of slots[b], zero where the sequence holds none (ring_attn_cache_read)."""
+    of slots[b], zero where the sequence holds none (ring_attn_cache_read_ex).  Rows of padding (slot -1) and of
+    entries that are left out are zero in a fresh output and stay as they were in a given k or v."""
     dev, B = cache._at(), slots.shape[0]
     s = _batch(slots, "slots", dev, B)
     at = None if start is None else _batch(start, "start", dev, B)
     shape = (B, cache._c.heads, length, cache._c.head_dim)
-    if k is None:
+    fill_k, fill_v = k is None, v is None
+    if fill_k:
         k = _new(cache.k, shape, torch.bfloat16, stream)
-    if v is None:
+    if fill_v:
         v = _new(cache.k, shape, torch.bfloat16, stream)
     _need_dense(k, "k", dev, torch.bfloat16, shape)
     _need_dense(v, "v", dev, torch.bfloat16, shape)
-    _check(_cache_read(cache._ref, layer, s, at, B, length, k.data_ptr(), v.data_ptr(), _raw_stream(stream, dev)),
-           "ring_attn_cache_read")
+    _check(_cache_read_ex(cache._ref, layer, s, at, B, length, k.data_ptr(), v.data_ptr(), fill_k, fill_v,
+                          _raw_stream(stream, dev)), "ring_attn_cache_read_ex")
     return k, v
 
 
@@ -629,9 +634,10 @@ def cache_attend(cache: KVCache, layer: int, slots: torch.Tensor, n_new: Optiona
                  workspace: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
                  lse: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """Attention of each sequence's last n_new[b] tokens (None: T) over one layer of the cache
-    (ring_attn_cache_attend): q [B, Hq, T, Dh] bf16, views with a contiguous last dimension included, Hq a
+    (ring_attn_cache_attend_ex): q [B, Hq, T, Dh] bf16, views with a contiguous last dimension included, Hq a
     multiple of the cache's heads.  Returns (o [B, Hq, T, Dh] bf16 or float32, lse [B, Hq, T] float32) as
-    fwd() does; a float32 o is one part for merge()."""
+    fwd() does; a float32 o is one part for merge().  Rows t >= n_new[b], of padding (slot -1) and of entries that
+    are left out are 0 and -inf in fresh outputs and stay as they were in a given out or lse."""
     dev = cache._at()
     q_st = _need_rows(q, "q", dev, torch.bfloat16)
     B, Hq, T, Dh = q.shape
@@ -643,18 +649,19 @@ def cache_attend(cache: KVCache, layer: int, slots: torch.Tensor, n_new: Optiona
     s = _batch(slots, "slots", dev, B)
     n = None if n_new is None else _batch(n_new, "n_new", dev, B)
     ws, size = _workspace(workspace, cache_attend_workspace_bytes(T, Hq, heads, Dh), q, dev, stream)
-    if out is None:
+    fill_o, fill_lse = out is None, lse is None
+    if fill_o:
         out = _new(q, (B, Hq, T, Dh), out_dtype, stream)
     else:
         _need_dense(out, "out", dev, out_dtype, (B, Hq, T, Dh))
-    if lse is None:
+    if fill_lse:
         lse = _new(q, (B, Hq, T), torch.float32, stream)
     else:
         _need_dense(lse, "lse", dev, torch.float32, (B, Hq, T))
-    code = _cache_attend(cache._ref, layer, s, n, B, T, Hq, q.data_ptr(), _strides(*q_st), float(scale) if scale else 0.0,
+    code = _cache_attend_ex(cache._ref, layer, s, n, B, T, Hq, q.data_ptr(), _strides(*q_st), float(scale) if scale else 0.0,
                          bool(causal), out.data_ptr(), RA_BF16 if out_dtype == torch.bfloat16 else RA_F32,
-                         lse.data_ptr(), ws.data_ptr(), size, _raw_stream(stream, dev))
-    _check(code, "ring_attn_cache_attend")
+                         lse.data_ptr(), fill_o, fill_lse, ws.data_ptr(), size, _raw_stream(stream, dev))
+    _check(code, "ring_attn_cache_attend_ex")
     return out, lse
 
 
