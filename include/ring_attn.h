@@ -17,7 +17,8 @@
  *   Pointers   device pointers (cudaMalloc / torch CUDA memory) unless stated; tensors
  *              read by TMA (q, k, v and the backward inputs) must be 16-byte aligned.
  *              The caller owns every buffer; the library never allocates or frees device
- *              memory and never synchronises, except ring_attn_device_status.
+ *              memory and never synchronises, except ring_attn_device_status and
+ *              ring_attn_kernel_status.
  *   Stream     `stream` is a cudaStream_t (NULL = legacy default stream); all work is
  *              enqueued on it.  Calls return as soon as the work is enqueued.
  *   Mask       causal != 0 selects the autoregressive mask on global positions: key j is
@@ -486,11 +487,14 @@ RA_API int ring_attn_bwd_visit_tiles(int S, int D, int causal, int k0, int tile_
 RA_API unsigned long long ring_attn_launch_count(void);
 
 /*
- * ring_attn_device_status -- synchronises `stream`, returns the device status word
- * (RA_OK, or the first RA_ERR_TIMEOUT or RA_ERR_PAGES that a kernel recorded) and clears it.  Returns
- * RA_ERR_CUDA if the synchronisation itself fails.
+ * ring_attn_device_status -- synchronises `stream`, returns what kernels recorded in the device status words
+ * and clears what it returns: RA_ERR_TIMEOUT if a wait gave up; if none did, RA_ERR_PAGES if a cache call left an
+ * entry out; else RA_OK.  After RA_ERR_TIMEOUT the next call returns RA_ERR_PAGES if that was recorded too.
+ * Returns RA_ERR_CUDA if the synchronisation itself fails.
+ * ring_attn_kernel_status -- the same, of RA_ERR_TIMEOUT alone: it leaves RA_ERR_PAGES to the cache's caller.
  */
 RA_API int ring_attn_device_status(ra_stream stream);
+RA_API int ring_attn_kernel_status(ra_stream stream);
 
 /*
  * ring_attn_last_cuda_error -- diagnostics for RA_ERR_CUDA: the cudaError_t / CUresult value

@@ -10,7 +10,8 @@
 //
 // Slots, lengths, tables and page numbers live in device memory, where the host cannot check them:
 // every kernel checks what it reads from them before it goes by it, leaves out what is out of
-// range and records RA_ERR_PAGES in the device status word.
+// range and records RA_ERR_PAGES in a status word of the cache's own (a kernel's RA_ERR_TIMEOUT, in g_status, means
+// that a result is incomplete, and neither may hide the other).
 #pragma once
 #include <cstdint>
 #include <cuda_bf16.h>
@@ -29,6 +30,9 @@ struct Pool {                 // one layer's view, or all layers' (page operator
   int *table, *lens, *refs;   // [slots][max_pages], [slots], [pages]
   int layers, pages, heads, page, Dh, slots, max_pages;
 };
+
+__device__ int g_pages;       // 0, or RA_ERR_PAGES; ring_attn_device_status reads and clears it
+__device__ __forceinline__ void record_pages() { atomicExch(&g_pages, RA_ERR_PAGES); }
 
 // 2^e for e in [-126, 127].
 __device__ __forceinline__ float two_to(int e) { return __int_as_float((e + 127) << 23); }

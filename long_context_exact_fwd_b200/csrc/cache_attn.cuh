@@ -240,13 +240,13 @@ __global__ void __launch_bounds__(AT_THREADS, at_per_sm(HD, NT)) attend_kernel(c
       if (slot >= 0 && slot < c.slots) {
         const int len = c.lens[slot], n = p.n_new ? p.n_new[b] : p.T;
         const bool ok = n >= 0 && n <= p.T && len >= 0 && len <= c.max_pages * static_cast<long long>(c.page);
-        if (!ok && blockIdx.x == 0) record_status(RA_ERR_PAGES);
+        if (!ok && blockIdx.x == 0) record_pages();
         if (ok && n > 0) w = (max(1, (len + AT_TILE - 1) / AT_TILE) + AT_START) * c.heads * p.n_blocks;
         s_slot[b] = slot;
         s_len[b] = len;
         if (ok) s_n[b] = n;
       } else if (slot != -1 && blockIdx.x == 0) {
-        record_status(RA_ERR_PAGES);
+        record_pages();
       }
       padding |= s_n[b] < p.T;
     }
@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(AT_THREADS, at_per_sm(HD, NT)) attend_kernel(c
       if (tok >= len) return -1;
       const int pid = table[tok >> p.page_shift];
       if (pid < 0 || pid >= c.pages) {
-        record_status(RA_ERR_PAGES);
+        record_pages();
         return -1;
       }
       return pid;

@@ -135,7 +135,7 @@ __device__ __forceinline__ int ch_pages(const AttendParams& p, const int* table,
   if (tok >= len) return -1;
   const int pid = table[tok >> p.page_shift];
   if (pid >= 0 && pid < p.c.pages) return pid;
-  record_status(RA_ERR_PAGES);
+  record_pages();
   return -1;
 }
 
@@ -659,11 +659,11 @@ __global__ void __launch_bounds__(CH_THREADS, 1) chunk_kernel(const AttendParams
       len = c.lens[slot];
       n = p.n_new ? p.n_new[b] : p.T;
       if (n < 0 || n > p.T || len < 0 || len > c.max_pages * static_cast<long long>(c.page)) {
-        if (blockIdx.x == 0 && lane == 0) record_status(RA_ERR_PAGES);
+        if (blockIdx.x == 0 && lane == 0) record_pages();
         n = 0;
       }
     } else if (slot != -1 && blockIdx.x == 0 && lane == 0) {
-      record_status(RA_ERR_PAGES);
+      record_pages();
     }
     const int items = (n * p.g + CH_ROWS - 1) / CH_ROWS;
     int sum = 0;

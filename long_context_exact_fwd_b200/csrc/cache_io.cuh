@@ -78,14 +78,14 @@ __global__ void __launch_bounds__(AP_THREADS) append_kernel(const AppendParams p
   if (slot == -1) return;                         // a row of padding
   const bool reports = blockIdx.x == 0 && threadIdx.x == 0;
   if (slot < 0 || slot >= c.slots) {
-    if (reports) record_status(RA_ERR_PAGES);
+    if (reports) record_pages();
     return;
   }
   const int n = p.n_new ? p.n_new[b] : p.T;
   const int len = c.lens[slot];
   const int p0 = len - n;                         // first new position
   if (n < 0 || n > p.T || p0 < 0 || len > c.max_pages * static_cast<long long>(c.page)) {
-    if (reports) record_status(RA_ERR_PAGES);
+    if (reports) record_pages();
     return;
   }
   const int page_shift = 31 - __clz(c.page);
@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(AP_THREADS) append_kernel(const AppendParams p
   bool bad = pid < 0 || pid >= c.pages;
   if (!bad) bad = c.refs[pid] != 1;               // a page that others hold too is not written
   if (bad) {
-    if (threadIdx.x == 0) record_status(RA_ERR_PAGES);
+    if (threadIdx.x == 0) record_pages();
     return;
   }
   const __nv_bfloat16* src = (kv ? p.v : p.k) + b * (kv ? p.vb : p.kb) + h * (kv ? p.vh : p.kh);
@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(AP_THREADS) append_kernel(const AppendParams p
   const unsigned wmax = __reduce_max_sync(0xffffffffu, amax & 0xffffu) | flag;
   if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = wmax;
   if (named_before(p.slots, b, slot)) {           // barrier: s_max and every read of the old scale
-    if (reports) record_status(RA_ERR_PAGES);
+    if (reports) record_pages();
     return;
   }
   unsigned m = 0, odd = 0;
@@ -204,13 +204,13 @@ __global__ void __launch_bounds__(IO_THREADS) read_kernel(const ReadParams p) {
   const int slot = p.slots[b];
   const bool held = slot >= 0 && slot < c.slots;
   if (!held) {
-    if (slot != -1 && blockIdx.x == 0 && threadIdx.x == 0) record_status(RA_ERR_PAGES);
+    if (slot != -1 && blockIdx.x == 0 && threadIdx.x == 0) record_pages();
     if (!(kv ? p.fill_v : p.fill_k)) return;
   }
   const int start = p.start && held ? p.start[b] : 0;
   int len = held ? c.lens[slot] : 0;
   if (len < 0 || len > c.max_pages * static_cast<long long>(c.page)) {   // holds nothing that could be read
-    if (blockIdx.x == 0 && threadIdx.x == 0) record_status(RA_ERR_PAGES);
+    if (blockIdx.x == 0 && threadIdx.x == 0) record_pages();
     len = 0;
   }
   const int* row = c.table + static_cast<long long>(held ? slot : 0) * c.max_pages;
@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(IO_THREADS) read_kernel(const ReadParams p) {
     if (t < p.length && pos >= 0 && pos < len) {
       const int pid = row[pos >> page_shift];
       if (pid < 0 || pid >= c.pages) {
-        record_status(RA_ERR_PAGES);
+        record_pages();
       } else {
         const long long ph = static_cast<long long>(pid) * c.heads + h;
         w[i] = *reinterpret_cast<const uint2*>(codes + (((ph << page_shift) + (pos & (c.page - 1))) * HD + col));

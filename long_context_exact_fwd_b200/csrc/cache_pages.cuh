@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(PLAN_THREADS)
       }
     }
   }
-  if (bad) record_status(RA_ERR_PAGES);
+  if (bad) record_pages();
   s_last[b] = last;
   __syncthreads();
   // Entries that share a partly filled last page copy it, in batch order, until one holder is left.
@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(PLAN_THREADS)
   const int found = list_pages(c.refs, 0, c.pages, true, total, free_list, warp_sum);
   if (found < total) {
     if (threadIdx.x == 0) {
-      record_status(RA_ERR_PAGES);
+      record_pages();
       plan->pairs = 0;
     }
     return;
@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(PLAN_THREADS)
       len = c.lens[s];
       ok = c.lens[d] == 0 && len >= 0 && len <= c.max_pages * static_cast<long long>(c.page);
     }
-    if (!ok) record_status(RA_ERR_PAGES);
+    if (!ok) record_pages();
     active = ok;
   }
   const int n = active ? (len + c.page - 1) / c.page : 0;
@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(COPY_THREADS)
     const int col = i - first[r];
     const int pid = c.table[static_cast<long long>(src[r]) * c.max_pages + col];
     if (pid < 0 || pid >= c.pages) {
-      record_status(RA_ERR_PAGES);
+      record_pages();
       continue;
     }
     c.table[static_cast<long long>(dst[r]) * c.max_pages + col] = pid;
@@ -209,12 +209,12 @@ __global__ void __launch_bounds__(COPY_THREADS) trim_kernel(Pool c, const int* s
   if (slot == -1) return;
   const bool dup = named_before(slots, b, slot);
   if (slot < 0 || slot >= c.slots || dup) {
-    if (threadIdx.x == 0) record_status(RA_ERR_PAGES);
+    if (threadIdx.x == 0) record_pages();
     return;
   }
   const int len = c.lens[slot], kept = keep ? keep[b] : 0;
   if (len < 0 || kept < 0 || len > c.max_pages * static_cast<long long>(c.page)) {
-    if (threadIdx.x == 0) record_status(RA_ERR_PAGES);
+    if (threadIdx.x == 0) record_pages();
     return;
   }
   if (kept >= len) return;
@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(COPY_THREADS) trim_kernel(Pool c, const int* s
   for (int j = stay + threadIdx.x; j < have; j += COPY_THREADS) {
     const int pid = row[j];
     row[j] = -1;
-    if (pid < 0 || pid >= c.pages || atomicSub(c.refs + pid, 1) <= 0) record_status(RA_ERR_PAGES);
+    if (pid < 0 || pid >= c.pages || atomicSub(c.refs + pid, 1) <= 0) record_pages();
   }
   if (threadIdx.x == 0) c.lens[slot] = kept;
 }

@@ -16,6 +16,7 @@
 #include "fwd_f32.cuh"
 #include "merge.cuh"
 #include "bwd_sm100.cuh"
+#include "cache.cuh"
 #include "ffn_sm100.cuh"
 
 namespace {
@@ -95,6 +96,18 @@ DevInfo* dev_info(int* status) {
   }
   *status = RA_OK;
   return &g_dev[dev];
+}
+
+// Waits for the stream, then reads a device status word and clears it.
+int take_status(const int& word, ra_stream stream) {
+  if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return RA_ERR_CUDA;
+  int v = 0;
+  if (cudaMemcpyFromSymbol(&v, word, sizeof(int)) != cudaSuccess) return RA_ERR_CUDA;
+  if (v != 0) {
+    const int z = 0;
+    if (cudaMemcpyToSymbol(word, &z, sizeof(int)) != cudaSuccess) return RA_ERR_CUDA;
+  }
+  return v;
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -520,15 +533,11 @@ int ring_attn_visit_tiles(int S, int D, int causal, int q0, int tile_rows, int* 
   return n;
 }
 
+int ring_attn_kernel_status(ra_stream stream) { return take_status(ra::g_status, stream); }
+
 int ring_attn_device_status(ra_stream stream) {
-  if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return RA_ERR_CUDA;
-  int v = 0;
-  if (cudaMemcpyFromSymbol(&v, ra::g_status, sizeof(int)) != cudaSuccess) return RA_ERR_CUDA;
-  if (v != 0) {
-    const int z = 0;
-    if (cudaMemcpyToSymbol(ra::g_status, &z, sizeof(int)) != cudaSuccess) return RA_ERR_CUDA;
-  }
-  return v;
+  const int v = take_status(ra::g_status, stream);
+  return v != RA_OK ? v : take_status(ra::cache::g_pages, stream);
 }
 
 }  // extern "C"

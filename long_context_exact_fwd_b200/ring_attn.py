@@ -50,6 +50,7 @@ _merge_ex = _sig("ring_attn_merge_ex", _i, _vp, _vp, _i, _vp, _vp, _i, _i, _i, _
 _ring_order = _sig("ring_attn_ring_order", _i, _i, _i, _i, _ip, _i)
 _visit_tiles = _sig("ring_attn_visit_tiles", _i, _i, _i, _i, _i, _i, _ip, _i)
 _device_status = _sig("ring_attn_device_status", _i, _vp)
+_kernel_status = _sig("ring_attn_kernel_status", _i, _vp)
 _strerror = _sig("ring_attn_strerror", ctypes.c_char_p, _i)
 _version = _sig("ring_attn_version", _i)
 _last_cuda = _sig("ring_attn_last_cuda_error", _i, ctypes.POINTER(ctypes.c_char_p))
@@ -767,8 +768,14 @@ def launch_count() -> int:
 
 
 def device_status(stream=None) -> int:
-    """Synchronise the stream and return (and clear) the library's device status word."""
+    """Synchronise the stream and return (and clear) what kernels recorded: RA_ERR_TIMEOUT if a wait gave up,
+    otherwise RA_ERR_PAGES if a cache call left an entry out, otherwise 0."""
     return int(_device_status(_stream(stream)))
+
+
+def kernel_status(stream=None) -> int:
+    """device_status() of RA_ERR_TIMEOUT alone; RA_ERR_PAGES is left for the cache's caller."""
+    return int(_kernel_status(_stream(stream)))
 
 
 # raw entry points (for tests of the C ABI itself)

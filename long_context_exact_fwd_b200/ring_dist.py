@@ -118,9 +118,10 @@ def _cuda_merge_f32(o_parts, lse_parts):
 
 def _raise_on_device_status():
     """After a ring call on the CUDA library: synchronise and raise if a kernel gave up on a
-    bounded wait (its result would be incomplete).  One synchronisation per ring call."""
+    bounded wait (its result would be incomplete).  One synchronisation per ring call.  What a cache call
+    recorded is its caller's to read."""
     from . import ring_attn as ra
-    code = ra.device_status()
+    code = ra.kernel_status()
     if code != ra.RA_OK:
         raise ra.RingAttnError(code, "ring kernel")
 

@@ -68,3 +68,34 @@ def test_fresh_reads_hold_zero_in_rows_of_padding(ra):  # noqa: F811
     _, v = ra.cache_read(two.gpu, 0, _i32([-1, 2, 9, -1]), 60, k=given)
     assert ra.device_status() == ra.RA_ERR_PAGES
     assert torch.all(given[0] == 7.0) and torch.all(given[2:] == 7.0) and torch.all(v[0] == 0) and torch.all(v[2:] == 0)
+
+
+# ------------------------------------------------------------------------------------ two kinds of error
+@pytest.mark.parametrize("cache_first", [True, False])
+def test_an_entry_out_of_range_does_not_hide_a_timeout(ra, cache_first):  # noqa: F811
+    two = Both(ra, 8, 1, 16, 64, 2, 3)
+
+    def bad_slot():
+        ra.cache_trim(two.gpu, _i32([9]))
+
+    for call in ([bad_slot, lambda: ra.wait_selftest(0.02)] if cache_first else [lambda: ra.wait_selftest(0.02), bad_slot]):
+        call()
+    assert ra.device_status() == ra.RA_ERR_TIMEOUT
+    assert ra.device_status() == ra.RA_ERR_PAGES
+    assert ra.device_status() == 0
+
+
+def test_a_ring_does_not_raise_for_a_cache_entry(ra):  # noqa: F811
+    from long_context_exact_fwd_b200 import ring_dist as rd
+    two = Both(ra, 8, 1, 16, 64, 2, 3)
+    q, k, v = (_randn((1, 2, 128, 64), i).cuda() for i in (1, 2, 3))
+    ra.cache_trim(two.gpu, _i32([9]))
+    o, lse = rd.ring_fwd(q, k, v, True)
+    assert torch.isfinite(lse).all()
+    assert ra.device_status() == ra.RA_ERR_PAGES             # still there for the cache's caller
+    ra.wait_selftest(0.02)
+    ra.cache_trim(two.gpu, _i32([9]))
+    with pytest.raises(ra.RingAttnError) as e:
+        rd.ring_fwd(q, k, v, True)
+    assert e.value.code == ra.RA_ERR_TIMEOUT
+    assert ra.device_status() == ra.RA_ERR_PAGES and ra.device_status() == 0
