@@ -369,13 +369,19 @@ RA_API size_t ring_attn_cache_pages_workspace_size(int B, int pages);
  * batch order before the entry's new pages.  All or nothing: with too few free pages the call
  * changes nothing and records RA_ERR_PAGES; so does, for itself alone, an entry that repeats a
  * slot or would pass max_pages.  Two launches.
+ * _ex: granted [B] (device, or NULL; n_new itself, or apart from n_new and slots) receives n_new[b] of the entries that
+ * got their room and 0 of the others.  Passed on as the n_new of append and attend, it keeps a captured step from
+ * writing where nothing was reserved: append goes by lens, and its last n_new tokens would be the older ones.
  */
 RA_API int ring_attn_cache_reserve(const ra_cache* cache, const int* slots, const int* n_new, int B, void* workspace,
                                    size_t workspace_bytes, ra_stream stream);
+RA_API int ring_attn_cache_reserve_ex(const ra_cache* cache, const int* slots, const int* n_new, int B, int* granted,
+                                      void* workspace, size_t workspace_bytes, ra_stream stream);
 
 /*
  * ring_attn_cache_append -- writes the last n_new[b] tokens of every slots[b] (those that
- * ring_attn_cache_reserve made room for) into one layer's pages.
+ * ring_attn_cache_reserve made room for; where it did not, they are the tokens cached before, and are
+ * overwritten: see ring_attn_cache_reserve_ex) into one layer's pages.
  *   k, v      [B][heads][T][head_dim] bf16, strides {b, h, t} in elements (multiples of 8), 16-byte
  *             aligned; tokens t < n_new[b] <= T are read.  n_new NULL: T for every entry.
  * Per page and head: e = least exponent with amax <= 448 * 2^e over the finite new elements, within

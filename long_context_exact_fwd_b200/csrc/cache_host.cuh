@@ -293,12 +293,24 @@ size_t ring_attn_cache_pages_workspace_size(int B, int pages) {
 
 int ring_attn_cache_reserve(const ra_cache* cache, const int* slots, const int* n_new, int B, void* workspace,
                             size_t workspace_bytes, ra_stream stream) {
+  return ring_attn_cache_reserve_ex(cache, slots, n_new, B, nullptr, workspace, workspace_bytes, stream);
+}
+
+int ring_attn_cache_reserve_ex(const ra_cache* cache, const int* slots, const int* n_new, int B, int* granted,
+                               void* workspace, size_t workspace_bytes, ra_stream stream) {
   rc::Pool c;
   int st = cache_pool(cache, -1, &c);
   if (st != RA_OK) return st;
   if ((st = cache_batch(slots, B)) != RA_OK) return st;
   if (!n_new) return RA_ERR_ARG;
-  if (reinterpret_cast<uintptr_t>(n_new) % 4) return RA_ERR_ALIGN;
+  if (reinterpret_cast<uintptr_t>(n_new) % 4 || reinterpret_cast<uintptr_t>(granted) % 4) return RA_ERR_ALIGN;
+  if (granted) {   // written while slots and other counts may still be read
+    const auto over = [&](const int* x) {
+      const uintptr_t a = reinterpret_cast<uintptr_t>(x), g = reinterpret_cast<uintptr_t>(granted);
+      return a < g + 4ull * B && g < a + 4ull * B;
+    };
+    if (over(slots) || (granted != n_new && over(n_new))) return RA_ERR_ARG;
+  }
   if ((st = pages_check_ws(workspace, workspace_bytes, ring_attn_cache_pages_workspace_size(B, c.pages))) != RA_OK) return st;
   DevInfo* di = dev_info(&st);
   if (!di) return st;
@@ -306,7 +318,8 @@ int ring_attn_cache_reserve(const ra_cache* cache, const int* slots, const int* 
   rc::Plan* plan = static_cast<rc::Plan*>(workspace);
   int* pairs = reinterpret_cast<int*>(static_cast<char*>(workspace) + align256(sizeof(rc::Plan)));
   int* free_list = pairs + 2 * B;
-  st = launch_behind(rc::reserve_plan_kernel, dim3(1), rc::PLAN_THREADS, 0, s, c, slots, n_new, B, plan, pairs, free_list);
+  st = launch_behind(rc::reserve_plan_kernel, dim3(1), rc::PLAN_THREADS, 0, s, c, slots, n_new, B, granted, plan, pairs,
+                     free_list);
   if (st != RA_OK) return st;
   return launch_behind(rc::copy_pages_kernel, dim3(copy_grid(c, B, di->sm_count)), rc::COPY_THREADS, 0, s, c, plan, pairs,
                        pairs + 1, 2, nullptr);

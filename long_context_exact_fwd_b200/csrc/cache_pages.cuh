@@ -76,9 +76,11 @@ __device__ __forceinline__ int list_pages(const int* refs, int from, int to, boo
 }
 
 // Pages for positions len .. len + n_new - 1 of every entry; len += n_new.  All or nothing: with
-// too few free pages nothing changes.
+// too few free pages nothing changes.  granted (or null; may be n_new itself): n_new of the entries that were given
+// room, 0 of the others.
 __global__ void __launch_bounds__(PLAN_THREADS)
-    reserve_plan_kernel(Pool c, const int* slots, const int* n_new, int B, Plan* plan, int* pairs, int* free_list) {
+    reserve_plan_kernel(Pool c, const int* slots, const int* n_new, int B, int* granted, Plan* plan, int* pairs,
+                        int* free_list) {
   behind_last();
   __shared__ int s_slot[MAX_BATCH], s_last[MAX_BATCH], s_first[MAX_BATCH], s_have[MAX_BATCH], warp_sum[33];
   const int b = threadIdx.x;
@@ -133,6 +135,7 @@ __global__ void __launch_bounds__(PLAN_THREADS)
       record_pages();
       plan->pairs = 0;
     }
+    if (granted && b < B) granted[b] = 0;
     return;
   }
   __syncthreads();   // the list is complete, every count has been read
@@ -148,6 +151,7 @@ __global__ void __launch_bounds__(PLAN_THREADS)
     c.table[static_cast<long long>(s_slot[r]) * c.max_pages + s_have[r] + (i - s_first[r])] = pid;
   }
   if (active) c.lens[slot] = len + n;
+  if (granted && b < B) granted[b] = active ? n : 0;
   if (threadIdx.x == 0) plan->pairs = n_copies;
 }
 

@@ -76,6 +76,7 @@ _rope = _sig("ring_attn_rope", _i, _vp, _vp, _i, _llp, _vp, _vp, _i, _llp, _i, _
              _ll, _i, _i, _vp)
 _cache_pages_ws = _sig("ring_attn_cache_pages_workspace_size", _sz, _i, _i)
 _cache_reserve = _sig("ring_attn_cache_reserve", _i, _cp, _vp, _vp, _i, _vp, _sz, _vp)
+_cache_reserve_ex = _sig("ring_attn_cache_reserve_ex", _i, _cp, _vp, _vp, _i, _vp, _vp, _sz, _vp)
 _cache_append = _sig("ring_attn_cache_append", _i, _cp, _i, _vp, _vp, _i, _i, _vp, _llp, _vp, _llp, _vp)
 _cache_read = _sig("ring_attn_cache_read", _i, _cp, _i, _vp, _vp, _i, _i, _vp, _vp, _vp)
 _cache_read_ex = _sig("ring_attn_cache_read_ex", _i, _cp, _i, _vp, _vp, _i, _i, _vp, _vp, _i, _i, _vp)
@@ -582,13 +583,17 @@ def _workspace(workspace, need: int, like: torch.Tensor, dev: int, stream):
 
 
 def cache_reserve(cache: KVCache, slots: torch.Tensor, n_new: torch.Tensor, workspace: Optional[torch.Tensor] = None,
-                  stream=None) -> None:
+                  stream=None, granted: Optional[torch.Tensor] = None) -> None:
     """Room for n_new[b] more tokens of slots[b] (int32, on the device), once for all layers; lens grow
-    (ring_attn_cache_reserve).  Too few pages, or a slot out of range: device_status()."""
+    (ring_attn_cache_reserve_ex).  Too few pages, or a slot out of range: device_status(), and 0 in `granted` (int32
+    [B], may be n_new) where there was no room.  A step that goes on without asking, one captured in a graph above
+    all, passes `granted` as the n_new of the calls that follow: cache_append() would write over older tokens."""
     dev, B = cache._at(), slots.shape[0]
     s, n = _batch(slots, "slots", dev, B), _batch(n_new, "n_new", dev, B)
     ws, size = _workspace(workspace, cache_pages_workspace_bytes(B, cache._c.pages), cache.k, dev, stream)
-    _check(_cache_reserve(cache._ref, s, n, B, ws.data_ptr(), size, _raw_stream(stream, dev)), "ring_attn_cache_reserve")
+    g = None if granted is None else _batch(granted, "granted", dev, B)
+    _check(_cache_reserve_ex(cache._ref, s, n, B, g, ws.data_ptr(), size, _raw_stream(stream, dev)),
+           "ring_attn_cache_reserve_ex")
 
 
 def cache_append(cache: KVCache, layer: int, slots: torch.Tensor, n_new: Optional[torch.Tensor], k: torch.Tensor,

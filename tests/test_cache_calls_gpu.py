@@ -99,3 +99,66 @@ def test_a_ring_does_not_raise_for_a_cache_entry(ra):  # noqa: F811
         rd.ring_fwd(q, k, v, True)
     assert e.value.code == ra.RA_ERR_TIMEOUT
     assert ra.device_status() == ra.RA_ERR_PAGES and ra.device_status() == 0
+
+
+# ------------------------------------------------------------------------------------ a reserve that failed
+def test_a_step_without_room_keeps_what_is_cached(ra):  # noqa: F811
+    """Reserve, append, attend captured once: where reserve finds no room, append writes nothing over the
+    tokens that are there."""
+    two = Both(ra, pages=4, heads=1, page=16, Dh=64, slots=3, max_pages=2)
+    two.add([0, 1], [15, 30])
+    slots, n = _i32([0, 1, -1, 2]), _i32([1, 1, 1, 0])
+    granted = _i32([9, 9, 9, 9])
+    x = torch.zeros((4, 1, 1, 64), dtype=torch.bfloat16, device="cuda")
+    q = _randn((4, 2, 1, 64), 3).cuda()
+
+    def step():
+        ra.cache_reserve(two.gpu, slots, n, granted=granted)
+        ra.cache_append(two.gpu, 0, slots, granted, x, x)
+        return ra.cache_attend(two.gpu, 0, slots, granted, q)
+
+    books = [t.clone() for t in (two.gpu.table, two.gpu.lens, two.gpu.refs, two.gpu.k, two.gpu.v, two.gpu.k_scale, two.gpu.v_scale)]
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o, lse = step()
+    for t, b in zip((two.gpu.table, two.gpu.lens, two.gpu.refs, two.gpu.k, two.gpu.v, two.gpu.k_scale, two.gpu.v_scale), books):
+        t.copy_(b)
+    for i in range(6):
+        # slot 1 is full after two tokens (its entry alone is refused); slot 0 goes on to its second page
+        x.copy_(_randn(x.shape, 20 + i))
+        graph.replay()
+        room = two.cpu[0].lens[1] < 32
+        got = [1, 1 if room else 0, 0, 0]
+        assert ra.device_status() == (0 if room else ra.RA_ERR_PAGES)
+        assert granted.tolist() == got
+        two.cpu[0].reserve([0, 1], got[:2])
+        two.cpu[0].append([0, 1], got[:2], x[:2].float().cpu().numpy(), x[:2].float().cpu().numpy())
+        two.check()
+        # check_attend leaves rows that were not granted at 7
+        for b in (2, 3) if room else (1, 2, 3):
+            assert torch.all(o[b] == 0) and torch.all(torch.isneginf(lse[b]))
+            o[b], lse[b] = 7.0, 7.0
+        check_attend(two.cpu[0], [0, 1, -1, -1], got, q, o, lse)
+    # no page left for the batch: nobody is granted anything
+    x.copy_(_randn(x.shape, 40))
+    ra.cache_trim(two.gpu, _i32([1]), _i32([16]))
+    two.cpu[0].trim([1], [16])
+    two.add([2], [16])
+    ra.cache_reserve(two.gpu, _i32([0, 1]), _i32([1, 1]), granted=granted[:2])
+    assert ra.device_status() == ra.RA_ERR_PAGES and granted.tolist()[:2] == [0, 0]
+    ra.cache_append(two.gpu, 0, _i32([0, 1]), granted[:2], x[:2], x[:2])
+    two.check()
+
+
+def test_granted_is_checked(ra):  # noqa: F811
+    two = Both(ra, 8, 1, 16, 64, 2, 3)
+    for bad in (torch.zeros(2, dtype=torch.int64, device="cuda"), torch.zeros(2, dtype=torch.int32), _i32([0])):
+        with pytest.raises(ValueError):
+            ra.cache_reserve(two.gpu, _i32([0, 1]), _i32([1, 1]), granted=bad)
+    n = _i32([1, 1])
+    with pytest.raises(ra.RingAttnError):
+        ra.cache_reserve(two.gpu, n, _i32([1, 1]), granted=n)                  # over the slots
+    ra.cache_reserve(two.gpu, _i32([0, 1]), n, granted=n)                      # over the counts themselves
+    assert n.tolist() == [1, 1] and ra.device_status() == 0
