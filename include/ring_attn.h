@@ -345,8 +345,8 @@ RA_API int ring_attn_rope(const void* q, void* q_out, int Hq, const long long* q
  * three consistent.  They read slots, lengths and page numbers on the device: an entry with
  * slot -1 is padding (skipped, its output rows left as they were); one that is out of range is
  * skipped too and leaves RA_ERR_PAGES in the device status word (ring_attn_device_status).
- * At most 1024 entries a call.  Calls that change a cache must not overlap on the GPU with other
- * calls on the same cache.
+ * A table has fewer than 2^31 - 2048 entries (slots * max_pages).  At most 1024 entries a call.  Calls that
+ * change a cache must not overlap on the GPU with other calls on the same cache.
  */
 typedef struct ra_cache {
   void *k, *v;

@@ -23,6 +23,8 @@ int cache_pool(const ra_cache* c, int layer, rc::Pool* p) {
   if (c->head_dim != 64 && c->head_dim != 128) return RA_ERR_SHAPE;
   // positions fit in int (with a tile to spare), page numbers and per-layer head indexes too
   if (static_cast<long long>(c->max_pages) * c->page > INT_MAX - 1024) return RA_ERR_SHAPE;
+  // nor may a batch's pages, at most every entry of the table and a copy each, pass it: plans add them up
+  if (static_cast<long long>(c->slots) * c->max_pages > INT_MAX - 2 * rc::MAX_BATCH) return RA_ERR_SHAPE;
   if (c->pages > (1 << 28) || c->heads > 32767 || c->layers > (1 << 20)) return RA_ERR_SHAPE;
   if (static_cast<double>(c->layers) * c->pages * c->heads * c->page * c->head_dim > 9.0e18 / 4) return RA_ERR_SHAPE;
   if (!aligned16(c->k) || !aligned16(c->v)) return RA_ERR_ALIGN;

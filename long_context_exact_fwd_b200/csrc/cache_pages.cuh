@@ -21,7 +21,6 @@ constexpr int COPY_BYTES = 16384;    // bytes of one copy unit: 4 x 16 bytes a t
 // What a plan leaves in the workspace for the launch that follows.
 struct Plan {
   int pairs;       // page copies
-  int n_live;      // compact: pages in use
   int rows;        // fork: entries
   int items;       // fork: table entries to copy
 };
@@ -255,10 +254,7 @@ __global__ void __launch_bounds__(PLAN_THREADS)
     c.refs[to] = c.refs[from];
     c.refs[from] = 0;
   }
-  if (threadIdx.x == 0) {
-    plan->pairs = n;
-    plan->n_live = n_live;
-  }
+  if (threadIdx.x == 0) plan->pairs = n;
 }
 
 // Copies pages src -> dst of the plan's pairs in all layers, keys, values and scales, in units of

@@ -263,3 +263,15 @@ def test_the_bindings_refuse_cpu_tensors(ra):
         ra.rope(x, plan)
     with pytest.raises((ValueError, RuntimeError, AssertionError)):
         ra.kv_cache(1, 4, 2, 16, 64, 2, 2, device="cpu")
+
+
+def test_a_table_whose_pages_cannot_be_counted_is_refused(ra):
+    """A batch may ask for every entry of the table and a copy each; the plans add them up in 32 bits."""
+    most = 2 ** 31 - 1 - 2 * 1024
+    for slots, max_pages in ((17, (2 ** 31 - 1025) // 16), (2 ** 20, 2048), (most // 5 + 1, 5), (2 ** 31 - 1, 1)):
+        for name, call in _calls(ra, _cache_struct(ra, slots=slots, max_pages=max_pages, page=16)).items():
+            assert call() == ra.RA_ERR_SHAPE, (name, slots, max_pages)
+    if not torch.cuda.is_available():
+        for slots, max_pages in ((16, 2 ** 20), (most // 5, 5)):
+            for name, call in _calls(ra, _cache_struct(ra, slots=slots, max_pages=max_pages, page=16)).items():
+                assert call() in (ra.RA_ERR_CUDA, ra.RA_ERR_DEVICE), (name, slots, max_pages)
