@@ -503,10 +503,8 @@ def ring_bwd_zigzag_emulated(q_shards, k_shards, v_shards, o_shards, lse_shards,
 
 def _cuda_cache_attend(cache, layer, slots, n_new, q, causal):
     from . import ring_attn as ra
-    # rows of padding stay a part of weight 0
-    o = torch.zeros(q.shape, dtype=torch.float32, device=q.device)
-    lse = torch.full(q.shape[:3], float("-inf"), dtype=torch.float32, device=q.device)
-    return ra.cache_attend(cache, layer, slots, n_new, q, causal=causal, out_dtype=torch.float32, out=o, lse=lse)
+    # rows of padding are a part of weight 0: o = 0, lse = -inf
+    return ra.cache_attend(cache, layer, slots, n_new, q, causal=causal, out_dtype=torch.float32)
 
 
 def ring_cache_attend(cache, layer: int, slots: torch.Tensor, n_new: Optional[torch.Tensor], q: torch.Tensor,
@@ -516,7 +514,10 @@ def ring_cache_attend(cache, layer: int, slots: torch.Tensor, n_new: Optional[to
     slots[b], a part of sequence b's keys and values, and every rank has the same q [B, H, T, Dh].
     `newest` says whether this rank's part ends with the new tokens themselves (exactly one rank: there
     the queries are masked by position); the other ranks' parts lie before them and are seen whole, so
-    their n_new only says which rows exist.  Returns (o, lse) of the whole contexts, on every rank."""
+    their n_new only says which rows exist.  Returns (o, lse) of the whole contexts, on every rank.
+    Does not wait for the GPU, so that a step can be captured in a graph: errors are left for
+    ring_attn.device_status(), as by the cache's own calls (a rank that raised here would leave the others
+    waiting in their next collective)."""
     o, lse = (attend or _cuda_cache_attend)(cache, layer, slots, n_new, q, newest)
     world = dist.get_world_size(group) if dist.is_initialized() else 1
     if world > 1:
@@ -526,7 +527,4 @@ def ring_cache_attend(cache, layer: int, slots: torch.Tensor, n_new: Optional[to
         o_parts, lse_parts = torch.stack(os), torch.stack(lses)
     else:
         o_parts, lse_parts = o.unsqueeze(0), lse.unsqueeze(0)
-    out = (merge or _cuda_merge)(o_parts, lse_parts)
-    if attend is None and merge is None:
-        _raise_on_device_status()
-    return out
+    return (merge or _cuda_merge)(o_parts, lse_parts)

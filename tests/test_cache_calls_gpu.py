@@ -162,3 +162,23 @@ def test_granted_is_checked(ra):  # noqa: F811
         ra.cache_reserve(two.gpu, n, _i32([1, 1]), granted=n)                  # over the slots
     ra.cache_reserve(two.gpu, _i32([0, 1]), n, granted=n)                      # over the counts themselves
     assert n.tolist() == [1, 1] and ra.device_status() == 0
+
+
+# ------------------------------------------------------------------------------------ contexts cut across ranks
+def test_cached_parts_in_a_graph(ra):  # noqa: F811
+    from long_context_exact_fwd_b200 import ring_dist as rd
+    two = Both(ra, 20, 2, 16, 64, 3, 8)
+    two.add([0, 2], [100, 37])
+    q = _randn((3, 4, 1, 64), 3).cuda()
+    slots, n = _i32([2, -1, 0]), _i32([1, 1, 1])
+    want = rd.ring_cache_attend(two.gpu, 0, slots, n, q, True)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = rd.ring_cache_attend(two.gpu, 0, slots, n, q, True)
+    graph.replay()
+    assert ra.device_status() == 0
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    # errors are the cache's: left for device_status(), as by every other call on it
+    rd.ring_cache_attend(two.gpu, 0, _i32([2, 7, 0]), n, q, True)
+    assert ra.device_status() == ra.RA_ERR_PAGES
