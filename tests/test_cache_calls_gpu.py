@@ -1,4 +1,5 @@
-"""Calls on the cache that its documentation allows."""
+"""Calls on the cache that its documentation allows: rows of padding in fresh outputs, errors of several kinds, a
+reserve that failed inside a captured step, and batches of hundreds of sequences."""
 import numpy as np
 import pytest
 import torch
@@ -182,3 +183,43 @@ def test_cached_parts_in_a_graph(ra):  # noqa: F811
     # errors are the cache's: left for device_status(), as by every other call on it
     rd.ring_cache_attend(two.gpu, 0, _i32([2, 7, 0]), n, q, True)
     assert ra.device_status() == ra.RA_ERR_PAGES
+
+
+# ------------------------------------------------------------------------------------ many sequences
+@pytest.mark.parametrize("B,g,T", [(300, 4, 5), (1024, 2, 1), (257, 4, 20), (1024, 64, 1)])
+def test_attention_of_many_sequences(ra, B, g, T):  # noqa: F811
+    """More entries than a block has threads, ragged, some of them padding."""
+    rng = np.random.default_rng(B)
+    two = Both(ra, 4 * B + 4, 1, 16, 64, B, 5)
+    lengths = [int(x) for x in rng.integers(1, 64, B)]
+    perm = [int(s) for s in rng.permutation(B)]
+    two.add(perm, lengths)
+    slots = [-1 if i % 11 == 5 else s for i, s in enumerate(perm)]
+    n_new = [int(min(x, rng.integers(0, T + 1))) for x in lengths]
+    n_new[-1], slots[-1] = 1, perm[-1]
+    two.attend(slots, n_new, g, T)
+    two.attend(slots, n_new, g, T, causal=False, out_dtype=torch.float32)
+
+
+def test_pages_of_many_sequences(ra):  # noqa: F811
+    """Plans over hundreds of entries: shared, partly filled pages whose holders lie in different warps."""
+    rng = np.random.default_rng(5)
+    N = 600
+    two = Both(ra, pages=2500, heads=1, page=16, Dh=64, slots=N, max_pages=6)
+    first = list(range(0, 40))
+    two.add(first, [int(x) for x in rng.integers(1, 60, 40)])
+    dst = [int(s) for s in 40 + rng.permutation(N - 40)[:500]]
+    two.fork([int(rng.integers(0, 40)) for _ in dst], dst)
+    two.check()
+    for step in range(3):
+        slots = [int(s) for s in rng.permutation(first + dst)[:450]]
+        slots[100], slots[333] = -1, -1
+        n = [int(x) for x in rng.integers(0, 9, 450)]
+        two.add(slots, n)
+        two.check()
+        two.trim([int(s) for s in rng.permutation(first + dst)[:200]], [int(x) for x in rng.integers(0, 50, 200)])
+        two.check()
+        two.compact()
+        two.check()
+    live = [int(s) for s in np.flatnonzero(two.cpu[0].lens)][:300]
+    two.attend(live, [1] * len(live), 2, 1)
