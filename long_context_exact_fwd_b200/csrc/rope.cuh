@@ -6,7 +6,7 @@
 //
 // Angles.  The plan holds theta_i / 2 pi as a 64-bit fixed-point fraction of a turn, so
 // position * step mod 2^64 is the phase with whole turns dropped, exact in integer arithmetic:
-// the error left is position * 2^-65 turns, at any position.  The phase is brought to the nearest
+// with a step to the nearest unit the error left is position * 2^-65 turns, at any position.  The phase is brought to the nearest
 // quarter turn before it becomes a float (|r| <= 1/8 turn keeps 24 good bits).  No table is kept or
 // read.
 //

@@ -387,6 +387,29 @@ def rope_inv_freq(rot: int, base: float = 10000.0, scaling: str = "none", factor
     raise ValueError(f"unknown scaling {scaling!r}")
 
 
+@functools.lru_cache(maxsize=64)
+def _pi(bits: int) -> int:
+    """pi * 2^bits to a unit or two, by Machin's formula: pi = 16 atan(1/5) - 4 atan(1/239)."""
+    def atan(x):   # of 1 / x, 32 bits to spare
+        power = (1 << (bits + 32)) // x
+        total, n = power, 1
+        while power:
+            power //= -x * x
+            n += 2
+            total += power // n
+        return total
+    return (16 * atan(5) - 4 * atan(239)) >> 32
+
+
+def _step(theta: float) -> int:
+    """theta / 2 pi in units of 2^-64 turn, whole turns dropped, to the nearest unit.  In integers: a quotient of
+    doubles would be off by up to 2^-53 of itself, hundreds of units."""
+    bits = 128 + max(0, math.frexp(theta)[1])
+    n, d = theta.as_integer_ratio()
+    den = d * _pi(bits)
+    return ((n << (64 + bits)) + den) // (2 * den) % (1 << 64)
+
+
 def rope_plan(inv_freq: torch.Tensor, layout: str = "half", amplitude: float = 1.0, device=None) -> RopePlan:
     """The plan for rope(): inv_freq [rot / 2] (radians per position, finite), layout "half" (pairs
     i, i + rot / 2) or "interleaved" (pairs 2i, 2i + 1)."""
@@ -400,7 +423,7 @@ def rope_plan(inv_freq: torch.Tensor, layout: str = "half", amplitude: float = 1
     for w in inv_freq.detach().double().cpu().tolist():
         if not math.isfinite(w):
             raise ValueError("inv_freq must be finite")
-        u = round(math.ldexp(math.fmod(w / (2 * math.pi), 1.0), 64)) % (1 << 64)
+        u = _step(w)
         steps.append(u - (1 << 64) if u >= 1 << 63 else u)
     device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
     return RopePlan(torch.tensor(steps, dtype=torch.int64).to(device), 2 * len(steps), layout == "interleaved",

@@ -275,3 +275,28 @@ def test_a_table_whose_pages_cannot_be_counted_is_refused(ra):
         for slots, max_pages in ((16, 2 ** 20), (most // 5, 5)):
             for name, call in _calls(ra, _cache_struct(ra, slots=slots, max_pages=max_pages, page=16)).items():
                 assert call() in (ra.RA_ERR_CUDA, ra.RA_ERR_DEVICE), (name, slots, max_pages)
+
+
+# 100 digits behind the point
+PI = "3.1415926535897932384626433832795028841971693993751058209749445923078164062862089986280348253421170679"
+
+
+def exact_turns(theta, units=1):
+    """theta / 2 pi * units of a double theta without whole turns, in (-units / 2, units / 2], to some 70 digits."""
+    from decimal import Decimal, localcontext
+    with localcontext() as c:
+        c.prec = 110
+        turns = Decimal(theta) / (2 * Decimal(PI)) * units
+        return turns - units * (turns / units).to_integral_value()
+
+
+def test_rope_steps_are_the_nearest(ra):
+    thetas = [1.0, -1.0, 0.5, 2.5, 6.283185307179586, 1e-300, 1e-9, 1e9, -3e12, 1e20]
+    for kw in (dict(), dict(base=500000.0), dict(scaling="linear", factor=3.0), dict(scaling="ramp", factor=8.0, original_length=8192)):
+        thetas += ra.rope_inv_freq(128, **kw)[0].tolist()
+    steps = ra.rope_plan(torch.tensor(thetas, dtype=torch.float64), device="cpu").steps.tolist()
+    for theta, s in zip(thetas, steps):
+        want = exact_turns(theta, 2 ** 64)
+        whole = int(want)
+        off = (whole - s + 2 ** 63) % 2 ** 64 - 2 ** 63 + float(want - whole)
+        assert abs(off) <= 0.5000001, (theta, off)

@@ -236,3 +236,26 @@ def test_rows_that_start_at_smaller_vectors(ra, shift, rot, inter, dtype):
     _check(y, x, p2, w.numpy(), inter, 1.0)
     ra.rope(x, ra.rope_plan(w, "interleaved" if inter else "half"), offset=50, out=x)
     assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("start", [1_000_003, 2 ** 31 + 5, 2 ** 40 + 1, -(2 ** 43) - 7])
+@pytest.mark.parametrize("kw", [dict(), dict(scaling="ramp", factor=8.0, original_length=8192)])
+def test_far_positions_of_a_plan(ra, start, kw):
+    """The plan as it is made: its steps are the nearest, so the phase is off by position 2^-65 turns."""
+    from decimal import localcontext
+    from test_oracle_cache import exact_turns
+    w, amp = ra.rope_inv_freq(64, **kw)
+    q = _x((1, 2, 9, 64), torch.float32, 4)
+    y = ra.rope(q, ra.rope_plan(w, amplitude=amp), offset=start).double().cpu().numpy()
+    # angles in turns, whole ones dropped
+    with localcontext() as ctx:
+        ctx.prec = 110
+        per = [exact_turns(f) for f in w.tolist()]
+        turns = np.array([[float(t * (start + i) - (t * (start + i)).to_integral_value()) for t in per] for i in range(9)])
+    c, s = amp * np.cos(2 * np.pi * turns), amp * np.sin(2 * np.pi * turns)
+    x = q.double().cpu().numpy()
+    x1, x2 = x[..., :32], x[..., 32:]
+    ref = np.concatenate((x1 * c - x2 * s, x1 * s + x2 * c), -1)
+    size = np.tile(np.abs(x1) + np.abs(x2), 2)
+    tol = 2.0 ** -24 * np.abs(ref) + (2.0 ** -20 + 2 * np.pi * abs(start) * 2.0 ** -65) * amp * size
+    assert np.all(np.abs(y - ref) <= tol), float((np.abs(y - ref) / tol).max())
