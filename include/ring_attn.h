@@ -316,7 +316,8 @@ RA_API int ring_attn_merge_ex(const float* o_parts, const float* lse_parts, int 
  *              dimension; q_strides = {in b, h, s, out b, h, s} in elements, host memory.  In place
  *              (same address and strides) is allowed, any other overlap of q and q_out is refused.
  *   k, k_out   the same with Hk heads, or NULL, NULL with Hk = 0.  q_out and k_out must not share
- *              elements, nor lie over the other's input (interleaved rows of one buffer are fine).
+ *              elements, nor lie over the other's input (rows of one buffer side by side are fine); refused where the
+ *              first or last element of one lies in the other.
  *   steps      [rot / 2] device, theta_i / (2 pi) in units of 2^-64 turn (mod 2^64): position * step
  *              mod 2^64 is the phase, exact at any position.
  *   rot        rotated columns, even, 2 .. Dh; Dh even, at most 1024.
@@ -398,7 +399,7 @@ RA_API int ring_attn_cache_append(const ra_cache* cache, int layer, const int* s
  * ring_attn_cache_read -- one layer's keys and values as bf16 (exact): positions start[b] ..
  * start[b] + length - 1 of slots[b] (start NULL: 0) into k, v [B][heads][length][head_dim], zero
  * at positions that the sequence does not hold (a length out of range holds none) and of tokens whose page
- * number is out of range.  One launch.
+ * number is out of range.  k and v must not overlap (RA_ERR_ARG).  One launch.
  * _ex: fill_k, fill_v != 0 zero the rows of entries that are padding or left out in k, v (for outputs that hold
  * nothing yet); 0 leaves them as they were, as the plain call does.
  */
@@ -420,7 +421,7 @@ RA_API int ring_attn_cache_read_ex(const ra_cache* cache, int layer, const int* 
  *             number is out of range are not seen.
  *   workspace ring_attn_cache_attend_workspace_size bytes, 256-byte aligned, of this call alone while
  *             it runs; contents on entry do not matter.
- * o must not overlap q (RA_ERR_ARG).  exp(s - lse) times the value scale of the token's page is rounded to fp16
+ * o, lse and q must not overlap (RA_ERR_ARG).  exp(s - lse) times the value scale of the token's page is rounded to fp16
  * before it multiplies the code of v: 11 bits where it is above 2^-21 of the largest that the query itself has, an
  * absolute 2^-32 of that below (tokens that it does not see have no part in this); sums are float32.  Calls with 64 rows and more per head (T * Hq / heads) run on tcgen05.  Two launches; a
  * bounded wait that gave up leaves RA_ERR_TIMEOUT in the device status word.

@@ -57,6 +57,12 @@ int cache_rows(const void* x, const long long* st, int B, int H, int T) {
   return aligned16(x) ? RA_OK : RA_ERR_ALIGN;
 }
 
+// Whether `a_bytes` from a and `b_bytes` from b have a byte in common.
+bool overlap(const void* a, unsigned long long a_bytes, const void* b, unsigned long long b_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + b_bytes && y < x + a_bytes;
+}
+
 size_t pages_workspace(long long words) { return align256(sizeof(rc::Plan)) + align256(static_cast<size_t>(words) * 4); }
 
 int pages_check_ws(const void* workspace, size_t have, size_t need) {
@@ -205,6 +211,8 @@ int ring_attn_cache_read_ex(const ra_cache* cache, int layer, const int* slots, 
   if (st != RA_OK) return st;
   if ((st = cache_batch(slots, B)) != RA_OK) return st;
   if (!aligned16(k) || !aligned16(v) || reinterpret_cast<uintptr_t>(start) % 4) return RA_ERR_ALIGN;
+  const unsigned long long bytes = 2ull * B * p.c.heads * length * p.c.Dh;
+  if (overlap(k, bytes, v, bytes)) return RA_ERR_ARG;
   DevInfo* di = dev_info(&st);
   if (!di) return st;
   p.slots = slots;
@@ -246,12 +254,12 @@ int ring_attn_cache_attend_ex(const ra_cache* cache, int layer, const int* slots
   if (Hq % p.c.heads) return RA_ERR_SHAPE;
   if ((st = cache_rows(q, q_strides, B, Hq, T)) != RA_OK) return st;
   if (!aligned16(o) || reinterpret_cast<uintptr_t>(lse) % 4 || reinterpret_cast<uintptr_t>(n_new) % 4) return RA_ERR_ALIGN;
-  // rows are written while others' queries are still read: the output may not lie over the queries
+  // rows are written while others' queries are still read: the outputs may not lie over the queries, nor each other
   const auto reach = [&](int i, int n) { return n > 1 ? q_strides[i] * (n - 1) : 0; };
-  const uintptr_t q0 = reinterpret_cast<uintptr_t>(q), o0 = reinterpret_cast<uintptr_t>(o);
-  const uintptr_t q1 = q0 + 2 * static_cast<uintptr_t>(reach(0, B) + reach(1, Hq) + reach(2, T) + p.c.Dh);
-  const uintptr_t o1 = o0 + static_cast<uintptr_t>(B) * Hq * T * p.c.Dh * (o_dtype == RA_F32 ? 4 : 2);
-  if (q0 < o1 && o0 < q1) return RA_ERR_ARG;
+  const unsigned long long q_bytes = 2ull * (reach(0, B) + reach(1, Hq) + reach(2, T) + p.c.Dh);
+  const unsigned long long lse_bytes = 4ull * B * Hq * T, o_bytes = lse_bytes / 4 * p.c.Dh * (o_dtype == RA_F32 ? 4 : 2);
+  if (overlap(q, q_bytes, o, o_bytes) || overlap(q, q_bytes, lse, lse_bytes) || overlap(o, o_bytes, lse, lse_bytes))
+    return RA_ERR_ARG;
   p.g = Hq / p.c.heads;
   const long long rows = static_cast<long long>(T) * p.g;
   if (rows > INT_MAX / 2) return RA_ERR_SHAPE;
@@ -306,13 +314,10 @@ int ring_attn_cache_reserve_ex(const ra_cache* cache, const int* slots, const in
   if ((st = cache_batch(slots, B)) != RA_OK) return st;
   if (!n_new) return RA_ERR_ARG;
   if (reinterpret_cast<uintptr_t>(n_new) % 4 || reinterpret_cast<uintptr_t>(granted) % 4) return RA_ERR_ALIGN;
-  if (granted) {   // written while slots and other counts may still be read
-    const auto over = [&](const int* x) {
-      const uintptr_t a = reinterpret_cast<uintptr_t>(x), g = reinterpret_cast<uintptr_t>(granted);
-      return a < g + 4ull * B && g < a + 4ull * B;
-    };
-    if (over(slots) || (granted != n_new && over(n_new))) return RA_ERR_ARG;
-  }
+  // written while slots and other counts may still be read
+  if (granted && (overlap(granted, 4ull * B, slots, 4ull * B) ||
+                  (granted != n_new && overlap(granted, 4ull * B, n_new, 4ull * B))))
+    return RA_ERR_ARG;
   if ((st = pages_check_ws(workspace, workspace_bytes, ring_attn_cache_pages_workspace_size(B, c.pages))) != RA_OK) return st;
   DevInfo* di = dev_info(&st);
   if (!di) return st;

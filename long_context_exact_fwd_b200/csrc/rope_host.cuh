@@ -42,6 +42,39 @@ int rope_tensor(ra::rope::Tensor* t, const void* x, void* y, int H, const long l
   return RA_OK;
 }
 
+// Whether a [B][H][S][Dh] view at `x` (element size `size`, strides st[3]) has an element at address `a`: going down
+// the strides, each index as far as it goes (exact where each dimension steps over the smaller ones, as outputs do).
+bool rope_has(const void* x, const long long* st, int B, int H, int S, int Dh, int size, uintptr_t a) {
+  const uintptr_t x0 = reinterpret_cast<uintptr_t>(x);
+  if (a < x0) return false;
+  long long off = static_cast<long long>((a - x0) / size);
+  const int n[3] = {B, H, S};
+  bool done[3] = {false, false, false};
+  for (int k = 0; k < 3; ++k) {
+    int m = -1;
+    for (int i = 0; i < 3; ++i)
+      if (!done[i] && (m < 0 || st[i] > st[m])) m = i;
+    done[m] = true;
+    if (st[m] > 0) off -= st[m] * (off / st[m] < n[m] - 1 ? off / st[m] : n[m] - 1);
+  }
+  return off < Dh;
+}
+
+// Whether one of two views has the other's first or last element: rows of one buffer side by side do not.
+bool rope_meet(const void* x, const long long* xs, int xh, const void* y, const long long* ys, int yh, int B, int S, int Dh,
+               int size) {
+  const auto ends = [&](const void* p, const long long* st, int h, uintptr_t* e) {
+    e[0] = reinterpret_cast<uintptr_t>(p);
+    e[1] = e[0] + (rope_extent(st[0], st[1], st[2], B, h, S, Dh) - 1) * size;
+  };
+  uintptr_t ex[2], ey[2];
+  ends(x, xs, xh, ex);
+  ends(y, ys, yh, ey);
+  for (int i = 0; i < 2; ++i)
+    if (rope_has(x, xs, B, xh, S, Dh, size, ey[i]) || rope_has(y, ys, B, yh, S, Dh, size, ex[i])) return true;
+  return false;
+}
+
 // One thread a unit of a token, p.units of them a row.
 int rope_launch(void (*kernel)(ra::rope::Params), ra::rope::Params& p, int sm_count, cudaStream_t stream) {
   using namespace ra::rope;
@@ -135,7 +168,12 @@ int ring_attn_rope(const void* q, void* q_out, int Hq, const long long* q_stride
   if (st != RA_OK) return st;
   if (k || k_out || Hk) {
     if ((st = rope_tensor(&p.t[1], k, k_out, Hk, k_strides, B, S, Dh, size)) != RA_OK) return st;
-    if (q_out == k_out) return RA_ERR_ARG;
+    // written by one thread, read or written by another
+    const ra::rope::Tensor &a = p.t[0], &b = p.t[1];
+    const long long ai[3] = {a.xb, a.xh, a.xs}, ao[3] = {a.yb, a.yh, a.ys}, bi[3] = {b.xb, b.xh, b.xs}, bo[3] = {b.yb, b.yh, b.ys};
+    if (rope_meet(a.y, ao, Hq, b.y, bo, Hk, B, S, Dh, size) || rope_meet(a.y, ao, Hq, b.x, bi, Hk, B, S, Dh, size) ||
+        rope_meet(a.x, ai, Hq, b.y, bo, Hk, B, S, Dh, size))
+      return RA_ERR_ARG;
   }
   if (static_cast<long long>(Hq) + Hk > 65535) return RA_ERR_SHAPE;
   DevInfo* di = dev_info(&st);

@@ -277,6 +277,46 @@ def test_a_table_whose_pages_cannot_be_counted_is_refused(ra):
                 assert call() in (ra.RA_ERR_CUDA, ra.RA_ERR_DEVICE), (name, slots, max_pages)
 
 
+def test_outputs_over_other_tensors_are_refused(ra):
+    f = ra.raw.ring_attn_rope
+    B, S, Dh, Hq, Hk = 2, 3, 128, 4, 2
+
+    def call(q, q_out, k, k_out, st, kst=None, st_out=None, kst_out=None):
+        kst = kst or st
+        return f(P(q), P(q_out), Hq, (LL * 6)(*st, *(st_out or st)), P(k), P(k_out), Hk, (LL * 6)(*kst, *(kst_out or kst)), B, S, Dh,
+                 P(256), 128, 0, 1.0, None, 0, 0, 0, 0, 0, None)
+
+    dense, kdense = (Hq * S * Dh, S * Dh, Dh), (Hk * S * Dh, S * Dh, Dh)
+    row, fine = 2 * Dh, (ra.RA_OK, ra.RA_ERR_CUDA, ra.RA_ERR_DEVICE)     # bytes of a head's row
+    q, k, qo, ko = 1 << 20, 1 << 22, 1 << 24, 1 << 26
+    bad = [(q, k, k, ko), (q, qo, k, q), (q, q, k, q), (q, qo, k, qo),                 # one tensor for two
+           (q, qo, k, qo + row), (q, qo, k, qo - row), (q, k + row, k, ko), (q, k - row, k, ko), (q, qo, k, q + row),
+           (q, qo, k, qo + B * Hq * S * row - row), (q, q, k, q - B * Hk * S * row + row)]
+    for args in bad:
+        assert call(*args, dense, kdense) == ra.RA_ERR_ARG, args
+    fused = (S * (Hq + 2 * Hk) * Dh, Dh, (Hq + 2 * Hk) * Dh)                           # heads of a projection's rows
+    assert call(q, q, q + (Hq - 1) * row, q + (Hq - 1) * row, fused) == ra.RA_ERR_ARG
+    heads = ((Hq + 2 * Hk) * S * Dh, S * Dh, Dh)                                       # heads one after the other
+    assert call(q, q, q + (Hq - 1) * S * row, q + (Hq - 1) * S * row, heads) == ra.RA_ERR_ARG
+    if not torch.cuda.is_available():
+        for args in ((q, qo, k, ko), (q, q, k, k), (q, qo, q, ko), (q, qo, k, qo + B * Hq * S * row), (q, qo, k, qo - B * Hk * S * row)):
+            assert call(*args, dense, kdense) in fine, args
+        assert call(q, q, q + Hq * row, q + Hq * row, fused) in fine
+        assert call(q, q, q + Hq * S * row, q + Hq * S * row, heads) in fine
+        assert call(q, qo, q + Hq * row, ko, fused, None, dense, kdense) in fine
+
+    c = _cache_struct(ra)
+    n = 3 * 8 * 5                                                                      # rows of _calls' attend
+    for kw in (dict(lse=1 << 24), dict(lse=(1 << 24) + n * 256 - 4), dict(lse=(1 << 24) - 4 * n + 4), dict(lse=1 << 20),
+               dict(lse=(1 << 20) + 512)):
+        assert _calls(ra, c, **kw)["attend"]() == ra.RA_ERR_ARG, kw
+    for x2 in ((1 << 20) + 256, (1 << 20) - 256, (1 << 20) + 3 * 4 * 5 * 256 - 16):
+        assert _calls(ra, c, x2=x2)["read"]() == ra.RA_ERR_ARG
+    if not torch.cuda.is_available():
+        assert _calls(ra, c, lse=(1 << 24) + n * 256)["attend"]() in fine
+        assert _calls(ra, c, x2=(1 << 20) + 3 * 4 * 5 * 256)["read"]() in fine
+
+
 # 100 digits behind the point
 PI = "3.1415926535897932384626433832795028841971693993751058209749445923078164062862089986280348253421170679"
 
