@@ -23,7 +23,9 @@ namespace ra {
 namespace rope {
 
 constexpr int THREADS = 256;
-constexpr int HEADS_AT_ONCE = 4;   // their loads in flight together
+// Heads that rope_rows_kernel loads before it stores the first, and by which rope_kernel's loop is unrolled (its
+// stores may be to the next heads' inputs, for all that the compiler knows, so its loads stay behind them).
+constexpr int HEADS_AT_ONCE = 4;
 
 struct Tensor {               // one of Q, K: strides in elements, last dimension contiguous
   const void* x;

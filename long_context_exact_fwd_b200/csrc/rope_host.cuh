@@ -98,10 +98,14 @@ int rope_units(ra::rope::Params& p, int sm_count, bool interleaved, cudaStream_t
   using namespace ra::rope;
   p.rot_units = interleaved ? p.rot / N : p.rot / 2 / N;
   p.units = p.rot_units + (p.Dh - p.rot) / N;
-  if constexpr (N == 2) {
-    if (interleaved) return rope_launch(rope_kernel<T, N, true, VECTOR>, p, sm_count, stream);
+  if constexpr (N == 2 && !VECTOR) {   // interleaved pairs alone come here
+    return rope_launch(rope_kernel<T, N, true, VECTOR>, p, sm_count, stream);
+  } else {
+    if constexpr (N == 2) {
+      if (interleaved) return rope_launch(rope_kernel<T, N, true, VECTOR>, p, sm_count, stream);
+    }
+    return rope_launch(rope_kernel<T, N, false, VECTOR>, p, sm_count, stream);
   }
-  return rope_launch(rope_kernel<T, N, false, VECTOR>, p, sm_count, stream);
 }
 
 template <typename T, int N, bool INTERLEAVED>
