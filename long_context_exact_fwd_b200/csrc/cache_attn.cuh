@@ -186,10 +186,10 @@ __device__ __forceinline__ void join_parts(const float2 (&ml)[N], const float4 (
   }
 }
 
-// Rows t >= n[b] (shared memory; 0 for an entry that is left out), 32 tokens of a query head at a time over the grid.
+// Rows t >= n[b] (shared memory; 0 for an entry that is left out), 128 tokens of a query head at a time over the grid.
 template <int HD>
 __device__ __forceinline__ void fill_padding(const AttendParams& p, const int* n) {
-  constexpr int AT_ONCE = 32;
+  constexpr int AT_ONCE = 128;
   const int heads = p.c.heads * p.g, per_head = (p.T + AT_ONCE - 1) / AT_ONCE;
   const long long units = static_cast<long long>(p.B) * heads * per_head;
   for (long long u = blockIdx.x; u < units; u += gridDim.x) {
