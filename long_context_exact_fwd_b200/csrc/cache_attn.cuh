@@ -26,8 +26,9 @@
 // known on the device), so stretches end inside sequences: such parts go to the workspace and a
 // second, small launch joins them.  Each warp streams its own tiles with cp.async through a private
 // ring in shared memory, no block barrier inside a stretch (TMA boxes in its place: 7 % slower).
-// Measured on B200, 8 heads of 128, 4 query heads each: one context of 512K tokens 168 us, 98 % of a copy's
-// rate; 128K 50 us (83 %, some 9 us are start, join and launches); 32 of 16 to 16384 tokens 91 us (91 %).
+// Measured on B200, 8 heads of 128, 4 query heads each: one context of 512K tokens 170 us, 97 % of a copy's
+// rate; 128K 50 us (81 %, some 9 us are start, join and launches); 32 of 16 to 16384 tokens 93 us (89 %).
+// The row's own references cost 1 to 2 % at 8 rows, 3 to 10 % at 24 (the unit of a warp's rows: 92 us for the 32).
 #pragma once
 #include "cache.cuh"
 

@@ -17,8 +17,8 @@
 // Work is cut as in attend_kernel: one line of 128-key tiles over all items, equal stretches, parts
 // joined by chunk_join_kernel.
 // Bound: the products, and shared memory, which both operands of S, the tiles of V and the conversion go
-// through (about 320 KB a key tile; a tile takes some 4200 cycles, 2048 of them its products).  Measured on
-// B200, 16 query heads on 4 of 128, 2048 new tokens: at 16K tokens 285 us, 904 TFLOP/s; at 32K 538 us, 990.
+// through (about 320 KB a key tile; a tile takes some 4300 cycles, 2048 of them its products).  Measured on
+// B200, 16 query heads on 4 of 128, 2048 new tokens: at 16K tokens 292 us, 882 TFLOP/s; at 32K 562 us, 948.
 #pragma once
 #include "cache_attn.cuh"
 #include "cache_io.cuh"

@@ -78,9 +78,9 @@ int copy_grid(const rc::Pool& c, long long pairs, int sm_count) {
 
 // Which kernel a call's rows per kv head (T * g) take: 0 is chunk_kernel; otherwise attend_kernel with
 // blocks of 8 * nt rows, as few blocks as 24 rows allow and the narrowest that do.  Measured, attend_kernel
-// and chunk_kernel, 4 query heads on each of 4 or 8 of 128: 16 contexts up to 4K, 48 rows 63 and 66 us, 64 rows 87
-// and 66, 128 rows 151 and 73; one context of 32K, 48 rows 31 and 38, 64 rows 38 and 38, 128 rows 59 and 40; one of
-// 4K, where neither is busy, 64 rows 20 and 26 (the host does not know the lengths).
+// and chunk_kernel, 4 query heads on each of 8 of 128: 16 contexts up to 4K, 48 rows 66 and 68 us, 64 rows 90
+// and 68, 128 rows 153 and 74; one context of 32K, 48 rows 46 and 55, 64 rows 60 and 55, 128 rows 101 and 57; one of
+// 4K, where neither is busy, 64 rows 23 and 27 (the host does not know the lengths).
 constexpr int CHUNK_ROWS = 64;
 // Calls of so few segments join them with a block per row and 16 warps (4 warps a row otherwise).  Measured, 16
 // warps and 4: one segment of 128K tokens (444 parts) 17.7 and 27.4 us, eight of them 49.9 and 51.5, eight of 8K
